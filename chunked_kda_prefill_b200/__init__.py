@@ -9,3 +9,6 @@ from .api import (KdaPlan, LAYOUTS, decode, device_status, flash_kda, flash_kda_
                   forward_kernel_names, forward_summary, kernels_per_forward, make_plan,
                   noalloc_status, plan, state_chain)
 from .context_parallel import flash_kda_context_parallel  # noqa: F401
+from .qk import qk_norm_rope, qk_norm_rope_backward  # noqa: F401
+from .recurrence import (KdaRecurrencePlan, gated_recurrence, gated_recurrence_backward,  # noqa: F401
+                         gated_recurrence_step, recurrence_plan)

@@ -1,0 +1,78 @@
+"""What the operators around the prefill share in the binding: element types, strided tensor
+arguments, the launch stream and the device of a call."""
+from __future__ import annotations
+
+import contextlib
+
+import torch
+
+from ._lib import KdaError, KdaView
+
+# kda_dtype_t
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def dtype_code(t: torch.Tensor, name: str) -> int:
+    code = DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bf16, fp16 or fp32, got {t.dtype}")
+    return code
+
+
+def expect(t, name: str, dtype, device, shape) -> None:
+    """A tensor of exactly this type, device and shape; its strides are the caller's business."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.shape != shape:
+        raise KdaError(3, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def expect_dense(t, name: str, dtype, device, shape) -> None:
+    expect(t, name, dtype, device, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def view(t: torch.Tensor, name: str, layout: str, channels: bool = True) -> KdaView:
+    """kda_view_t of a tensor in a layout (the library checks alignment and ranges)."""
+    st = t.stride()
+    if channels and st[-1] != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    if layout == "BNSD":
+        return KdaView(t.data_ptr(), st[0], st[1], st[2])
+    if layout == "BSND":
+        return KdaView(t.data_ptr(), st[0], st[2], st[1])
+    return KdaView(t.data_ptr(), 0, st[1], st[0])
+
+
+def viewable(t: torch.Tensor) -> bool:
+    """Whether view() and the library's alignment rule take a tensor with channels as it lies."""
+    size = t.element_size()
+    return (t.stride(-1) == 1 and t.data_ptr() % 16 == 0
+            and all(n == 1 or s * size % 16 == 0 for n, s in zip(t.shape[:-1], t.stride()[:-1])))
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        yield
+
+
+_here = contextlib.nullcontext()
+
+
+def launch_on(device: torch.device, stream):
+    """(context, cuda stream handle): inside the context the call's device is the current one, and
+    what is allocated belongs to the stream that the kernels run on."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return _here, torch.cuda.current_stream(device).cuda_stream
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if s.device != device:
+        raise ValueError(f"stream is on {s.device}, the tensors on {device}")
+    return _on(device, s), s.cuda_stream
+
+
+def needs_grad(*tensors) -> bool:
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)

@@ -24,8 +24,9 @@ Range range_of(const void* p, size_t bytes) {
   return {lo, lo + bytes};
 }
 
-// Checks that the current device is an sm_100 part; the compute capability is cached per device
-// ordinal.
+}  // namespace
+
+// the compute capability is cached per device ordinal
 kda_status_t check_device() {
   static PerDevice major_of;
   int dev = 0;
@@ -37,8 +38,6 @@ kda_status_t check_device() {
     return KDA_ERR_CUDA;
   return major == 10 ? KDA_OK : KDA_ERR_DEVICE;
 }
-
-}  // namespace
 
 size_t simt_workspace_bytes(const int32_t* plan) {
   return kWsHeaderBytes + (size_t)plan[PH_TOTAL_CHUNKS] * kWsChunkBytes;

@@ -100,6 +100,7 @@ extern "C" const char* kda_status_string(kda_status_t st) {
     case KDA_ERR_CAPACITY:
       return "KDA_ERR_CAPACITY: problem needs more scratch than kda_forward_noalloc's fixed "
              "KDA_NOALLOC_SCRATCH_BYTES; use kda_forward with a workspace";
+    case KDA_ERR_DTYPE: return "KDA_ERR_DTYPE: element type must be bf16, fp16 or fp32";
   }
   return "KDA_ERR_UNKNOWN";
 }

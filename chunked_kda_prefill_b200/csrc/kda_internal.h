@@ -64,6 +64,8 @@ int32_t plan_checksum(const int32_t* plan, size_t n);
 // Host-side validation shared by the entry points; returns KDA_OK or an error code.
 kda_status_t validate_shape(const kda_shape_t* s);
 kda_status_t validate_plan(const int32_t* plan, size_t n, const kda_shape_t* s);
+// KDA_OK if the current device is an sm_100 part.
+kda_status_t check_device();
 // Workspace bytes of kda_forward for a validated plan.
 size_t fused_workspace_bytes(const int32_t* plan);
 

@@ -1,0 +1,162 @@
+"""RMS norm and rotation of query and key heads over libkda.so (include/kda.h).
+
+    q, k = kda.qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, 1e-6, "BSND")
+
+Per token and head, r = 1 / sqrt(mean(x^2) + eps) and n = x r weight; the pair i of the first
+2 * len(inv_freq) channels then turns by position * inv_freq[i].  The outputs are dense in the
+layout, as flash_kda and decode take them.  ``qk_norm_rope`` is differentiable with respect to q, k
+and the weights; ``qk_norm_rope_backward`` is its backward pass as a call of its own.
+
+Single tokens (a decode batch) are the TND layout with one token per sequence: q [B, Nq, D],
+positions [B].
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import KdaError, KdaQkShape, check
+from ._views import (dtype_code, expect, expect_dense, launch_on, needs_grad, view, viewable)
+from .api import LAYOUTS, _ptr
+
+
+def _check(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved) -> KdaQkShape:
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("qk_norm_rope runs on a CUDA device only")
+    if layout not in LAYOUTS:
+        raise KdaError(2, f"layout {layout!r}")
+    if q.dim() != (3 if layout == "TND" else 4) or k.dim() != q.dim():
+        raise KdaError(3, f"q and k have {q.dim()} and {k.dim()} dimensions under {layout}")
+    code = dtype_code(q, "q")
+    if layout == "TND":
+        (S, Nq, D), B, Nk = q.shape, 1, k.shape[1]
+        k_shape, tokens = (S, Nk, D), (S,)
+    elif layout == "BSND":
+        (B, S, Nq, D), Nk = q.shape, k.shape[2]
+        k_shape, tokens = (B, S, Nk, D), (B, S)
+    else:
+        (B, Nq, S, D), Nk = q.shape, k.shape[1]
+        k_shape, tokens = (B, Nk, S, D), (B, S)
+    if max(B, S, Nq, Nk, D) >= 1 << 31:
+        raise KdaError(3, "a size of q or k does not fit 32 bits")
+    expect(k, "k", q.dtype, dev, k_shape)
+    if positions is not None:
+        expect_dense(positions, "positions", torch.int32, dev, tokens)
+    turned = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise KdaError(3, "inv_freq must be a vector")
+        turned = 2 * inv_freq.shape[0]
+        expect_dense(inv_freq, "inv_freq", torch.float32, dev, inv_freq.shape)
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            expect_dense(w, name, torch.float32, dev, (D,))
+    return KdaQkShape(LAYOUTS[layout], B, Nq, Nk, S, D, code, turned, int(bool(interleaved)), eps)
+
+
+def _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved, q_out, k_out,
+             stream):
+    shape = _check(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved)
+    dev = q.device
+    for t, name, like in ((q_out, "q_out", q), (k_out, "k_out", k)):
+        if t is not None:
+            expect_dense(t, name, q.dtype, dev, like.shape)
+    ctx, handle = launch_on(dev, stream)
+    with ctx:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        check(_lib.load().kda_qk_norm_rope(
+            ctypes.byref(shape), ctypes.byref(view(q, "q", layout)),
+            ctypes.byref(view(k, "k", layout)), _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
+            _ptr(k_weight), q_out.data_ptr(), k_out.data_ptr(), handle), "kda_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k_weight,
+                          eps: float, layout: str, interleaved: bool = False,
+                          dq: torch.Tensor | None = None, dk: torch.Tensor | None = None,
+                          stream: torch.cuda.Stream | None = None):
+    """Gradients (dq, dk, dq_weight, dk_weight) of qk_norm_rope at its inputs.
+
+    dq_out, dk_out: the outputs' gradients, like q and k (strides allowed).  dq and dk may be given
+    (dq_out and dk_out themselves where those are dense).  A weight's gradient is None when the
+    weight is.
+    """
+    shape = _check(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved)
+    dev = q.device
+    expect(dq_out, "dq_out", q.dtype, dev, q.shape)
+    expect(dk_out, "dk_out", q.dtype, dev, k.shape)
+    for t, name, like in ((dq, "dq", q), (dk, "dk", k)):
+        if t is not None:
+            expect_dense(t, name, q.dtype, dev, like.shape)
+    L = _lib.load()
+    ws_bytes = ctypes.c_size_t(0)
+    check(L.kda_qk_norm_rope_workspace_size(ctypes.byref(shape), ctypes.byref(ws_bytes)),
+          "kda_qk_norm_rope_workspace_size")
+    ctx, handle = launch_on(dev, stream)
+    with ctx:
+        if dq is None:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        if dk is None:
+            dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        dqw = torch.empty_like(q_weight) if q_weight is not None else None
+        dkw = torch.empty_like(k_weight) if k_weight is not None else None
+        ws = torch.empty(ws_bytes.value, dtype=torch.uint8, device=dev)
+        check(L.kda_qk_norm_rope_backward(
+            ctypes.byref(shape), ctypes.byref(view(dq_out, "dq_out", layout)),
+            ctypes.byref(view(dk_out, "dk_out", layout)), ctypes.byref(view(q, "q", layout)),
+            ctypes.byref(view(k, "k", layout)), _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
+            _ptr(k_weight), ws.data_ptr(), ws_bytes.value, dq.data_ptr(), dk.data_ptr(),
+            _ptr(dqw), _ptr(dkw), handle), "kda_qk_norm_rope_backward")
+    return dq, dk, dqw, dkw
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved):
+        ctx.save_for_backward(q, k, positions, inv_freq, q_weight, k_weight)
+        ctx.call = eps, layout, interleaved
+        return _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved,
+                        None, None, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        dq_out, dk_out = (t if viewable(t) else t.contiguous() for t in (dq_out, dk_out))
+        q, k, positions, inv_freq, q_weight, k_weight = ctx.saved_tensors
+        dq, dk, dqw, dkw = qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq,
+                                                 q_weight, k_weight, *ctx.call)
+        return dq, dk, None, None, dqw, dkw, None, None, None
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps: float, layout: str,
+                 interleaved: bool = False, q_out: torch.Tensor | None = None,
+                 k_out: torch.Tensor | None = None, stream: torch.cuda.Stream | None = None):
+    """Norm and rotation of q and k in one pass.  Returns (q_out, k_out), dense in the layout.
+
+    q, k: bf16, fp16 or fp32, head dim 128 or 64, any numbers of heads (any strides over slots,
+    heads and tokens; channels contiguous and 16-byte aligned, so slices of a fused projection are
+    taken as they lie).  positions: int32 [B, S] ([T] under TND) or None for 0..S-1; a negative one
+    marks padding (zeros out, no part in the gradients).  inv_freq: fp32, radians per position, up
+    to D/2 of them in multiples of 8, or None for no rotation.  q_weight, k_weight: fp32 [D] or
+    None.  Pairs are (i, i + len(inv_freq)), or (2i, 2i + 1) when ``interleaved``.  q_out and k_out
+    may be q and k themselves where those are dense.
+
+    Differentiable when q, k or a weight requires a gradient; then q_out, k_out and stream cannot
+    be given (choose the stream with torch.cuda.stream).
+    """
+    if inv_freq is not None and needs_grad(inv_freq):
+        raise ValueError("inv_freq has no gradient here")
+    if needs_grad(q, k, q_weight, k_weight):
+        if q_out is not None or k_out is not None or stream is not None:
+            raise ValueError("q_out, k_out and stream cannot be combined with inputs that require "
+                             "a gradient")
+        return _QkNormRope.apply(q, k, positions, inv_freq, q_weight, k_weight, eps, layout,
+                                 interleaved)
+    return _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved, q_out,
+                    k_out, stream)

@@ -63,7 +63,8 @@ typedef enum {
   KDA_ERR_TIMEOUT = 12,    /* a bounded device-side wait gave up (reported by kda_device_status) */
   KDA_ERR_DEVICE = 13,     /* the current device is not an sm_100 GPU */
   KDA_ERR_ALIGN = 14,      /* q/k/v/g/out/state/workspace not 16-byte aligned (beta: 2-byte) */
-  KDA_ERR_CAPACITY = 15    /* kda_forward_noalloc: problem needs more than its fixed scratch */
+  KDA_ERR_CAPACITY = 15,   /* kda_forward_noalloc: problem needs more than its fixed scratch */
+  KDA_ERR_DTYPE = 16       /* element type is not bf16, fp16 or fp32 */
 } kda_status_t;
 
 /* Tensor layouts of q/k/v/g/beta/out (FlashKDA README, 参数说明):
@@ -269,6 +270,161 @@ KDA_API kda_status_t kda_decode(int32_t B, int32_t Nqk, int32_t Nv, int32_t D, c
                                 float scale, const float* state_in, const float* A_log,
                                 const float* dt_bias, float lower_bound, void* out,
                                 float* state_out, kda_stream_t stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Operators around the prefill and the decode step of a layer: the gated recurrence (the vector
+ * form of the KDA state) and the norm and rotation of queries and keys.  Each exists forward and
+ * backward, in bf16, fp16 and fp32 with all arithmetic in fp32, in the three layouts above, for
+ * head dims 128 and 64.  Conventions as above: the caller owns every buffer, checks are made on
+ * the host before anything is enqueued, calls are asynchronous on `stream`.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Element type of a call's inputs and outputs (states and parameters are fp32). */
+typedef enum { KDA_BF16 = 0, KDA_FP16 = 1, KDA_FP32 = 2 } kda_dtype_t;
+
+/* A tensor argument that need not be dense: its address and its strides, in elements, over
+ * sequence slots (unused under TND), heads and tokens.  Channels are contiguous.  A stride may be
+ * 0 (a broadcast input).  For tensors with a channel axis the address and the strides are
+ * multiples of 16 bytes (KDA_ERR_ALIGN); a negative stride is KDA_ERR_SHAPE. */
+typedef struct {
+  const void* data;
+  int64_t stride_b, stride_n, stride_s;
+} kda_view_t;
+
+typedef struct {
+  int32_t layout; /* kda_layout_t */
+  int32_t B;      /* sequences: batch slots (BNSD/BSND) or len(cu_seqlens) - 1 (TND) */
+  int32_t N;      /* heads */
+  int32_t S;      /* storage length per slot (BNSD/BSND) or total packed tokens T (TND) */
+  int32_t D;      /* head dim, 128 or 64 */
+  int32_t dtype;  /* kda_dtype_t of x, g, beta, out and their gradients */
+} kda_recurrence_shape_t;
+
+/* The gated recurrence: per sequence, head n and channel d, with kda_forward's activations of
+ * the raw gate g and the write logit beta,
+ *
+ *     a_t = exp(lower_bound * sigmoid(exp(A_log[n]) * (g_t + dt_bias[n, d])))
+ *     h_t = a_t h_{t-1} + sigmoid(beta_t[n]) x_t,        h_0 = initial_state,    out_t = h_t.
+ *
+ * Plan: int32 words built on the host from the shape and the valid lengths alone (cu_seqlens_host
+ * as for kda_plan: prefix sums, required for TND, optional otherwise, every length >= 1).  It
+ * cuts every sequence into tiles of 8192 / D tokens.  Reusable for every call with the same shape
+ * and lengths, forward and backward, whatever the element type. */
+KDA_API kda_status_t kda_recurrence_plan_size(const kda_recurrence_shape_t* shape,
+                                              const int32_t* cu_seqlens_host, size_t* n_int32);
+KDA_API kda_status_t kda_recurrence_plan(const kda_recurrence_shape_t* shape,
+                                         const int32_t* cu_seqlens_host, int32_t* plan,
+                                         size_t n_int32);
+
+/* Device bytes of a plan's workspace for kda_recurrence_forward (backward == 0) or
+ * kda_recurrence_backward (backward != 0).  Calls that overlap on the GPU need one each. */
+KDA_API kda_status_t kda_recurrence_workspace_size(const int32_t* plan_host, size_t n_int32,
+                                                   int32_t backward, size_t* bytes);
+
+/* fp32 values of the `states` buffer: one [N, D] state per tile. */
+KDA_API kda_status_t kda_recurrence_states_size(const int32_t* plan_host, size_t n_int32,
+                                                size_t* n_floats);
+
+/* The forward pass.
+ *   plan_host, plan_dev, n_int32: the plan, and the same words in device memory.
+ *   x, g           : [.., D] in shape's dtype and layout;  beta: the same without channels.
+ *   initial_state  : fp32 [B, N, D] or NULL for zeros;  A_log: fp32 [N];  dt_bias: fp32 [N, D].
+ *   lower_bound    : in [-5, 0].
+ *   states         : fp32, kda_recurrence_states_size values, for kda_recurrence_backward; or
+ *                    NULL.
+ *   workspace      : device scratch, 256-byte aligned; kda_device_status reads its status word.
+ *   out            : dense, x's shape, one rounding to nearest even; rows past a sequence's valid
+ *                    length are written as zeros, and the inputs' rows there are never read.
+ *   final_state    : fp32 [B, N, D], the unrounded state after each sequence's last token; may be
+ *                    initial_state itself (a backward pass then needs a copy of that), must not
+ *                    overlap it otherwise.
+ * Outputs must not overlap one another or an input (KDA_ERR_ALIAS). */
+KDA_API kda_status_t kda_recurrence_forward(
+    const kda_recurrence_shape_t* shape, const int32_t* plan_host, const int32_t* plan_dev,
+    size_t n_int32, const kda_view_t* x, const kda_view_t* g, const kda_view_t* beta,
+    const float* initial_state, const float* A_log, const float* dt_bias, float lower_bound,
+    float* states, void* workspace, size_t workspace_bytes, void* out, float* final_state,
+    kda_stream_t stream);
+
+/* The backward pass.  With lam_t = dout_t + a_{t+1} lam_{t+1} (lam of the last token adds
+ * dfinal_state):
+ *     dx_t = sigmoid(beta_t) lam_t          dbeta_t = sigmoid'(beta_t) sum_d lam_t x_t
+ *     dg_t = lam_t h_{t-1} a_t lower_bound sigmoid'(z_t) exp(A_log)   (z_t the sigmoid's argument)
+ *     ddt_bias = sum dg_t      dA_log = sum dg_t (g_t + dt_bias)      dinitial_state = a_1 lam_1
+ *   states         : as written by kda_recurrence_forward on the same inputs and plan; h is
+ *                    recomputed from it in fp32.
+ *   dout           : as out (strided allowed), or NULL for zeros;  dfinal_state: fp32 [B, N, D]
+ *                    or NULL for zeros.
+ *   dx, dg, dbeta  : dense, like x, g, beta; zeros past a valid length.
+ *   dinitial_state : fp32 [B, N, D], or NULL when it is not wanted.
+ *   dA_log, ddt_bias: fp32 [N], [N, D], summed over all sequences in a fixed order (the same
+ *                    bits on every run). */
+KDA_API kda_status_t kda_recurrence_backward(
+    const kda_recurrence_shape_t* shape, const int32_t* plan_host, const int32_t* plan_dev,
+    size_t n_int32, const kda_view_t* dout, const float* dfinal_state, const kda_view_t* x,
+    const kda_view_t* g, const kda_view_t* beta, const float* initial_state, const float* A_log,
+    const float* dt_bias, float lower_bound, const float* states, void* workspace,
+    size_t workspace_bytes, void* dx, void* dg, void* dbeta, float* dinitial_state,
+    float* dA_log, float* ddt_bias, kda_stream_t stream);
+
+/* One token of the recurrence for each of B sequences.
+ *   x, g: dense [B, N, D];  beta: dense [B, N];  out: dense [B, N, D], all of `dtype`.
+ *   state_in: fp32 [B, N, D] or NULL for zeros;  state_out: fp32 [B, N, D]; may be state_in
+ *   itself (updated in place), must not overlap it otherwise. */
+KDA_API kda_status_t kda_recurrence_step(int32_t B, int32_t N, int32_t D, int32_t dtype,
+                                         const void* x, const void* g, const void* beta,
+                                         const float* state_in, const float* A_log,
+                                         const float* dt_bias, float lower_bound, void* out,
+                                         float* state_out, kda_stream_t stream);
+
+typedef struct {
+  int32_t layout;      /* kda_layout_t */
+  int32_t B;           /* batch slots; ignored under TND */
+  int32_t Nq, Nk;      /* query and key heads, any numbers >= 1 */
+  int32_t S;           /* tokens per slot (BNSD/BSND) or packed tokens (TND; single-token serving
+                          is TND with one token per sequence) */
+  int32_t D;           /* head dim, 128 or 64 */
+  int32_t dtype;       /* kda_dtype_t of q, k, their outputs and gradients */
+  int32_t rotary_dim;  /* channels turned: 0 (norm only) or a multiple of 16 up to D */
+  int32_t interleaved; /* 0: channel i turns with i + rotary_dim/2; 1: 2i with 2i + 1 */
+  float eps;           /* added to the mean square; finite, >= 0 */
+} kda_qk_shape_t;
+
+/* RMS norm of every query and key head with a learned weight, then rotation, in one pass over
+ * the data.  Per row (token, head), r = 1 / sqrt(mean(x^2) + eps) and n = x r weight; the pair i
+ * of the first rotary_dim channels turns by the angle position * inv_freq[i]:
+ *     (n1, n2) -> (n1 cos - n2 sin, n1 sin + n2 cos).
+ * The angle's phase is formed in fp64, so it holds for every int32 position.
+ *   q, k        : [.., D] in the layout (strides allowed: slices of a fused projection).
+ *   positions   : int32, dense [B, S] ([S] under TND), or NULL for 0..S-1 in every slot.  A
+ *                 negative position marks padding: the row is not read, its outputs and gradients
+ *                 are zeros, and it adds nothing to the weights' gradients.
+ *   inv_freq    : fp32 [rotary_dim / 2], radians per position; may be NULL when rotary_dim is 0.
+ *   q_weight, k_weight: fp32 [D], or NULL for ones.
+ *   q_out, k_out: dense in the layout; each may be its own input itself (a dense input, turned in
+ *                 place) and must not overlap anything otherwise (KDA_ERR_ALIAS). */
+KDA_API kda_status_t kda_qk_norm_rope(const kda_qk_shape_t* shape, const kda_view_t* q,
+                                      const kda_view_t* k, const int32_t* positions,
+                                      const float* inv_freq, const float* q_weight,
+                                      const float* k_weight, void* q_out, void* k_out,
+                                      kda_stream_t stream);
+
+/* Device bytes of kda_qk_norm_rope_backward's workspace. */
+KDA_API kda_status_t kda_qk_norm_rope_workspace_size(const kda_qk_shape_t* shape, size_t* bytes);
+
+/* The backward pass: with dn the outputs' gradient turned back by the same angles and xh = x r,
+ *     dx = r (dn weight - xh mean(dn weight xh)),    dweight = sum over rows of dn xh.
+ *   dq_out, dk_out: like q, k (strides allowed).
+ *   dq, dk        : dense in the layout; each may be its own dq_out or dk_out itself, and must not
+ *                   overlap anything otherwise.
+ *   dq_weight, dk_weight: fp32 [D], or NULL when not wanted; summed in a fixed order (the same bits
+ *                   on every run).
+ *   workspace     : 256-byte aligned, kda_qk_norm_rope_workspace_size bytes. */
+KDA_API kda_status_t kda_qk_norm_rope_backward(
+    const kda_qk_shape_t* shape, const kda_view_t* dq_out, const kda_view_t* dk_out,
+    const kda_view_t* q, const kda_view_t* k, const int32_t* positions, const float* inv_freq,
+    const float* q_weight, const float* k_weight, void* workspace, size_t workspace_bytes,
+    void* dq, void* dk, float* dq_weight, float* dk_weight, kda_stream_t stream);
 
 #ifdef __cplusplus
 }
