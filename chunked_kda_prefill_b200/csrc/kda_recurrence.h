@@ -25,9 +25,9 @@ enum RecHeader : int {
 // RR_SLOT is the sequence, RR_ROW0 the tile's first token row within its slot (or in the packed
 // rows), RR_VALID its tokens, RR_STORE its output rows (RR_VALID and the padding after it),
 // RR_INDEX its place in the states and workspace arrays (consecutive within a sequence), RR_TILE
-// its index within the sequence, RR_COUNT the sequence's tiles and RR_LEN its tokens.
+// its index within the sequence and RR_COUNT the sequence's tiles.
 enum RecRecord : int {
-  RR_SLOT = 0, RR_ROW0, RR_VALID, RR_STORE, RR_INDEX, RR_TILE, RR_COUNT, RR_LEN
+  RR_SLOT = 0, RR_ROW0, RR_VALID, RR_STORE, RR_INDEX, RR_TILE, RR_COUNT, RR_RESERVED
 };
 
 kda_status_t validate_recurrence_shape(const kda_recurrence_shape_t* s);

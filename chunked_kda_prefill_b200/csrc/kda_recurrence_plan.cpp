@@ -95,7 +95,7 @@ kda_status_t build(const kda_recurrence_shape_t& s, const int32_t* cu, int32_t* 
     rec[RR_INDEX] = index;
     rec[RR_TILE] = j;
     rec[RR_COUNT] = q.tiles;
-    rec[RR_LEN] = q.len;
+    rec[RR_RESERVED] = 0;
     rec += kRecRecord;
   };
   const bool tnd = s.layout == KDA_LAYOUT_TND;

@@ -77,9 +77,10 @@ def recurrence(x, g, beta, h0, A_log, dt_bias, lb, layout, lengths, dout=None, d
         if not backward:
             continue
         lam = torch.zeros(n, N, D, dtype=torch.float64) if dout is None else pick(dout).clone()
+        M = lam.abs()  # of the terms: a map's product and sum round each before they may cancel
         if dfinal is not None:
             lam[n - 1] += dfinal[b]
-        M = lam.abs()
+            M[n - 1] += dfinal[b].abs()
         E = torch.zeros_like(lam)
         E[n - 1] = U * M[n - 1]
         for t in range(n - 2, -1, -1):
@@ -110,7 +111,7 @@ def recurrence(x, g, beta, h0, A_log, dt_bias, lb, layout, lengths, dout=None, d
         res["dA_log"][0].add_((dg * raw).sum((0, 2)))
         res["dA_log"][1].add_(((Eg + (64 + 2) * U * dg.abs()) * raw.abs()).sum((0, 2)))
         res["dh0"][0][b] = a[0] * lam[0]
-        res["dh0"][1][b] = a[0] * (E[0] + C * U * lam[0].abs())
+        res["dh0"][1][b] = a[0] * (E[0] + C * U * M[0])
     for name in ("out", "dx", "dg", "dbeta"):
         if name in res:
             v, e = res[name]
