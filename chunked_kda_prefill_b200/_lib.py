@@ -100,7 +100,7 @@ def load():
     L.kda_recurrence_forward.argtypes = [p_rec, p_i32, vp, sz, p_view, p_view, p_view, vp, vp, vp,
                                          f32, vp, vp, sz, vp, vp, vp]
     L.kda_recurrence_backward.argtypes = [p_rec, p_i32, vp, sz, p_view, vp, p_view, p_view, p_view,
-                                          vp, vp, vp, f32, vp, vp, sz, vp, vp, vp, vp, vp, vp, vp]
+                                          vp, vp, f32, vp, vp, sz, vp, vp, vp, vp, vp, vp, vp]
     L.kda_recurrence_step.argtypes = [i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, f32, vp, vp, vp]
     L.kda_qk_norm_rope.argtypes = [p_qk, p_view, p_view, vp, vp, vp, vp, vp, vp, vp]
     L.kda_qk_norm_rope_workspace_size.argtypes = [p_qk, p_sz]

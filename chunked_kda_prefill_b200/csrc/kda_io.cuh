@@ -91,16 +91,50 @@ struct GateScale {
 __device__ __forceinline__ GateScale gate_scale(float A_log, float lower_bound) {
   constexpr float kLog2e = 1.4426950408889634f;
   const float ea = expf(A_log);
-  return {ea, -kLog2e * ea, lower_bound * kLog2e};
+  // never zero: a raw gate of -inf closes the gate whatever A_log is
+  return {ea, fminf(-kLog2e * ea, -1.1754944e-38f), lower_bound * kLog2e};
 }
 // sigmoid(z) and, in *t, e^-z (which may be infinite: the sigmoid is then 0)
 __device__ __forceinline__ float gate_sigmoid(const GateScale& c, float raw, float* t) {
   *t = ex2(c.nz * raw);
   return rcp(1.0f + *t);
 }
-// 1 - s without cancellation: s e^-z where s is near 1; e^-z may be infinite only where s is 0
-__device__ __forceinline__ float one_minus(float s, float t) { return s < 0.5f ? 1.0f - s : s * t; }
-
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// 4 channels as two pairs, for the packed fp32 instructions
+struct F4 {
+  float2 lo, hi;
+};
+__device__ __forceinline__ F4 splat(float v) { return {make_float2(v, v), make_float2(v, v)}; }
+__device__ __forceinline__ F4 f4(const float (&x)[4]) {
+  return {make_float2(x[0], x[1]), make_float2(x[2], x[3])};
+}
+__device__ __forceinline__ F4 f4(float4 x) { return {make_float2(x.x, x.y), make_float2(x.z, x.w)}; }
+__device__ __forceinline__ F4 operator+(F4 a, F4 b) {
+  return {__fadd2_rn(a.lo, b.lo), __fadd2_rn(a.hi, b.hi)};
+}
+__device__ __forceinline__ F4 operator*(F4 a, F4 b) {
+  return {__fmul2_rn(a.lo, b.lo), __fmul2_rn(a.hi, b.hi)};
+}
+__device__ __forceinline__ F4 fma4(F4 a, F4 b, F4 c) {
+  return {__ffma2_rn(a.lo, b.lo, c.lo), __ffma2_rn(a.hi, b.hi, c.hi)};
+}
+template <class F>
+__device__ __forceinline__ F4 each(F4 a, F&& f) {
+  return {make_float2(f(a.lo.x), f(a.lo.y)), make_float2(f(a.hi.x), f(a.hi.y))};
+}
+__device__ __forceinline__ F4 lds4(const float* p) { return f4(*reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ void sts4(float* p, F4 v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v.lo.x, v.lo.y, v.hi.x, v.hi.y);
+}
+// memory that other blocks write
+__device__ __forceinline__ F4 ldcg4(const float* p) {
+  return f4(__ldcg(reinterpret_cast<const float4*>(p)));
+}
+template <class T>
+__device__ __forceinline__ void st4(T* p, F4 v) {
+  const float x[4] = {v.lo.x, v.lo.y, v.hi.x, v.hi.y};
+  st4(p, x);
+}
 
 }  // namespace kda

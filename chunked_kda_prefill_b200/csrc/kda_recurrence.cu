@@ -2,19 +2,17 @@
 //     a_t = exp(lb sigmoid(e^A (g_t + bias))),  h_t = a_t h_{t-1} + sigmoid(beta_t) x_t.
 //
 // A run of tokens maps its start state to its end state by h -> A h + H, with A the product of its
-// decays, and such maps compose.  So a sequence is cut into tiles that blocks work on at the same
-// time: a block reads its tile once, forms the tile's map, gets the state before the tile from the
-// tiles before it, and writes the tile's outputs (the backward pass the same from the other end).
-// Both passes are bound by HBM: 6 bytes a value forward (16-bit), 10 backward.
+// decays, and such maps compose.  A cluster of 1 to 8 blocks walks one (sequence, head) from its
+// start (the backward pass from its end), a tile of 8192 values per block and step; a thread has 8
+// tokens of 4 channels.  In a step every thread forms its tokens' map, the block composes its
+// threads' maps and the cluster its blocks', through shared memory, and with the state before its
+// tokens a thread runs through them once more from registers and writes.  The data is read once.
+// Which block does what is fixed by the plan and the launch, so the same call gives the same bits.
 //
-// The state before a tile.  A block publishes its tile's map as soon as it has it and the state
-// behind the tile once it knows that; each with a flag.  It looks back over the flags for the
-// nearest tile whose end state is known, and applies the maps in between in order.  Whichever way
-// a state is reached, it is the same sequence of multiply-adds on the same values, so results do
-// not depend on timing.  Blocks take their tiles from a counter, in the plan's order, so a tile's
-// predecessors are always with blocks that already run: the waits end.
+// Both passes are bound by HBM: 6 bytes a value forward (16-bit), 10 backward.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -31,151 +29,33 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kRows = 8;  // tokens of a thread, 4 channels each
 
-// A tile's place in the chain of its sequence: 0 nothing yet, then the tile's map, then the state
-// that leaves it.
-enum Flag : int32_t { FLAG_NONE = 0, FLAG_MAP = 1, FLAG_STATE = 2 };
-
 struct RecParams {
   kda_view_t x, g, beta, dout;  // device addresses and strides
   const int32_t* plan;
   int32_t checksum;
-  int32_t N, chain;
-  int32_t chained;   // some sequence has more than one tile
+  int32_t N, units;
+  int32_t slot_rows;  // rows that a slot's outputs have, padding included; 0 for packed rows
+  int32_t cluster;
   const float* h0;
   const float* A_log;
   const float* dt_bias;
   float lower_bound;
   const float* dfinal;
-  int32_t* status;   // [0] the status word, [1] the tile counter
-  int32_t* flags;    // [chain][N]
-  float* map_a;      // [chain][N][D] products of decays
-  float* map_h;      // [chain][N][D] end states from zero
-  float* ends;       // [chain][N][D] states that leave the tiles
-  const float* states;  // backward: the forward pass's ends
-  void* out;         // forward: out; backward: dx
+  int32_t* status;
+  float* states;  // [tiles][N][D] the states before the tiles: forward writes, backward reads
+  void* out;      // forward: out; backward: dx
   void* dg;
   void* dbeta;
   float* final_state;
   float* dh0;
-  float* part_bias;  // [chain][N][D]
-  float* part_A;     // [chain][N]
-  kda_view_t od, bd; // strides of the dense outputs with and without channels
+  float* part_bias;   // [B][cluster][N][D]
+  float* part_A;      // [B][cluster][N]
+  kda_view_t od, bd;  // strides of the dense outputs with and without channels
 };
 
 template <class T>
 __device__ __forceinline__ const T* at(const kda_view_t& v, long long b, long long n, long long s) {
   return static_cast<const T*>(v.data) + b * v.stride_b + n * v.stride_n + s * v.stride_s;
-}
-
-__device__ __forceinline__ int32_t ld_acquire(const int32_t* p) {
-  int32_t v;
-  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ void st_release(int32_t* p, int32_t v) {
-  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
-}
-
-// A work item: a tile's record and a head.
-struct Item {
-  int slot, row0, valid, store, index, tile, count, n;
-};
-
-// The block's item, or false when the plan on the device is not the host's.  Forward, counter value
-// i is item i; backward, the tiles with tokens are taken from the last to the first.
-template <bool BACKWARD>
-__device__ __forceinline__ bool take_item(const RecParams& p, int* shared, Item* it) {
-  if (p.plan[RH_CHECKSUM] != p.checksum) {
-    if (threadIdx.x == 0) *p.status = DS_PLAN;
-    return false;
-  }
-  int id = blockIdx.x;
-  if (p.chained) {
-    if (threadIdx.x == 0) *shared = atomicAdd(p.status + 1, 1);
-    __syncthreads();
-    id = *shared;
-  }
-  int k = id / p.N;
-  it->n = id - k * p.N;
-  if (BACKWARD && k < p.chain) k = p.chain - 1 - k;
-  const int4* r = reinterpret_cast<const int4*>(p.plan + kRecHeader + (size_t)k * kRecRecord);
-  const int4 u = __ldg(r), v = __ldg(r + 1);
-  it->slot = u.x;
-  it->row0 = u.y;
-  it->valid = u.z;
-  it->store = u.w;
-  it->index = v.x;
-  it->tile = v.y;
-  it->count = v.z;
-  return true;
-}
-
-// One warp publishes 4 channels a lane of one or two arrays, then the flag.
-__device__ __forceinline__ void publish(int32_t* flag, int32_t value, bool mine, float* to_a,
-                                        const float (&a)[4], float* to_b, const float (&b)[4]) {
-  if (mine) {
-    *reinterpret_cast<float4*>(to_a) = make_float4(a[0], a[1], a[2], a[3]);
-    if (to_b) *reinterpret_cast<float4*>(to_b) = make_float4(b[0], b[1], b[2], b[3]);
-  }
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) {
-    __threadfence();
-    st_release(flag, value);
-  }
-}
-
-__device__ __forceinline__ void ld_shared_by_blocks(const float* p, float (&v)[4]) {
-  const float4 w = __ldcg(reinterpret_cast<const float4*>(p));
-  v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-}
-
-// The state that enters a tile, for one warp: 4 channels a lane at `chan`.  `before` tiles precede
-// it in the chain's direction, at index + step, index + 2 step, ...; the first one of a chain
-// publishes its end state without looking.  Publishes the tile's own map first if it has to wait.
-// A wait that gives up records DS_TIMEOUT and returns NaN.
-template <int D>
-__device__ void look_back(const RecParams& p, const Item& it, int step, int before, bool mine,
-                          int chan, bool successor, const float (&ta)[4], const float (&th)[4],
-                          float (&c)[4]) {
-  const int lane = threadIdx.x & 31;
-  const size_t own = (size_t)it.index * p.N + it.n;
-  const long long stride = (long long)step * p.N;
-  bool published = !successor;
-  int base = 0, found = -1;
-  for (int tries = 0; found < 0; ++tries) {
-    const int back = base + lane;  // 0 is the direct predecessor
-    const int32_t f =
-        back < before ? ld_acquire(p.flags + (long long)own + (back + 1) * stride) : FLAG_NONE;
-    const unsigned state = __ballot_sync(0xffffffffu, f == FLAG_STATE);
-    const unsigned some = __ballot_sync(0xffffffffu, f != FLAG_NONE);
-    const int first = __ffs(state) - 1;
-    if (first >= 0 && (~some & ((1u << first) - 1u)) == 0) {
-      found = base + first;
-      break;
-    }
-    if (!published) {
-      publish(p.flags + own, FLAG_MAP, mine, p.map_a + own * D + chan, ta, p.map_h + own * D + chan,
-              th);
-      published = true;
-    }
-    if (some == 0xffffffffu) base += 32;  // only maps so far: look further back
-    if ((tries & 1023) == 1023 &&
-        (tries > (1 << 21) || *reinterpret_cast<volatile int32_t*>(p.status) != DS_OK)) {
-      if (lane == 0) atomicCAS(p.status, DS_OK, DS_TIMEOUT);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) c[e] = __int_as_float(0x7fc00000);
-      return;
-    }
-  }
-  __syncwarp();
-  ld_shared_by_blocks(p.ends + (own + (found + 1) * stride) * D + chan, c);
-  for (int i = found - 1; i >= 0; --i) {
-    float a[4], h[4];
-    ld_shared_by_blocks(p.map_a + (own + (i + 1) * stride) * D + chan, a);
-    ld_shared_by_blocks(p.map_h + (own + (i + 1) * stride) * D + chan, h);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] = fmaf(a[e], c[e], h[e]);
-  }
 }
 
 // Which 4 channels and 8 tokens of a tile a thread has.
@@ -185,153 +65,307 @@ struct Place {
   static constexpr int kGroups = kThreads / kLanes;
   static constexpr int kTile = kGroups * kRows;
   static_assert(kTile == rec_tile_rows(D), "a tile is the block's threads by their tokens");
-  int chan, group;
-  __device__ Place() : chan((threadIdx.x % kLanes) * 4), group(threadIdx.x / kLanes) {}
+  int chan, group, r0;
+  __device__ Place()
+      : chan((threadIdx.x % kLanes) * 4), group(threadIdx.x / kLanes), r0(group * kRows) {}
 };
 
-// sigmoid of the write logits of the tile's tokens, into shared memory
+// One (sequence, head) of the walk.
+struct Unit {
+  int slot, start, len, base;  // the plan's record
+  int n, steps;
+  int place;  // of the sequence in the plan
+};
+
+// A block's walk: units in rounds over the clusters, every other round in reverse, so that with the
+// plan's order (longest first) no cluster gets the longer unit of every round.  The record of the
+// unit after the current one is requested a unit ahead.
+struct Walk {
+  Unit u;
+  int step, round;
+  int4 ahead;
+
+  __device__ static int index(const RecParams& p, int round) {
+    const int clusters = gridDim.x / p.cluster, q = blockIdx.x / p.cluster;
+    const long long i = (long long)round * clusters + (round & 1 ? clusters - 1 - q : q);
+    return i < p.units ? (int)i : -1;
+  }
+  __device__ static int4 record(const RecParams& p, int round) {
+    const int i = index(p, round);
+    const int4* rec = reinterpret_cast<const int4*>(p.plan + kRecHeader);
+    return i < 0 ? make_int4(0, 0, 0, 0) : __ldg(rec + i / p.N);
+  }
+  template <int R>
+  __device__ void enter(const RecParams& p) {
+    const int i = index(p, round);
+    u.slot = ahead.x;
+    u.start = ahead.y;
+    u.len = ahead.z;
+    u.base = ahead.w;
+    u.place = i < 0 ? -1 : i / p.N;
+    u.n = i < 0 ? -1 : i - u.place * p.N;
+    const int rows = p.slot_rows ? p.slot_rows : u.len;
+    u.steps = ((rows - 1) / R) / p.cluster + 1;
+    step = 0;
+    ahead = record(p, round + 1);
+  }
+  template <int R>
+  __device__ void begin(const RecParams& p) {
+    round = 0;
+    ahead = record(p, 0);
+    enter<R>(p);
+  }
+  template <int R>
+  __device__ void next(const RecParams& p) {
+    if (++step < u.steps) return;
+    ++round;
+    enter<R>(p);
+  }
+  __device__ bool done() const { return u.n < 0; }
+};
+
+// A block's tile in a step: its first row within the sequence, its rows with tokens, and whether any
+// block of the cluster has such rows.
+struct Tile {
+  int row, valid, index;
+  bool work;
+};
+template <int R, bool BACKWARD>
+__device__ __forceinline__ Tile tile_of(const RecParams& p, const Walk& w, int rank) {
+  Tile t;
+  const int first = (BACKWARD ? w.u.steps - 1 - w.step : w.step) * p.cluster;
+  t.index = first + rank;
+  // the cluster's last tiles may lie behind the slot, and behind 32 bits
+  t.row = (int)min((long long)t.index * R, (long long)INT_MAX);
+  t.valid = max(0, min(R, w.u.len - t.row));
+  t.work = (long long)first * R < w.u.len;
+  return t;
+}
+
+// Whether the plan on the device is the host's; block 0 leaves the status.
+__device__ __forceinline__ bool same_plan(const RecParams& p) {
+  const bool same = p.plan[RH_CHECKSUM] == p.checksum;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = same ? DS_OK : DS_PLAN;
+  return same;
+}
+
+// ---- clusters ----
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 4 floats at this block's shared address `p` in the block of another rank
+__device__ __forceinline__ F4 ld_rank(const float* p, int rank) {
+  uint32_t addr = (uint32_t)__cvta_generic_to_shared(p), far;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(addr), "r"(rank));
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(far)
+               : "memory");
+  return f4(v);
+}
+
+// ---- loads ----
+// 4 channels from global to the thread's own place in shared memory
+template <class T>
+__device__ __forceinline__ void copy_async(T* to, const T* from) {
+  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
+  if constexpr (sizeof(T) == 2)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(from));
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from));
+}
+template <class T>
+__device__ __forceinline__ F4 own4(const T* p) {
+  Vec4<T> v;
+  v.w = *reinterpret_cast<const decltype(v.w)*>(p);
+  float x[4];
+  widen(v, x);
+  return f4(x);
+}
+
+// Starts the loads of the thread's tokens of one tensor; every thread reads only what it copied
+// itself.  Behind the last token the channels are zeros, or -inf where they are gates: sigmoid and
+// write are then zero and the decay one, so those rows change no map.
 template <class T, int D>
-__device__ __forceinline__ void load_beta(const RecParams& p, const Item& it, float* sb) {
-  for (int r = threadIdx.x; r < Place<D>::kTile; r += kThreads)
-    sb[r] = r < it.valid ? sigmoid(to_f32(*at<T>(p.beta, it.slot, it.n, it.row0 + r))) : 0.f;
+__device__ __forceinline__ void request(T* to, const kda_view_t& v, const Unit& u, const Tile& t,
+                                        const Place<D>& me, bool gate) {
+  const T* from = at<T>(v, u.slot, u.n, (long long)u.start + t.row + me.r0) + me.chan;
+  T* dst = to + me.r0 * D + me.chan;
+  const int mine = t.valid - me.r0;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    if (k < mine) {
+      copy_async(dst + k * D, from);
+      from += v.stride_s;
+    } else {
+      st4(dst + k * D, splat(gate ? -INFINITY : 0.f));
+    }
+  }
+}
+// The write logits of a tile, one a thread.
+template <class T>
+__device__ __forceinline__ float request_beta(const RecParams& p, const Unit& u, const Tile& t) {
+  const int r = threadIdx.x;
+  return r < t.valid ? to_f32(*at<T>(p.beta, u.slot, u.n, (long long)u.start + t.row + r)) : 0.f;
+}
+
+// Two stages of shared memory for the tile at work and the next one; fp32 tiles have one, so that
+// two blocks still fit an SM.
+template <class T>
+constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
+
+template <class T, int D>
+constexpr int forward_smem() {
+  return kStages<T> * 2 * kRecTileElems * (int)sizeof(T);
+}
+template <class T, int D>
+constexpr int backward_smem() {
+  return kStages<T> * 3 * kRecTileElems * (int)sizeof(T);
 }
 
 template <class T, int D>
 __global__ void __launch_bounds__(kThreads, 2) rec_forward_kernel(const RecParams p) {
   using P = Place<D>;
-  __shared__ int ticket;
-  __shared__ float sb[P::kTile];
-  __shared__ __align__(16) float sa[P::kGroups][D], sh[P::kGroups][D], carry[D];
-  Item it;
-  if (!take_item<false>(p, &ticket, &it)) return;
+  constexpr int R = P::kTile;
+  extern __shared__ __align__(16) unsigned char raw_smem[];
+  T* const stage = reinterpret_cast<T*>(raw_smem);  // [kStages][g, x][R][D]
+  __shared__ float sb[2][R];
+  __shared__ __align__(16) float sa[2][P::kGroups][D], sh[2][P::kGroups][D];
+  __shared__ __align__(16) float map_a[2][D], map_h[2][D], carry_in[D], carry_out[D];
+  if (!same_plan(p)) return;
   const P me;
-  const int r0 = me.group * kRows;
-  T* out = static_cast<T*>(p.out) + (long long)it.slot * p.od.stride_b +
-           (long long)it.n * p.od.stride_n + (long long)it.row0 * p.od.stride_s + me.chan;
-  if (it.valid == 0) {  // padding
-    const float z[4] = {};
-    for (int i = 0; i < kRows; ++i)
-      if (r0 + i < it.store) st4(out + (long long)(r0 + i) * p.od.stride_s, z);
-    return;
-  }
-  const T* xs = at<T>(p.x, it.slot, it.n, it.row0) + me.chan;
-  const T* gs = at<T>(p.g, it.slot, it.n, it.row0) + me.chan;
-  Vec4<T> rx[kRows], rg[kRows];
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    rx[i] = rg[i] = Vec4<T>{};
-    if (r0 + i < it.valid) {
-      rg[i] = ld4(gs + (long long)(r0 + i) * p.g.stride_s);
-      rx[i] = ld4(xs + (long long)(r0 + i) * p.x.stride_s);
+  const int rank = blockIdx.x % p.cluster;
+  Walk now, next;
+  now.begin<R>(p);
+  next = now;
+  F4 h0_next = splat(0.f);
+  float beta = 0.f;
+  // the loads of `next`'s tile, and its start state where a unit begins
+  auto start = [&](int i) {
+    if (!next.done()) {
+      const Tile t = tile_of<R, false>(p, next, rank);
+      T* to = stage + (i % kStages<T>) * 2 * kRecTileElems;
+      if (t.work) {
+        request(to, p.g, next.u, t, me, true);
+        request(to + kRecTileElems, p.x, next.u, t, me, false);
+      }
+      beta = request_beta<T>(p, next.u, t);
+      if (next.step == 0) {
+        h0_next = splat(0.f);
+        if (p.h0)
+          h0_next = f4(*reinterpret_cast<const float4*>(
+              p.h0 + ((size_t)next.u.slot * p.N + next.u.n) * D + me.chan));
+      }
     }
-  }
-  load_beta<T, D>(p, it, sb);
-  const GateScale gc = gate_scale(__ldg(p.A_log + it.n), p.lower_bound);
-  float bias[4];
-  ld_shared_by_blocks(p.dt_bias + (size_t)it.n * D + me.chan, bias);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  start(0);
+  if (threadIdx.x < R) sb[0][threadIdx.x] = sigmoid(beta);
   __syncthreads();
+  F4 carry = splat(0.f);
+  for (int i = 0; !now.done(); ++i) {
+    const int buf = i & 1;
+    const Tile t = tile_of<R, false>(p, now, rank);
+    if (now.step == 0) carry = h0_next;
+    next.next<R>(p);
+    if (kStages<T> == 2) start(i + 1);
+    const T* const tg = stage + (i % kStages<T>) * 2 * kRecTileElems + me.r0 * D + me.chan;
+    const T* const tx = tg + kRecTileElems;
+    const GateScale gc = gate_scale(__ldg(p.A_log + now.u.n), p.lower_bound);
+    const F4 bias =
+        f4(__ldg(reinterpret_cast<const float4*>(p.dt_bias + (size_t)now.u.n * D + me.chan)));
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages<T> - 1) : "memory");
 
-  // the thread's own run of tokens: decays, writes and the map
-  float a[kRows][4], u[kRows][4], pa[4], ph[4];
+    // the thread's own tokens: decays, writes and the map
+    F4 a[kRows], u[kRows], pa = splat(1.f), ph = splat(0.f);
+    if (t.work) {
+      const F4 nz = splat(gc.nz), l2 = splat(gc.l2), one = splat(1.f);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    pa[e] = 1.f;
-    ph[e] = 0.f;
-  }
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    float g[4];
-    widen(rg[i], g);
-    widen(rx[i], u[i]);
-    const float b = sb[r0 + i];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float t;
-      a[i][e] = r0 + i < it.valid ? ex2(gc.l2 * gate_sigmoid(gc, g[e] + bias[e], &t)) : 1.f;
-      u[i][e] *= b;
-      pa[e] *= a[i][e];
-      ph[e] = fmaf(a[i][e], ph[e], u[i][e]);
+      for (int k = 0; k < kRows; ++k) {
+        const F4 e = each((own4(tg + k * D) + bias) * nz, ex2);
+        a[k] = each(each(e + one, rcp) * l2, ex2);
+        u[k] = own4(tx + k * D) * splat(sb[buf][me.r0 + k]);
+        pa = pa * a[k];
+        ph = fma4(a[k], ph, u[k]);
+      }
+      sts4(&sa[buf][me.group][me.chan], pa);
+      sts4(&sh[buf][me.group][me.chan], ph);
     }
-  }
-  st4(&sa[me.group][me.chan], pa);
-  st4(&sh[me.group][me.chan], ph);
-  __syncthreads();
-  // the map of the tokens before the thread's own
-  float qa[4], qh[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    qa[e] = 1.f;
-    qh[e] = 0.f;
-  }
-  for (int k = 0; k < me.group; ++k) {
-    const float4 ka = *reinterpret_cast<const float4*>(&sa[k][me.chan]);
-    const float4 kh = *reinterpret_cast<const float4*>(&sh[k][me.chan]);
-    qa[0] *= ka.x; qa[1] *= ka.y; qa[2] *= ka.z; qa[3] *= ka.w;
-    qh[0] = fmaf(ka.x, qh[0], kh.x);
-    qh[1] = fmaf(ka.y, qh[1], kh.y);
-    qh[2] = fmaf(ka.z, qh[2], kh.z);
-    qh[3] = fmaf(ka.w, qh[3], kh.w);
-  }
-  const size_t st = ((size_t)it.slot * p.N + it.n) * D + me.chan;
-  const size_t own = (size_t)it.index * p.N + it.n;
-  if (threadIdx.x >= kThreads - 32) {  // the warp that has the last tokens
-    const bool mine = me.group == P::kGroups - 1;
-    const bool successor = it.tile + 1 < it.count;
-    float ta[4], th[4], c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      ta[e] = qa[e] * pa[e];
-      th[e] = fmaf(pa[e], qh[e], ph[e]);
+    if (kStages<T> == 1) start(i + 1);
+    if (threadIdx.x < R) sb[buf ^ 1][threadIdx.x] = sigmoid(beta);
+    __syncthreads();
+    F4 h = carry;
+    if (t.work) {
+      if (p.cluster == 1) {
+        for (int k = 0; k < P::kGroups; ++k) {
+          if (k == me.group) h = carry;
+          carry = fma4(lds4(&sa[buf][k][me.chan]), carry, lds4(&sh[buf][k][me.chan]));
+        }
+      } else {
+        // the block's map, for the other ranks; the map before the thread's own tokens meanwhile
+        if (threadIdx.x < P::kLanes) {
+          F4 ta = splat(1.f), th = splat(0.f);
+          for (int k = 0; k < P::kGroups; ++k) {
+            const F4 ka = lds4(&sa[buf][k][me.chan]);
+            ta = ta * ka;
+            th = fma4(ka, th, lds4(&sh[buf][k][me.chan]));
+          }
+          sts4(&map_a[buf][me.chan], ta);
+          sts4(&map_h[buf][me.chan], th);
+        }
+        cluster_arrive();
+        F4 qa = splat(1.f), qh = splat(0.f);
+        for (int k = 0; k < me.group; ++k) {
+          const F4 ka = lds4(&sa[buf][k][me.chan]);
+          qa = qa * ka;
+          qh = fma4(ka, qh, lds4(&sh[buf][k][me.chan]));
+        }
+        cluster_wait();
+        if (threadIdx.x < P::kLanes) {
+          for (int r = 0; r < p.cluster; ++r) {
+            if (r == rank) sts4(&carry_in[me.chan], carry);
+            carry = fma4(ld_rank(&map_a[buf][me.chan], r), carry, ld_rank(&map_h[buf][me.chan], r));
+          }
+          sts4(&carry_out[me.chan], carry);
+        }
+        __syncthreads();
+        h = lds4(&carry_in[me.chan]);
+        carry = lds4(&carry_out[me.chan]);
+        if (me.group == 0 && p.states && t.valid > 0)
+          sts4(p.states + ((size_t)(now.u.base + t.index) * p.N + now.u.n) * D + me.chan, h);
+        h = fma4(qa, h, qh);
+      }
     }
-    if (it.tile > 0) {
-      look_back<D>(p, it, -1, it.tile, mine, me.chan, successor, ta, th, c);
-    } else if (p.h0) {
-      const float4 w = *reinterpret_cast<const float4*>(p.h0 + st);
-      c[0] = w.x; c[1] = w.y; c[2] = w.z; c[3] = w.w;
-    }
-    float end[4];
+    if (p.cluster == 1 && me.group == 0 && p.states && t.valid > 0)
+      sts4(p.states + ((size_t)(now.u.base + t.index) * p.N + now.u.n) * D + me.chan, h);
+    // the outputs, and zeros behind the last token
+    {
+      const int rows = p.slot_rows ? min(R, p.slot_rows - t.row) : t.valid;
+      T* out = static_cast<T*>(p.out) + (long long)now.u.slot * p.od.stride_b +
+               (long long)now.u.n * p.od.stride_n +
+               ((long long)now.u.start + t.row + me.r0) * p.od.stride_s + me.chan;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) end[e] = fmaf(ta[e], c[e], th[e]);
-    if (successor) publish(p.flags + own, FLAG_STATE, mine, p.ends + own * D + me.chan, end, nullptr, end);
-    if (mine) {
-      st4(&carry[me.chan], c);
-      if (!successor) st4(p.final_state + st, end);
+      for (int k = 0; k < kRows; ++k) {
+        if (t.work) h = fma4(a[k], h, u[k]);
+        if (me.r0 + k < rows) st4(out, me.r0 + k < t.valid ? h : splat(0.f));
+        out += p.od.stride_s;
+      }
     }
+    if (rank == 0 && me.group == 0 && now.step + 1 == now.u.steps)
+      sts4(p.final_state + ((size_t)now.u.slot * p.N + now.u.n) * D + me.chan, carry);
+    now = next;
   }
-  __syncthreads();
-  float h[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) h[e] = fmaf(qa[e], carry[me.chan + e], qh[e]);
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = fmaf(a[i][e], h[e], u[i][e]);
-    T* dst = out + (long long)(r0 + i) * p.od.stride_s;
-    if (r0 + i < it.valid) {
-      st4(dst, h);
-    } else if (r0 + i < it.store) {
-      const float z[4] = {};
-      st4(dst, z);
-    }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (p.cluster > 1) {  // no block leaves while another reads its map
+    cluster_arrive();
+    cluster_wait();
   }
-}
-
-// 4 channels from global to the thread's own place in shared memory, or zeros there
-template <class T>
-__device__ __forceinline__ void copy_async(T* to, const T* from, bool real) {
-  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
-  const int n = real ? (int)sizeof(T) * 4 : 0;
-  if constexpr (sizeof(T) == 2)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(from), "r"(n));
-  else
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(n));
-}
-
-template <class T>
-__device__ __forceinline__ void ld_own(const T* p, float (&x)[4]) {
-  Vec4<T> v;
-  v.w = *reinterpret_cast<const decltype(v.w)*>(p);
-  widen(v, x);
 }
 
 // Sums of 8 values over the LANES lanes of a group, by halving the values as the distance halves:
@@ -357,199 +391,225 @@ __device__ __forceinline__ float group_sum8(float (&v)[8], int lane) {
 template <class T, int D>
 __global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(const RecParams p) {
   using P = Place<D>;
+  constexpr int R = P::kTile;
   extern __shared__ __align__(16) unsigned char raw_smem[];
-  T* const sg = reinterpret_cast<T*>(raw_smem);  // g, x, dout of the tile, [kTile][D] each
-  T* const sx = sg + kRecTileElems;
-  T* const sd = sx + kRecTileElems;
-  __shared__ int ticket;
-  __shared__ float sb[P::kTile], sum_a[kThreads / 32];
-  __shared__ __align__(16) float sa[P::kGroups][D], sh[P::kGroups][D], sc[P::kGroups][D], carry[D];
-  Item it;
-  if (!take_item<true>(p, &ticket, &it)) return;
+  T* const stage = reinterpret_cast<T*>(raw_smem);  // [kStages][g, x, dout][R][D]
+  __shared__ float sb[2][R], sum_a[kThreads / 32];
+  __shared__ __align__(16) float sa[P::kGroups][D], sh[P::kGroups][D], sc[P::kGroups][D];
+  __shared__ __align__(16) float map_a[D], map_c[D], carry_in[D], carry_out[D];
+  if (!same_plan(p)) return;
   const P me;
-  const int r0 = me.group * kRows;
-  const long long o0 = (long long)it.slot * p.od.stride_b + (long long)it.n * p.od.stride_n +
-                       (long long)it.row0 * p.od.stride_s + me.chan;
-  T* dx = static_cast<T*>(p.out) + o0;
-  T* dg = static_cast<T*>(p.dg) + o0;
-  T* dbeta = static_cast<T*>(p.dbeta) + (long long)it.slot * p.bd.stride_b +
-             (long long)it.n * p.bd.stride_n + (long long)it.row0 * p.bd.stride_s;
-  const float zeros[4] = {};
-  // padding rows, of a tile without tokens or behind the last one
+  const int rank = blockIdx.x % p.cluster;
+  Walk now, next;
+  now.begin<R>(p);
+  next = now;
+  F4 c_next = splat(0.f), h_next = splat(0.f);
+  float beta = 0.f;
+  auto start = [&](int i) {
+    if (!next.done()) {
+      const Tile t = tile_of<R, true>(p, next, rank);
+      T* to = stage + (i % kStages<T>) * 3 * kRecTileElems;
+      if (t.work) {
+        request(to, p.g, next.u, t, me, true);
+        request(to + kRecTileElems, p.x, next.u, t, me, false);
+        if (p.dout.data) {
+          request(to + 2 * kRecTileElems, p.dout, next.u, t, me, false);
+        } else {
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = r0 + i;
-    if (r >= it.valid && r < it.store) {
-      st4(dx + (long long)r * p.od.stride_s, zeros);
-      st4(dg + (long long)r * p.od.stride_s, zeros);
-      if (me.chan == 0) dbeta[(long long)r * p.bd.stride_s] = from_f32<T>(0.f);
-    }
-  }
-  if (it.valid == 0) return;
-
-  const T* xs = at<T>(p.x, it.slot, it.n, it.row0) + me.chan;
-  const T* gs = at<T>(p.g, it.slot, it.n, it.row0) + me.chan;
-  const T* ds = p.dout.data ? at<T>(p.dout, it.slot, it.n, it.row0) + me.chan : xs;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int r = r0 + i, s = r * D + me.chan;
-    const bool real = r < it.valid;
-    copy_async(sg + s, real ? gs + (long long)r * p.g.stride_s : gs, real);
-    copy_async(sx + s, real ? xs + (long long)r * p.x.stride_s : xs, real);
-    copy_async(sd + s, real ? ds + (long long)r * p.dout.stride_s : ds, real && p.dout.data);
-  }
-  load_beta<T, D>(p, it, sb);
-  const GateScale gc = gate_scale(__ldg(p.A_log + it.n), p.lower_bound);
-  const size_t st = ((size_t)it.slot * p.N + it.n) * D + me.chan;
-  const size_t own = (size_t)it.index * p.N + it.n;
-  float bias[4], h[4] = {};
-  ld_shared_by_blocks(p.dt_bias + (size_t)it.n * D + me.chan, bias);
-  if (it.tile > 0) ld_shared_by_blocks(p.states + (own - p.N) * D + me.chan, h);
-  else if (p.h0) ld_shared_by_blocks(p.h0 + st, h);
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncthreads();
-
-  // decays, and the maps of the thread's tokens: of the state forwards, of a_t lam_t backwards
-  float a[kRows][4], w[kRows][4], pa[4], ph[4], pc[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    pa[e] = 1.f;
-    ph[e] = pc[e] = 0.f;
-  }
-  const float slope = p.lower_bound * gc.ea;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    const int s = (r0 + i) * D + me.chan;
-    float g[4], x[4], d[4];
-    ld_own(sg + s, g);
-    ld_own(sx + s, x);
-    ld_own(sd + s, d);
-    const float b = sb[r0 + i];
-    const bool real = r0 + i < it.valid;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float t;
-      const float sig = gate_sigmoid(gc, g[e] + bias[e], &t);
-      a[i][e] = real ? ex2(gc.l2 * sig) : 1.f;
-      w[i][e] = real ? slope * sig * one_minus(sig, t) * a[i][e] : 0.f;
-      pa[e] *= a[i][e];
-      ph[e] = fmaf(a[i][e], ph[e], b * x[e]);
-      pc[e] = fmaf(pa[e], d[e], pc[e]);
-    }
-  }
-  st4(&sa[me.group][me.chan], pa);
-  st4(&sh[me.group][me.chan], ph);
-  st4(&sc[me.group][me.chan], pc);
-  __syncthreads();
-  // the warp with the first tokens gets what comes from behind the tile
-  if (threadIdx.x < 32) {
-    const bool mine = me.group == 0, last = it.tile + 1 == it.count;
-    float ta[4], tc[4], c[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      ta[e] = 1.f;
-      tc[e] = 0.f;
-    }
-    for (int k = P::kGroups - 1; k >= 0; --k)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float ka = sa[k][me.chan + e];
-        ta[e] *= ka;
-        tc[e] = fmaf(ka, tc[e], sc[k][me.chan + e]);
+          for (int k = 0; k < kRows; ++k)
+            st4(to + 2 * kRecTileElems + (me.r0 + k) * D + me.chan, splat(0.f));
+        }
       }
-    if (!last) look_back<D>(p, it, 1, it.count - 1 - it.tile, mine, me.chan, it.tile > 0, ta, tc, c);
-    else if (p.dfinal) ld_shared_by_blocks(p.dfinal + st, c);
-    float end[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) end[e] = fmaf(ta[e], c[e], tc[e]);
-    if (it.tile > 0) publish(p.flags + own, FLAG_STATE, mine, p.ends + own * D + me.chan, end, nullptr, end);
-    if (mine) {
-      st4(&carry[me.chan], c);
-      if (it.tile == 0 && p.dh0) st4(p.dh0 + st, end);
+      beta = request_beta<T>(p, next.u, t);
+      h_next = splat(0.f);
+      if (t.valid > 0)
+        h_next = f4(__ldg(reinterpret_cast<const float4*>(
+            p.states + ((size_t)(next.u.base + t.index) * p.N + next.u.n) * D + me.chan)));
+      if (next.step == 0) {
+        c_next = splat(0.f);
+        if (p.dfinal)
+          c_next = f4(__ldg(reinterpret_cast<const float4*>(
+              p.dfinal + ((size_t)next.u.slot * p.N + next.u.n) * D + me.chan)));
+      }
     }
-  }
-  // the state before each token, into w: dg = lam w
-  for (int k = 0; k < me.group; ++k)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = fmaf(sa[k][me.chan + e], h[e], sh[k][me.chan + e]);
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    float x[4];
-    ld_own(sx + (r0 + i) * D + me.chan, x);
-    const float b = sb[r0 + i];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      w[i][e] *= h[e];
-      h[e] = fmaf(a[i][e], h[e], b * x[e]);
-    }
-  }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  start(0);
+  if (threadIdx.x < R) sb[0][threadIdx.x] = sigmoid(beta);
   __syncthreads();
-  float c[4], dot[kRows], sum_b[4] = {}, sum_raw = 0.f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) c[e] = carry[me.chan + e];
-  for (int k = P::kGroups - 1; k > me.group; --k)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] = fmaf(sa[k][me.chan + e], c[e], sc[k][me.chan + e]);
-#pragma unroll
-  for (int i = kRows - 1; i >= 0; --i) {
-    const int r = r0 + i, s = r * D + me.chan;
-    float g[4], x[4], d[4], lam[4], dgr[4];
-    ld_own(sg + s, g);
-    ld_own(sx + s, x);
-    ld_own(sd + s, d);
-    const float b = sb[r];
-    dot[i] = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      lam[e] = d[e] + c[e];
-      c[e] = a[i][e] * lam[e];
-      dot[i] = fmaf(lam[e], x[e], dot[i]);
-      dgr[e] = lam[e] * w[i][e];
-      lam[e] *= b;
-      sum_b[e] += dgr[e];
-      sum_raw = fmaf(dgr[e], g[e] + bias[e], sum_raw);
+  F4 carry = splat(0.f), sum_b = splat(0.f), sum_raw = splat(0.f);
+  for (int i = 0; !now.done(); ++i) {
+    const Tile t = tile_of<R, true>(p, now, rank);
+    const float* const b = sb[i & 1] + me.r0;
+    if (now.step == 0) {
+      carry = c_next;
+      sum_b = sum_raw = splat(0.f);
     }
-    if (r < it.valid) {
-      st4(dx + (long long)r * p.od.stride_s, lam);
-      st4(dg + (long long)r * p.od.stride_s, dgr);
+    F4 h = h_next;
+    next.next<R>(p);
+    if (kStages<T> == 2) start(i + 1);
+    const T* const tg = stage + (i % kStages<T>) * 3 * kRecTileElems + me.r0 * D + me.chan;
+    const T* const tx = tg + kRecTileElems;
+    const T* const td = tx + kRecTileElems;
+    const GateScale gc = gate_scale(__ldg(p.A_log + now.u.n), p.lower_bound);
+    const F4 bias =
+        f4(__ldg(reinterpret_cast<const float4*>(p.dt_bias + (size_t)now.u.n * D + me.chan)));
+    const long long row = p.od.stride_s;
+    const long long first = (long long)now.u.start + t.row + me.r0;
+    const long long o0 = (long long)now.u.slot * p.od.stride_b + (long long)now.u.n * p.od.stride_n +
+                         first * row + me.chan;
+    T* const dx = static_cast<T*>(p.out) + o0;
+    T* const dg = static_cast<T*>(p.dg) + o0;
+    T* const dbeta = static_cast<T*>(p.dbeta) + (long long)now.u.slot * p.bd.stride_b +
+                     (long long)now.u.n * p.bd.stride_n + first * p.bd.stride_s;
+    const int rows = p.slot_rows ? min(R, p.slot_rows - t.row) : t.valid;
+    if (t.valid < rows) {  // zeros behind the last token
+      for (int k = 0; k < kRows; ++k)
+        if (me.r0 + k >= t.valid && me.r0 + k < rows) {
+          st4(dx + k * row, splat(0.f));
+          st4(dg + k * row, splat(0.f));
+          if (me.chan == 0) dbeta[k * p.bd.stride_s] = from_f32<T>(0.f);
+        }
     }
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages<T> - 1) : "memory");
+
+    // decays, and the maps of the thread's tokens: of the state forwards, of a_t lam_t backwards
+    F4 a[kRows], w[kRows];
+    if (t.work) {
+      F4 pa = splat(1.f), ph = splat(0.f), pc = splat(0.f);
+      const F4 nz = splat(gc.nz), l2 = splat(gc.l2), one = splat(1.f);
+      const F4 slope = splat(p.lower_bound * gc.ea);
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        // e is kept finite: 1 - sigmoid is e sigmoid, without cancellation, and where the sigmoid
+        // is zero so is their product
+        const F4 e = each((own4(tg + k * D) + bias) * nz, [](float z) { return fminf(ex2(z), 3e38f); });
+        const F4 sig = each(e + one, rcp);
+        a[k] = each(sig * l2, ex2);
+        w[k] = sig * (e * sig) * (slope * a[k]);
+        pa = pa * a[k];
+        ph = fma4(a[k], ph, own4(tx + k * D) * splat(b[k]));
+        pc = fma4(pa, own4(td + k * D), pc);
+      }
+      sts4(&sa[me.group][me.chan], pa);
+      sts4(&sh[me.group][me.chan], ph);
+      sts4(&sc[me.group][me.chan], pc);
+    }
+    if (kStages<T> == 2 && threadIdx.x < R) sb[~i & 1][threadIdx.x] = sigmoid(beta);
+    __syncthreads();
+    float dot[kRows];
+    if (t.work) {
+      if (p.cluster > 1) {
+        if (threadIdx.x < P::kLanes) {
+          F4 ta = splat(1.f), tc = splat(0.f);
+          for (int k = P::kGroups - 1; k >= 0; --k) {
+            const F4 ka = lds4(&sa[k][me.chan]);
+            ta = ta * ka;
+            tc = fma4(ka, tc, lds4(&sc[k][me.chan]));
+          }
+          sts4(&map_a[me.chan], ta);
+          sts4(&map_c[me.chan], tc);
+        }
+        cluster_arrive();
+      }
+      // the state before each token, into w: dg = lam w
+      for (int k = 0; k < me.group; ++k) h = fma4(lds4(&sa[k][me.chan]), h, lds4(&sh[k][me.chan]));
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        w[k] = w[k] * h;
+        h = fma4(a[k], h, own4(tx + k * D) * splat(b[k]));
+      }
+      // a_t lam_t of what follows the thread's tokens
+      F4 c = carry;
+      if (p.cluster > 1) {
+        cluster_wait();
+        if (threadIdx.x < P::kLanes) {
+          for (int r = p.cluster - 1; r >= 0; --r) {
+            if (r == rank) sts4(&carry_in[me.chan], carry);
+            carry = fma4(ld_rank(&map_a[me.chan], r), carry, ld_rank(&map_c[me.chan], r));
+          }
+          sts4(&carry_out[me.chan], carry);
+        }
+        cluster_arrive();  // the maps have been read
+        __syncthreads();
+        c = lds4(&carry_in[me.chan]);
+        carry = lds4(&carry_out[me.chan]);
+        for (int k = P::kGroups - 1; k > me.group; --k)
+          c = fma4(lds4(&sa[k][me.chan]), c, lds4(&sc[k][me.chan]));
+        cluster_wait();
+      } else {
+        for (int k = P::kGroups - 1; k >= 0; --k) {
+          if (k == me.group) c = carry;
+          carry = fma4(lds4(&sa[k][me.chan]), carry, lds4(&sc[k][me.chan]));
+        }
+      }
+      F4 here_b = splat(0.f), here_raw = splat(0.f);
+#pragma unroll
+      for (int k = kRows - 1; k >= 0; --k) {
+        dot[k] = 0.f;
+        if (me.r0 + k < t.valid) {
+          const F4 lam = own4(td + k * D) + c;
+          c = a[k] * lam;
+          const F4 dgk = lam * w[k], lx = lam * own4(tx + k * D);
+          dot[k] = (lx.lo.x + lx.lo.y) + (lx.hi.x + lx.hi.y);
+          st4(dx + k * row, lam * splat(b[k]));
+          st4(dg + k * row, dgk);
+          here_b = here_b + dgk;
+          here_raw = fma4(dgk, own4(tg + k * D) + bias, here_raw);
+        }
+      }
+      sum_b = sum_b + here_b;
+      sum_raw = sum_raw + here_raw;
+      // dbeta: the sum over the token's channels
+      constexpr int kEach = P::kLanes / kRows;  // lanes that end with the same token
+      const int lane = threadIdx.x % P::kLanes, k = lane / kEach;
+      const float sum = group_sum8<P::kLanes>(dot, lane);
+      if (lane % kEach == 0 && me.r0 + k < t.valid)
+        dbeta[k * p.bd.stride_s] = from_f32<T>(sum * b[k] * (1.f - b[k]));
+    }
+    if (kStages<T> == 1) {
+      start(i + 1);
+      if (threadIdx.x < R) sb[~i & 1][threadIdx.x] = sigmoid(beta);
+    }
+    __syncthreads();  // the maps are read, and of one stage the next logits written
+    if (now.step + 1 == now.u.steps) {
+      if (p.dh0 && rank == 0 && me.group == 0)
+        sts4(p.dh0 + ((size_t)now.u.slot * p.N + now.u.n) * D + me.chan, carry);
+      // the unit's part of the parameters' gradients
+      float raw = (sum_raw.lo.x + sum_raw.lo.y) + (sum_raw.hi.x + sum_raw.hi.y);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) raw += __shfl_xor_sync(0xffffffffu, raw, o);
+      if ((threadIdx.x & 31) == 0) sum_a[threadIdx.x >> 5] = raw;
+      sts4(&sh[me.group][me.chan], sum_b);
+      __syncthreads();
+      const size_t part = ((size_t)now.u.place * p.cluster + rank) * p.N + now.u.n;
+      if (threadIdx.x < D) {
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < P::kGroups; ++k) sum += sh[k][threadIdx.x];
+        p.part_bias[part * D + threadIdx.x] = sum;
+      } else if (threadIdx.x == D) {
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kThreads / 32; ++k) sum += sum_a[k];
+        p.part_A[part] = sum;
+      }
+      __syncthreads();
+    }
+    now = next;
   }
-  // dbeta: the sum over the token's channels
-  {
-    constexpr int kEach = P::kLanes / 8;  // lanes that end with the same token
-    const int lane = threadIdx.x % P::kLanes;
-    const float sum = group_sum8<P::kLanes>(dot, lane);
-    const int r = r0 + lane / kEach;
-    if (lane % kEach == 0 && r < it.valid) {
-      const float b = sb[r];
-      dbeta[(long long)r * p.bd.stride_s] = from_f32<T>(sum * b * (1.f - b));
-    }
-  }
-  // the tile's part of the parameters' gradients
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum_raw += __shfl_xor_sync(0xffffffffu, sum_raw, o);
-  if ((threadIdx.x & 31) == 0) sum_a[threadIdx.x >> 5] = sum_raw;
-  __syncthreads();  // sh is free: its last reads are before the previous barrier
-  st4(&sh[me.group][me.chan], sum_b);
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < P::kGroups; ++k) sum += sh[k][threadIdx.x];
-    p.part_bias[own * D + threadIdx.x] = sum;
-  } else if (threadIdx.x == D) {
-    float sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < kThreads / 32; ++k) sum += sum_a[k];
-    p.part_A[own] = sum;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (p.cluster > 1) {
+    cluster_arrive();
+    cluster_wait();
   }
 }
 
-// ddt_bias and dA_log: the tiles' parts in a fixed order, in fp64.  A block has 32 channels of a
+// ddt_bias and dA_log: the units' parts in a fixed order, in fp64.  A block has 32 channels of a
 // head (the first one of a head its dA_log too), 32 threads a channel.
 template <int D>
 __global__ void __launch_bounds__(1024) rec_params_kernel(const float* part_bias,
-                                                          const float* part_A, int chain, int N,
+                                                          const float* part_A, int parts, int N,
                                                           float* dA_log, float* ddt_bias) {
   __shared__ double red[32][33];
   constexpr int kBlocks = D / 32;
@@ -557,7 +617,7 @@ __global__ void __launch_bounds__(1024) rec_params_kernel(const float* part_bias
   const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   double sum = 0;
 #pragma unroll 4
-  for (int k = row; k < chain; k += 32) sum += part_bias[((size_t)k * N + n) * D + d];
+  for (int k = row; k < parts; k += 32) sum += part_bias[((size_t)k * N + n) * D + d];
   red[row][lane] = sum;
   __syncthreads();
   if (row == 0) {
@@ -567,7 +627,7 @@ __global__ void __launch_bounds__(1024) rec_params_kernel(const float* part_bias
   if (blockIdx.x % kBlocks != 0) return;
   __syncthreads();
   sum = 0;
-  for (int k = threadIdx.x; k < chain; k += 1024) sum += part_A[(size_t)k * N + n];
+  for (int k = threadIdx.x; k < parts; k += 1024) sum += part_A[(size_t)k * N + n];
   red[row][lane] = sum;
   __syncthreads();
   if (row == 0) {
@@ -644,8 +704,8 @@ kda_status_t prepare(const kda_recurrence_shape_t* shape, const int32_t* plan_ho
   p->plan = plan_dev;
   p->checksum = plan_host[RH_CHECKSUM];
   p->N = shape->N;
-  p->chain = plan_host[RH_CHAIN];
-  p->chained = plan_host[RH_MAX_TILES] > 1;
+  p->units = shape->B * shape->N;
+  p->slot_rows = shape->layout == KDA_LAYOUT_TND ? 0 : shape->S;
   p->h0 = h0;
   p->A_log = A_log;
   p->dt_bias = dt_bias;
@@ -661,58 +721,92 @@ size_t states_floats(const int32_t* plan) {
   return (size_t)plan[RH_CHAIN] * plan[RH_N] * plan[RH_D];
 }
 
-// The workspace after its header: the flags, and the tiles' maps and end states of a chained plan;
-// then the parameters' partial gradients of a backward pass.
+// The workspace after its header: the parameters' partial gradients of a backward pass, one of each
+// block of a cluster at the most.
 struct Scratch {
-  size_t flags, map_a, map_h, ends, part_bias, part_A, total;
+  size_t part_A, total;
   Scratch(const int32_t* plan, bool backward) {
-    const size_t items = (size_t)plan[RH_CHAIN] * plan[RH_N];
-    const bool chained = plan[RH_MAX_TILES] > 1;
-    size_t off = kWsHeaderBytes;
-    auto take = [&off](size_t bytes) {
-      const size_t here = off;
-      off += (bytes + 255) / 256 * 256;
-      return here;
-    };
-    flags = take(chained ? items * 4 : 0);
-    map_a = take(chained ? states_floats(plan) * 4 : 0);
-    map_h = take(chained ? states_floats(plan) * 4 : 0);
-    ends = take(chained ? states_floats(plan) * 4 : 0);
-    part_bias = take(backward ? states_floats(plan) * 4 : 0);
-    part_A = take(backward ? items * 4 : 0);
-    total = off;
-  }
-  void place(void* workspace, RecParams* p) const {
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p->flags = reinterpret_cast<int32_t*>(ws + flags);
-    p->map_a = reinterpret_cast<float*>(ws + map_a);
-    p->map_h = reinterpret_cast<float*>(ws + map_h);
-    p->ends = reinterpret_cast<float*>(ws + ends);
-    p->part_bias = reinterpret_cast<float*>(ws + part_bias);
-    p->part_A = reinterpret_cast<float*>(ws + part_A);
+    const size_t heads = (size_t)plan[RH_B] * (1 << (kRecClusters - 1)) * plan[RH_N];
+    part_A = kWsHeaderBytes + heads * plan[RH_D] * 4;
+    total = backward ? part_A + heads * 4 : kWsHeaderBytes;
   }
 };
 
-template <class T, int D>
-cudaError_t launch_forward(const RecParams& p, unsigned grid, cudaStream_t s) {
-  rec_forward_kernel<T, D><<<grid, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+// What a kernel's launches need to know of a device: the blocks that it holds at a time, as clusters
+// of each size.
+struct Resident {
+  PerDevice of[kRecClusters];
+};
+
+void configure(int smem, int cluster, unsigned blocks, cudaStream_t s, cudaLaunchConfig_t* cfg,
+               cudaLaunchAttribute* attr) {
+  *cfg = cudaLaunchConfig_t{};
+  cfg->gridDim = dim3(blocks);
+  cfg->blockDim = dim3(kThreads);
+  cfg->dynamicSmemBytes = (size_t)smem;
+  cfg->stream = s;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = (unsigned)cluster;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+
+// Clusters of 2^c blocks that the current device holds at a time.
+template <class K>
+cudaError_t resident_clusters(K kernel, Resident& r, int smem, int c, int* clusters) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return once_per_device(r.of[c], dev, clusters, [&](int, int* n) {
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr;
+    configure(smem, 1 << c, 1u << c, nullptr, &cfg, &attr);
+    err = cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
+    return err == cudaSuccess && *n < 1 ? cudaErrorLaunchOutOfResources : err;
+  });
+}
+
+// Launches a pass on clusters of the size that takes the fewest steps one after another: those of
+// the longest unit, or, where that is more, of all units over the clusters that run at a time.  The
+// exchange between blocks makes a step of a cluster longer by about a third.
+template <class K>
+cudaError_t launch(K kernel, Resident& r, int smem, RecParams& p, const int32_t* plan,
+                   cudaStream_t s) {
+  int best = 0, best_clusters = 0;
+  double least = 0;
+  for (int c = 0; c < kRecClusters; ++c) {
+    int clusters = 0;
+    const cudaError_t e = resident_clusters(kernel, r, smem, c, &clusters);
+    if (e != cudaSuccess) return e;
+    const double all = (double)plan[RH_STEPS + c] * p.N / std::min(clusters, p.units);
+    const double one = (double)((plan[RH_MAX_TILES] + (1 << c) - 1) >> c);
+    const double cost = std::max(all, one) * (c == 0 ? 3 : 4);
+    if (c == 0 || cost < least) {
+      least = cost;
+      best = c;
+      best_clusters = clusters;
+    }
+  }
+  p.cluster = 1 << best;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  configure(smem, p.cluster, (unsigned)std::min(best_clusters, p.units) * p.cluster, s, &cfg, &attr);
+  return cudaLaunchKernelEx(&cfg, kernel, (const RecParams)p);
 }
 
 template <class T, int D>
-cudaError_t launch_backward(const RecParams& p, unsigned grid, cudaStream_t s) {
-  static PerDevice ready;
-  constexpr int kSmem = 3 * kRecTileElems * (int)sizeof(T);
-  int dev = 0, unused = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess)
-    e = once_per_device(ready, dev, &unused, [](int, int*) {
-      return cudaFuncSetAttribute(rec_backward_kernel<T, D>,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    });
-  if (e != cudaSuccess) return e;
-  rec_backward_kernel<T, D><<<grid, kThreads, kSmem, s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_forward(RecParams& p, const int32_t* plan, cudaStream_t s) {
+  static Resident resident;
+  return launch(rec_forward_kernel<T, D>, resident, forward_smem<T, D>(), p, plan, s);
+}
+
+template <class T, int D>
+cudaError_t launch_backward(RecParams& p, const int32_t* plan, cudaStream_t s) {
+  static Resident resident;
+  return launch(rec_backward_kernel<T, D>, resident, backward_smem<T, D>(), p, plan, s);
 }
 
 template <class F>
@@ -774,8 +868,8 @@ extern "C" kda_status_t kda_recurrence_forward(
   if (!out || !final_state) return KDA_ERR_NULL;
   if (!aligned16(out) || !aligned16(final_state) || !aligned16(states)) return KDA_ERR_ALIGN;
   const Sizes z = sizes_of(*shape);
-  // final_state may be initial_state itself: the tile that reads the start state does so before the
-  // tile that writes the end state has its carry
+  // final_state may be initial_state itself: a unit's blocks have read its start state before the
+  // barrier of its first step, and its end state is written after that of its last
   if (final_state == initial_state) in[3] = ByteRange{};
   const ByteRange outs[] = {dense_range(out, z.x), dense_range(final_state, z.state),
                             dense_range(states, states_floats(plan_host) * 4)};
@@ -783,16 +877,11 @@ extern "C" kda_status_t kda_recurrence_forward(
   if ((st = check_device()) != KDA_OK) return st;
 
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const Scratch scratch(plan_host, false);
-  scratch.place(workspace, &p);
-  if (states) p.ends = states;
+  p.states = states;
   p.out = out;
   p.final_state = final_state;
-  // the status word, the tile counter and the flags start at zero
-  if (cudaMemsetAsync(workspace, 0, scratch.map_a, s) != cudaSuccess) return KDA_ERR_CUDA;
-  const unsigned grid = (unsigned)plan_host[RH_TILES] * shape->N;
   const cudaError_t e = dispatch(*shape, [&](auto* tag, auto d) {
-    return launch_forward<std::remove_pointer_t<decltype(tag)>, decltype(d)::value>(p, grid, s);
+    return launch_forward<std::remove_pointer_t<decltype(tag)>, decltype(d)::value>(p, plan_host, s);
   });
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
@@ -800,13 +889,13 @@ extern "C" kda_status_t kda_recurrence_forward(
 extern "C" kda_status_t kda_recurrence_backward(
     const kda_recurrence_shape_t* shape, const int32_t* plan_host, const int32_t* plan_dev,
     size_t n_int32, const kda_view_t* dout, const float* dfinal_state, const kda_view_t* x,
-    const kda_view_t* g, const kda_view_t* beta, const float* initial_state, const float* A_log,
-    const float* dt_bias, float lower_bound, const float* states, void* workspace,
-    size_t workspace_bytes, void* dx, void* dg, void* dbeta, float* dinitial_state,
-    float* dA_log, float* ddt_bias, kda_stream_t stream) {
+    const kda_view_t* g, const kda_view_t* beta, const float* A_log, const float* dt_bias,
+    float lower_bound, const float* states, void* workspace, size_t workspace_bytes, void* dx,
+    void* dg, void* dbeta, float* dinitial_state, float* dA_log, float* ddt_bias,
+    kda_stream_t stream) {
   RecParams p{};
   ByteRange in[9], r_dout;
-  kda_status_t st = prepare(shape, plan_host, plan_dev, n_int32, x, g, beta, initial_state, A_log,
+  kda_status_t st = prepare(shape, plan_host, plan_dev, n_int32, x, g, beta, nullptr, A_log,
                             dt_bias, lower_bound, workspace, workspace_bytes, true, &p, in);
   if (st != KDA_OK) return st;
   if (!states || !dx || !dg || !dbeta || !dA_log || !ddt_bias) return KDA_ERR_NULL;
@@ -832,22 +921,22 @@ extern "C" kda_status_t kda_recurrence_backward(
 
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const Scratch scratch(plan_host, true);
-  scratch.place(workspace, &p);
-  p.states = states;
+  uint8_t* const ws = static_cast<uint8_t*>(workspace);
+  p.part_bias = reinterpret_cast<float*>(ws + kWsHeaderBytes);
+  p.part_A = reinterpret_cast<float*>(ws + scratch.part_A);
+  p.states = const_cast<float*>(states);
   p.dfinal = dfinal_state;
   p.out = dx;
   p.dg = dg;
   p.dbeta = dbeta;
   p.dh0 = dinitial_state;
-  if (cudaMemsetAsync(workspace, 0, scratch.map_a, s) != cudaSuccess) return KDA_ERR_CUDA;
-  const unsigned grid = (unsigned)plan_host[RH_TILES] * shape->N;
   const cudaError_t e = dispatch(*shape, [&](auto* tag, auto d) {
     constexpr int D = decltype(d)::value;
-    const cudaError_t err =
-        launch_backward<std::remove_pointer_t<decltype(tag)>, D>(p, grid, s);
+    using T = std::remove_pointer_t<decltype(tag)>;
+    const cudaError_t err = launch_backward<T, D>(p, plan_host, s);
     if (err != cudaSuccess) return err;
     rec_params_kernel<D><<<(unsigned)shape->N * (D / 32), 1024, 0, s>>>(
-        p.part_bias, p.part_A, p.chain, p.N, dA_log, ddt_bias);
+        p.part_bias, p.part_A, shape->B * p.cluster, p.N, dA_log, ddt_bias);
     return cudaGetLastError();
   });
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

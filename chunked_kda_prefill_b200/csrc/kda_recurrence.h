@@ -5,30 +5,28 @@
 
 namespace kda {
 
-// A plan is an int32 header followed by one record per tile.  A tile is kRecTileElems / D
-// consecutive tokens of one sequence, for all heads (a work item is a tile and a head).  The first
-// RH_CHAIN records are the tiles that hold valid tokens, ordered by their index within the
-// sequence and then longest sequence first: every tile comes after its predecessor, and the tiles
-// in flight at one time belong to as many sequences as possible.  The records after them are the
-// tiles of pure padding, whose output rows are only zeroed.
+// A plan is an int32 header followed by one record per sequence, longest first.  A tile is
+// kRecTileElems / D consecutive tokens of one (sequence, head); a cluster of blocks walks one
+// (sequence, head) at a time, a tile per block and step.
 constexpr int32_t kRecMagic = 0x4B524331;  // "KRC1"
 constexpr int32_t kRecVersion = 1;
-constexpr int kRecHeader = 16;
-constexpr int kRecRecord = 8;
+constexpr int kRecHeader = 24;
+constexpr int kRecRecord = 4;
 constexpr int kRecTileElems = 8192;
 constexpr int rec_tile_rows(int D) { return kRecTileElems / D; }
+// Cluster sizes that a launch chooses from: 1, 2, 4, 8.
+constexpr int kRecClusters = 4;
 
+// RH_CHAIN is the number of tiles with tokens, RH_MAX_TILES that of the sequence with most tiles
+// (padding rows included), RH_STEPS + c the steps of one head of every sequence on clusters of 2^c.
 enum RecHeader : int {
-  RH_MAGIC = 0, RH_VERSION, RH_HEADER_WORDS, RH_RECORD_WORDS, RH_TILES, RH_CHAIN, RH_LAYOUT, RH_B,
-  RH_N, RH_S, RH_D, RH_MAX_TILES, RH_TILE_ROWS, RH_RESERVED, RH_TABLE_HASH, RH_CHECKSUM
+  RH_MAGIC = 0, RH_VERSION, RH_HEADER_WORDS, RH_RECORD_WORDS, RH_LAYOUT, RH_B, RH_N, RH_S, RH_D,
+  RH_TILE_ROWS, RH_CHAIN, RH_MAX_TILES, RH_STEPS, RH_TABLE_HASH = RH_STEPS + kRecClusters,
+  RH_CHECKSUM = kRecHeader - 1
 };
-// RR_SLOT is the sequence, RR_ROW0 the tile's first token row within its slot (or in the packed
-// rows), RR_VALID its tokens, RR_STORE its output rows (RR_VALID and the padding after it),
-// RR_INDEX its place in the states and workspace arrays (consecutive within a sequence), RR_TILE
-// its index within the sequence and RR_COUNT the sequence's tiles.
-enum RecRecord : int {
-  RR_SLOT = 0, RR_ROW0, RR_VALID, RR_STORE, RR_INDEX, RR_TILE, RR_COUNT, RR_RESERVED
-};
+// RR_SLOT is the sequence, RR_START its first token within its slot (or in the packed rows),
+// RR_LEN its tokens and RR_BASE the place of its first tile in the states.
+enum RecRecord : int { RR_SLOT = 0, RR_START, RR_LEN, RR_BASE };
 
 kda_status_t validate_recurrence_shape(const kda_recurrence_shape_t* s);
 // Checks a host plan's header (its own checksum, which covers a hash of the records) and, when

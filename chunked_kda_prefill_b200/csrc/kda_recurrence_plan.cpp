@@ -1,5 +1,5 @@
-// kda_recurrence_plan.cpp -- host planner of the gated recurrence: the tiles of every sequence in
-// an order that any work item's predecessors precede.  Reads lengths only; never touches the GPU.
+// kda_recurrence_plan.cpp -- host planner of the gated recurrence: the sequences, longest first, and
+// how many steps they take.  Reads lengths only; never touches the GPU.
 #include <algorithm>
 #include <climits>
 #include <cstring>
@@ -31,8 +31,7 @@ uint32_t fnv(const int32_t* w, size_t n, uint32_t h = 2166136261u) {
   return h;
 }
 
-// Tile counts of a problem: records in all, and those with valid tokens.  Calls f(b, len) for
-// every sequence.
+// Calls f(b, len) for every sequence of a well-formed problem.
 template <class F>
 kda_status_t each_length(const kda_recurrence_shape_t& s, const int32_t* cu, F&& f) {
   const bool tnd = s.layout == KDA_LAYOUT_TND;
@@ -46,86 +45,59 @@ kda_status_t each_length(const kda_recurrence_shape_t& s, const int32_t* cu, F&&
   return KDA_OK;
 }
 
-struct Counts {
-  long long tiles = 0, chain = 0;
-};
+long long tiles_of(long long rows, int R) { return (rows + R - 1) / R; }
 
-kda_status_t count_tiles(const kda_recurrence_shape_t& s, const int32_t* cu, Counts* c) {
+// Whether the lengths are well formed and everything fits the kernels' 32-bit counters.
+kda_status_t check_lengths(const kda_recurrence_shape_t& s, const int32_t* cu) {
   const int R = rec_tile_rows(s.D);
-  const long long slot_tiles = ((long long)s.S + R - 1) / R;
+  long long tiles = 0;
   const kda_status_t st = each_length(s, cu, [&](int, int32_t len) {
-    const long long n = ((long long)len + R - 1) / R;
-    c->chain += n;
-    c->tiles += s.layout == KDA_LAYOUT_TND ? n : slot_tiles;
+    tiles += tiles_of(s.layout == KDA_LAYOUT_TND ? len : s.S, R);
   });
   if (st != KDA_OK) return st;
-  // a launch has one block per (tile, head)
-  if (c->tiles > INT_MAX / kRecRecord - kRecHeader || c->tiles * s.N > INT_MAX) return KDA_ERR_SHAPE;
-  return KDA_OK;
+  return tiles > INT_MAX / 2 ? KDA_ERR_SHAPE : KDA_OK;
 }
 
 kda_status_t build(const kda_recurrence_shape_t& s, const int32_t* cu, int32_t* plan, size_t n) {
-  Counts c;
-  kda_status_t st = count_tiles(s, cu, &c);
+  kda_status_t st = check_lengths(s, cu);
   if (st != KDA_OK) return st;
-  if (n < (size_t)kRecHeader + (size_t)c.tiles * kRecRecord) return KDA_ERR_PLAN;
-
+  if (n < (size_t)kRecHeader + (size_t)s.B * kRecRecord) return KDA_ERR_PLAN;
   const int R = rec_tile_rows(s.D);
-  struct Seq { int32_t b, start, len, tiles, base; };
+  const bool tnd = s.layout == KDA_LAYOUT_TND;
+  struct Seq { int32_t b, start, len; };
   std::vector<Seq> seqs;
   seqs.reserve(s.B);
-  each_length(s, cu, [&](int b, int32_t len) {
-    const int32_t start = s.layout == KDA_LAYOUT_TND ? cu[b] : 0;
-    seqs.push_back({b, start, len, (int32_t)(((long long)len + R - 1) / R), 0});
-  });
+  each_length(s, cu, [&](int b, int32_t len) { seqs.push_back({b, tnd ? cu[b] : 0, len}); });
   std::stable_sort(seqs.begin(), seqs.end(),
-                   [](const Seq& a, const Seq& d) { return a.tiles > d.tiles; });
-  int32_t base = 0;
-  for (Seq& q : seqs) {
-    q.base = base;
-    base += q.tiles;
-  }
-
-  int32_t* rec = plan + kRecHeader;
-  auto put = [&](const Seq& q, int32_t j, int32_t valid, int32_t store, int32_t index) {
-    rec[RR_SLOT] = q.b;
-    rec[RR_ROW0] = q.start + j * R;
-    rec[RR_VALID] = valid;
-    rec[RR_STORE] = store;
-    rec[RR_INDEX] = index;
-    rec[RR_TILE] = j;
-    rec[RR_COUNT] = q.tiles;
-    rec[RR_RESERVED] = 0;
-    rec += kRecRecord;
-  };
-  const bool tnd = s.layout == KDA_LAYOUT_TND;
-  for (int32_t j = 0; j < seqs.front().tiles; ++j)
-    for (const Seq& q : seqs) {
-      if (q.tiles <= j) break;  // the rest are shorter
-      const int32_t valid = std::min(R, q.len - j * R);
-      put(q, j, valid, tnd ? valid : std::min(R, s.S - j * R), q.base + j);
-    }
-  if (!tnd) {
-    const int32_t slot_tiles = (int32_t)(((long long)s.S + R - 1) / R);
-    for (const Seq& q : seqs)
-      for (int32_t j = q.tiles; j < slot_tiles; ++j) put(q, j, 0, std::min(R, s.S - j * R), 0);
-  }
-
+                   [](const Seq& a, const Seq& d) { return a.len > d.len; });
   std::memset(plan, 0, kRecHeader * sizeof(int32_t));
+  int32_t* rec = plan + kRecHeader;
+  long long base = 0, most = 0, steps[kRecClusters] = {};
+  for (const Seq& q : seqs) {
+    rec[RR_SLOT] = q.b;
+    rec[RR_START] = q.start;
+    rec[RR_LEN] = q.len;
+    rec[RR_BASE] = (int32_t)base;
+    rec += kRecRecord;
+    base += tiles_of(q.len, R);
+    const long long all = tiles_of(tnd ? q.len : s.S, R);
+    most = std::max(most, all);
+    for (int c = 0; c < kRecClusters; ++c) steps[c] += tiles_of(all, 1 << c);
+  }
   plan[RH_MAGIC] = kRecMagic;
   plan[RH_VERSION] = kRecVersion;
   plan[RH_HEADER_WORDS] = kRecHeader;
   plan[RH_RECORD_WORDS] = kRecRecord;
-  plan[RH_TILES] = (int32_t)c.tiles;
-  plan[RH_CHAIN] = (int32_t)c.chain;
   plan[RH_LAYOUT] = s.layout;
   plan[RH_B] = s.B;
   plan[RH_N] = s.N;
   plan[RH_S] = s.S;
   plan[RH_D] = s.D;
-  plan[RH_MAX_TILES] = seqs.front().tiles;
   plan[RH_TILE_ROWS] = R;
-  plan[RH_TABLE_HASH] = (int32_t)(fnv(plan + kRecHeader, (size_t)c.tiles * kRecRecord) & 0x7fffffff);
+  plan[RH_CHAIN] = (int32_t)base;
+  plan[RH_MAX_TILES] = (int32_t)most;
+  for (int c = 0; c < kRecClusters; ++c) plan[RH_STEPS + c] = (int32_t)steps[c];
+  plan[RH_TABLE_HASH] = (int32_t)(fnv(plan + kRecHeader, (size_t)s.B * kRecRecord) & 0x7fffffff);
   plan[RH_CHECKSUM] = (int32_t)(fnv(plan, RH_CHECKSUM) & 0x7fffffff);
   return KDA_OK;
 }
@@ -139,8 +111,7 @@ kda_status_t validate_recurrence_plan(const int32_t* p, size_t n, const kda_recu
       p[RH_HEADER_WORDS] != kRecHeader || p[RH_RECORD_WORDS] != kRecRecord)
     return KDA_ERR_PLAN;
   if ((int32_t)(fnv(p, RH_CHECKSUM) & 0x7fffffff) != p[RH_CHECKSUM]) return KDA_ERR_PLAN;
-  if (p[RH_TILES] < 1 || n < (size_t)kRecHeader + (size_t)p[RH_TILES] * kRecRecord)
-    return KDA_ERR_PLAN;
+  if (p[RH_B] < 1 || n < (size_t)kRecHeader + (size_t)p[RH_B] * kRecRecord) return KDA_ERR_PLAN;
   if (s && (p[RH_LAYOUT] != s->layout || p[RH_B] != s->B || p[RH_N] != s->N || p[RH_S] != s->S ||
             p[RH_D] != s->D))
     return KDA_ERR_PLAN;
@@ -156,10 +127,9 @@ extern "C" kda_status_t kda_recurrence_plan_size(const kda_recurrence_shape_t* s
   if (!n_int32) return KDA_ERR_NULL;
   kda_status_t st = validate_recurrence_shape(shape);
   if (st != KDA_OK) return st;
-  Counts c;
-  st = count_tiles(*shape, cu, &c);
+  st = check_lengths(*shape, cu);
   if (st != KDA_OK) return st;
-  *n_int32 = (size_t)kRecHeader + (size_t)c.tiles * kRecRecord;
+  *n_int32 = (size_t)kRecHeader + (size_t)shape->B * kRecRecord;
   return KDA_OK;
 }
 

@@ -31,7 +31,7 @@ _P_I32 = ctypes.POINTER(ctypes.c_int32)
 
 @dataclass
 class KdaRecurrencePlan:
-    """Host and device copies of the tile schedule, and the sizes that it asks for."""
+    """Host and device copies of the schedule, and the sizes that it asks for."""
     shape: KdaRecurrenceShape
     layout: str
     host: np.ndarray
@@ -61,7 +61,7 @@ class KdaRecurrencePlan:
     @property
     def tiles(self) -> int:
         """Tiles that hold valid tokens."""
-        return int(self.host[5])
+        return int(self.host[10])
 
 
 def recurrence_plan(x: torch.Tensor, layout: str, cu_seqlens=None) -> KdaRecurrencePlan:
@@ -205,8 +205,8 @@ def gated_recurrence_backward(dout, dfinal_state, x, g, beta, initial_state, A_l
             ctypes.byref(view(dout, "dout", layout)) if dout is not None else None,
             _ptr(dfinal_state), ctypes.byref(view(x, "x", layout)),
             ctypes.byref(view(g, "g", layout)),
-            ctypes.byref(view(beta, "beta", layout, channels=False)), _ptr(initial_state),
-            A_log.data_ptr(), dt_bias.data_ptr(), float(lower_bound), states.data_ptr(),
+            ctypes.byref(view(beta, "beta", layout, channels=False)), A_log.data_ptr(),
+            dt_bias.data_ptr(), float(lower_bound), states.data_ptr(),
             ws.data_ptr(), ws_bytes, dx.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr(dh0),
             dA_log.data_ptr(), ddt_bias.data_ptr(), handle), "kda_recurrence_backward")
     return dx, dg, dbeta, dh0, dA_log, ddt_bias

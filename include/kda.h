@@ -307,9 +307,9 @@ typedef struct {
  *     h_t = a_t h_{t-1} + sigmoid(beta_t[n]) x_t,        h_0 = initial_state,    out_t = h_t.
  *
  * Plan: int32 words built on the host from the shape and the valid lengths alone (cu_seqlens_host
- * as for kda_plan: prefix sums, required for TND, optional otherwise, every length >= 1).  It
- * cuts every sequence into tiles of 8192 / D tokens.  Reusable for every call with the same shape
- * and lengths, forward and backward, whatever the element type. */
+ * as for kda_plan: prefix sums, required for TND, optional otherwise, every length >= 1).
+ * Reusable for every call with the same shape and lengths, forward and backward, whatever the
+ * element type. */
 KDA_API kda_status_t kda_recurrence_plan_size(const kda_recurrence_shape_t* shape,
                                               const int32_t* cu_seqlens_host, size_t* n_int32);
 KDA_API kda_status_t kda_recurrence_plan(const kda_recurrence_shape_t* shape,
@@ -321,7 +321,8 @@ KDA_API kda_status_t kda_recurrence_plan(const kda_recurrence_shape_t* shape,
 KDA_API kda_status_t kda_recurrence_workspace_size(const int32_t* plan_host, size_t n_int32,
                                                    int32_t backward, size_t* bytes);
 
-/* fp32 values of the `states` buffer: one [N, D] state per tile. */
+/* fp32 values of the `states` buffer: the [N, D] states before every 8192 / D tokens of each
+ * sequence, from its first one. */
 KDA_API kda_status_t kda_recurrence_states_size(const int32_t* plan_host, size_t n_int32,
                                                 size_t* n_floats);
 
@@ -336,8 +337,7 @@ KDA_API kda_status_t kda_recurrence_states_size(const int32_t* plan_host, size_t
  *   out            : dense, x's shape, one rounding to nearest even; rows past a sequence's valid
  *                    length are written as zeros, and the inputs' rows there are never read.
  *   final_state    : fp32 [B, N, D], the unrounded state after each sequence's last token; may be
- *                    initial_state itself (a backward pass then needs a copy of that), must not
- *                    overlap it otherwise.
+ *                    initial_state itself, must not overlap it otherwise.
  * Outputs must not overlap one another or an input (KDA_ERR_ALIAS). */
 KDA_API kda_status_t kda_recurrence_forward(
     const kda_recurrence_shape_t* shape, const int32_t* plan_host, const int32_t* plan_dev,
@@ -351,8 +351,8 @@ KDA_API kda_status_t kda_recurrence_forward(
  *     dx_t = sigmoid(beta_t) lam_t          dbeta_t = sigmoid'(beta_t) sum_d lam_t x_t
  *     dg_t = lam_t h_{t-1} a_t lower_bound sigmoid'(z_t) exp(A_log)   (z_t the sigmoid's argument)
  *     ddt_bias = sum dg_t      dA_log = sum dg_t (g_t + dt_bias)      dinitial_state = a_1 lam_1
- *   states         : as written by kda_recurrence_forward on the same inputs and plan; h is
- *                    recomputed from it in fp32.
+ *   states         : as written by kda_recurrence_forward on the same inputs and plan (the initial
+ *                    state among them); h is recomputed from it in fp32.
  *   dout           : as out (strided allowed), or NULL for zeros;  dfinal_state: fp32 [B, N, D]
  *                    or NULL for zeros.
  *   dx, dg, dbeta  : dense, like x, g, beta; zeros past a valid length.
@@ -362,10 +362,10 @@ KDA_API kda_status_t kda_recurrence_forward(
 KDA_API kda_status_t kda_recurrence_backward(
     const kda_recurrence_shape_t* shape, const int32_t* plan_host, const int32_t* plan_dev,
     size_t n_int32, const kda_view_t* dout, const float* dfinal_state, const kda_view_t* x,
-    const kda_view_t* g, const kda_view_t* beta, const float* initial_state, const float* A_log,
-    const float* dt_bias, float lower_bound, const float* states, void* workspace,
-    size_t workspace_bytes, void* dx, void* dg, void* dbeta, float* dinitial_state,
-    float* dA_log, float* ddt_bias, kda_stream_t stream);
+    const kda_view_t* g, const kda_view_t* beta, const float* A_log, const float* dt_bias,
+    float lower_bound, const float* states, void* workspace, size_t workspace_bytes, void* dx,
+    void* dg, void* dbeta, float* dinitial_state, float* dA_log, float* ddt_bias,
+    kda_stream_t stream);
 
 /* One token of the recurrence for each of B sequences.
  *   x, g: dense [B, N, D];  beta: dense [B, N];  out: dense [B, N, D], all of `dtype`.

@@ -104,12 +104,13 @@ def recurrence(x, g, beta, h0, A_log, dt_bias, lb, layout, lengths, dout=None, d
               + (C + 26 + 8 * (ea * raw).abs()) * U * dg.abs())
         pick(res["dg"][0])[:] = dg
         pick(res["dg"][1])[:] = Eg
-        # sums over tokens: terms' bounds, and 64 roundings on the way (16 rows in order, then the
-        # joins of a tile and of the tiles)
+        # sums over tokens: the terms' bounds, and the roundings on a term's way: 8 tokens in order,
+        # one for each of the walk's steps of at least 64 tokens, 16 threads, 4 channels and 32 lanes
+        K = 64 + n // 64
         res["ddt_bias"][0].add_(dg.sum(0))
-        res["ddt_bias"][1].add_((Eg + 64 * U * dg.abs()).sum(0))
+        res["ddt_bias"][1].add_((Eg + K * U * dg.abs()).sum(0))
         res["dA_log"][0].add_((dg * raw).sum((0, 2)))
-        res["dA_log"][1].add_(((Eg + (64 + 2) * U * dg.abs()) * raw.abs()).sum((0, 2)))
+        res["dA_log"][1].add_(((Eg + (K + 2) * U * dg.abs()) * raw.abs()).sum((0, 2)))
         res["dh0"][0][b] = a[0] * lam[0]
         res["dh0"][1][b] = a[0] * (E[0] + C * U * M[0])
     for name in ("out", "dx", "dg", "dbeta"):

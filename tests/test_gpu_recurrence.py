@@ -248,7 +248,7 @@ def test_another_plan_on_the_device_is_reported(cuda_ok):
     """A device copy that is not the host plan's: nothing is computed and the status says so."""
     d = make("TND", [100, 30], 2, 64, BF, seed=14)
     plan = d["plan"]
-    plan.dev[15] += 1
+    plan.dev[23] += 1
     ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
     kda.gated_recurrence(*args(d, -5.0, "TND"), workspace=ws)
     with pytest.raises(kda.KdaError) as e:

@@ -59,37 +59,27 @@ def test_recurrence_lengths(L, layout, B, S, cu, code):
 @pytest.mark.parametrize("D", [128, 64])
 @pytest.mark.parametrize("layout,S,lengths", [
     (2, None, [1]), (2, None, [130, 1, 700, 64, 65, 63]), (1, 300, [300, 1, 128]), (0, 129, [129, 64])])
-def test_tiles_cover_every_row_once(L, D, layout, S, lengths):
+def test_plan_records(L, D, layout, S, lengths):
+    """Sequences longest first, ties in order, with their rows and their places in the states; the
+    steps of clusters of 1, 2, 4 and 8 blocks."""
     cu = np.concatenate([[0], np.cumsum(lengths)])
     S = S or int(cu[-1])
     st, p = rec_plan(L, rec_shape(layout=layout, B=len(lengths), S=S, D=D), cu)
     assert st == 0
-    R, chain, rec = 8192 // D, int(p[5]), p[16:].reshape(-1, 8)
-    assert int(p[4]) == len(rec) and int(p[12]) == R
-    assert int(p[11]) == max(-(-n // R) for n in lengths)
-    rows = np.zeros((1 if layout == 2 else len(lengths), S), dtype=int)
-    valid = np.zeros_like(rows)
-    seen = {}
-    for i, (slot, row0, n, store, index, tile, count, *_) in enumerate(rec.tolist()):
-        at = 0 if layout == 2 else slot
-        rows[at, row0:row0 + store] += 1
-        valid[at, row0:row0 + n] += 1
-        assert (n > 0) == (i < chain) and n <= store <= R and row0 + store <= S
-        if n:
-            # predecessors come first, at the place before this one
-            assert tile == 0 or seen[(slot, tile - 1)] == index - 1
-            seen[(slot, tile)] = index
-            assert count == -(-lengths[slot] // R)
-            assert row0 == (int(cu[slot]) if layout == 2 else 0) + tile * R
-    assert (rows == 1).all()
-    assert sorted(seen.values()) == list(range(chain))
-    for b, n in enumerate(lengths):
-        lo = int(cu[b]) if layout == 2 else 0
-        assert (valid[0 if layout == 2 else b, lo:lo + n] == 1).all()
-    assert valid.sum() == sum(lengths)
+    R, rec = 8192 // D, p[24:].reshape(-1, 4).tolist()
+    tiles = lambda n: -(-n // R)  # noqa: E731
+    order = sorted(range(len(lengths)), key=lambda b: -lengths[b])
+    base = 0
+    for (slot, start, n, at), b in zip(rec, order, strict=True):
+        assert (slot, start, n, at) == (b, int(cu[b]) if layout == 2 else 0, lengths[b], base)
+        base += tiles(n)
+    assert int(p[10]) == base
+    walked = [tiles(n if layout == 2 else S) for n in lengths]
+    assert int(p[11]) == max(walked)
+    assert p[12:16].tolist() == [sum(-(-t // c) for t in walked) for c in (1, 2, 4, 8)]
     floats = ctypes.c_size_t(0)
     assert L.kda_recurrence_states_size(p.ctypes.data_as(P_I32), p.size, ctypes.byref(floats)) == 0
-    assert floats.value == chain * 3 * D
+    assert floats.value == base * 3 * D
 
 
 def test_recurrence_plan_capacity_and_corruption(L):
@@ -100,7 +90,7 @@ def test_recurrence_plan_capacity_and_corruption(L):
         a.ctypes.data_as(P_I32), a.size if k is None else k, 0, ctypes.byref(n))
     assert ok(p) == 0 and n.value >= 256
     assert ok(p, p.size - 1) == PLAN and ok(p, 3) == PLAN
-    for word in (0, 4, 5, 11, 14, 15):
+    for word in (0, 4, 5, 10, 11, 12, 16, 23):
         bad = p.copy()
         bad[word] += 1
         assert ok(bad) == PLAN, word
@@ -133,8 +123,8 @@ def rec_call(L, p, shape, backward=False, **over):
     head = (ctypes.byref(shape), p.ctypes.data_as(P_I32), a["plan_dev"], p.size)
     if backward:
         return L.kda_recurrence_backward(
-            *head, v["dout"], a["dfinal"], v["x"], v["g"], v["beta"], a["h0"], a["A"], a["bias"],
-            a["lb"], a["states"], a["ws"], a["ws_bytes"], a["dx"], a["dg"], a["dbeta"], a["dh0"],
+            *head, v["dout"], a["dfinal"], v["x"], v["g"], v["beta"], a["A"], a["bias"], a["lb"],
+            a["states"], a["ws"], a["ws_bytes"], a["dx"], a["dg"], a["dbeta"], a["dh0"],
             a["dA"], a["dbias"], None)
     return L.kda_recurrence_forward(
         *head, v["x"], v["g"], v["beta"], a["h0"], a["A"], a["bias"], a["lb"], a["states"], a["ws"],
@@ -161,7 +151,7 @@ def test_recurrence_argument_checks(L):
         assert c(x=(0x10000000, -row[0], row[1], row[2])) == SHAPE      # negative stride
         assert c(x=(0x10000000, 1 << 60, row[1], row[2])) == SHAPE
         assert c(beta=(0x30000001, 900, 1, 3)) == ALIGN
-        assert c(h0=0x40000004) == ALIGN
+        assert backward or c(h0=0x40000004) == ALIGN
         name = "dx" if backward else "out"
         assert c(**{name: 0x10000000 + 256}) == ALIAS                    # an input
         assert c(**{name: 0x10000000 - nbytes + 16}) == ALIAS
