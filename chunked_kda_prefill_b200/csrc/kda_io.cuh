@@ -7,7 +7,11 @@
 
 #include <cstdint>
 
+#include "kda_sm100.cuh"
+
 namespace kda {
+
+using namespace sm100;
 
 // 4 consecutive channels as they lie in memory (8 bytes, or 16 for fp32)
 template <class T>
@@ -70,11 +74,6 @@ __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2hal
 template <>
 __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -101,40 +100,128 @@ __device__ __forceinline__ float gate_sigmoid(const GateScale& c, float raw, flo
 }
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
-// 4 channels as two pairs, for the packed fp32 instructions
-struct F4 {
-  float2 lo, hi;
+// 2 P consecutive channels in pairs, for the packed fp32 instructions
+template <int P>
+struct Pairs {
+  float2 v[P];
 };
-__device__ __forceinline__ F4 splat(float v) { return {make_float2(v, v), make_float2(v, v)}; }
-__device__ __forceinline__ F4 f4(const float (&x)[4]) {
-  return {make_float2(x[0], x[1]), make_float2(x[2], x[3])};
+template <int P>
+__device__ __forceinline__ Pairs<P> splat(float x) {
+  Pairs<P> r;
+#pragma unroll
+  for (int i = 0; i < P; ++i) r.v[i] = make_float2(x, x);
+  return r;
 }
-__device__ __forceinline__ F4 f4(float4 x) { return {make_float2(x.x, x.y), make_float2(x.z, x.w)}; }
-__device__ __forceinline__ F4 operator+(F4 a, F4 b) {
-  return {__fadd2_rn(a.lo, b.lo), __fadd2_rn(a.hi, b.hi)};
+template <int P>
+__device__ __forceinline__ Pairs<P> operator+(Pairs<P> a, Pairs<P> b) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) a.v[i] = __fadd2_rn(a.v[i], b.v[i]);
+  return a;
 }
-__device__ __forceinline__ F4 operator*(F4 a, F4 b) {
-  return {__fmul2_rn(a.lo, b.lo), __fmul2_rn(a.hi, b.hi)};
+template <int P>
+__device__ __forceinline__ Pairs<P> operator*(Pairs<P> a, Pairs<P> b) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) a.v[i] = __fmul2_rn(a.v[i], b.v[i]);
+  return a;
 }
-__device__ __forceinline__ F4 fma4(F4 a, F4 b, F4 c) {
-  return {__ffma2_rn(a.lo, b.lo, c.lo), __ffma2_rn(a.hi, b.hi, c.hi)};
+template <int P>
+__device__ __forceinline__ Pairs<P> operator*(Pairs<P> a, float b) {
+  return a * splat<P>(b);
 }
-template <class F>
-__device__ __forceinline__ F4 each(F4 a, F&& f) {
-  return {make_float2(f(a.lo.x), f(a.lo.y)), make_float2(f(a.hi.x), f(a.hi.y))};
+template <int P>
+__device__ __forceinline__ Pairs<P> fma(Pairs<P> a, Pairs<P> b, Pairs<P> c) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) c.v[i] = __ffma2_rn(a.v[i], b.v[i], c.v[i]);
+  return c;
 }
-__device__ __forceinline__ F4 lds4(const float* p) { return f4(*reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ void sts4(float* p, F4 v) {
-  *reinterpret_cast<float4*>(p) = make_float4(v.lo.x, v.lo.y, v.hi.x, v.hi.y);
+template <int P, class F>
+__device__ __forceinline__ Pairs<P> each(Pairs<P> a, F&& f) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) a.v[i] = make_float2(f(a.v[i].x), f(a.v[i].y));
+  return a;
 }
-// memory that other blocks write
-__device__ __forceinline__ F4 ldcg4(const float* p) {
-  return f4(__ldcg(reinterpret_cast<const float4*>(p)));
+template <int P>
+__device__ __forceinline__ float sum(Pairs<P> a) {
+  float2 s = a.v[0];
+#pragma unroll
+  for (int i = 1; i < P; ++i) s = __fadd2_rn(s, a.v[i]);
+  return s.x + s.y;
 }
-template <class T>
-__device__ __forceinline__ void st4(T* p, F4 v) {
-  const float x[4] = {v.lo.x, v.lo.y, v.hi.x, v.hi.y};
-  st4(p, x);
+
+// V consecutive channels as they lie in memory: 4, 8 or 16 bytes
+template <int BYTES>
+struct BitsOf;
+template <>
+struct BitsOf<4> {
+  using type = uint32_t;
+};
+template <>
+struct BitsOf<8> {
+  using type = uint2;
+};
+template <>
+struct BitsOf<16> {
+  using type = uint4;
+};
+template <class T, int V>
+using Bits = typename BitsOf<V * (int)sizeof(T)>::type;
+
+__device__ __forceinline__ float2 widen2(uint32_t w, __nv_bfloat16) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ float2 widen2(uint32_t w, __half) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <class T, int V>
+__device__ __forceinline__ Pairs<V / 2> widen(Bits<T, V> w) {
+  Pairs<V / 2> r;
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (V == 4) {
+      r.v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+      r.v[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+    } else {
+      r.v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+    }
+  } else if constexpr (V == 4) {
+    r.v[0] = widen2(w.x, T());
+    r.v[1] = widen2(w.y, T());
+  } else {
+    r.v[0] = widen2(w, T());
+  }
+  return r;
+}
+// rounded to nearest even
+__device__ __forceinline__ uint32_t narrow2(float2 a, __nv_bfloat16) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a.x, a.y);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t narrow2(float2 a, __half) {
+  const __half2 r = __floats2half2_rn(a.x, a.y);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+template <class T, int P>
+__device__ __forceinline__ void store(T* p, Pairs<P> a) {
+  Bits<T, 2 * P> w;
+  if constexpr (sizeof(T) == 4 && P == 2) {
+    w = make_uint4(__float_as_uint(a.v[0].x), __float_as_uint(a.v[0].y),
+                   __float_as_uint(a.v[1].x), __float_as_uint(a.v[1].y));
+  } else if constexpr (sizeof(T) == 4) {
+    w = make_uint2(__float_as_uint(a.v[0].x), __float_as_uint(a.v[0].y));
+  } else if constexpr (P == 2) {
+    w = make_uint2(narrow2(a.v[0], T()), narrow2(a.v[1], T()));
+  } else {
+    w = narrow2(a.v[0], T());
+  }
+  *reinterpret_cast<Bits<T, 2 * P>*>(p) = w;
+}
+template <int P, class T>
+__device__ __forceinline__ Pairs<P> load(const T* p) {
+  return widen<T, 2 * P>(*reinterpret_cast<const Bits<T, 2 * P>*>(p));
+}
+// through the read-only path: nothing on the device writes it meanwhile
+template <int P, class T>
+__device__ __forceinline__ Pairs<P> load_const(const T* p) {
+  return widen<T, 2 * P>(__ldg(reinterpret_cast<const Bits<T, 2 * P>*>(p)));
 }
 
 }  // namespace kda

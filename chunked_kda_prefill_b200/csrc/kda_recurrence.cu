@@ -1,13 +1,17 @@
 // kda_recurrence.cu -- the gated recurrence, the vector form of the KDA state:
 //     a_t = exp(lb sigmoid(e^A (g_t + bias))),  h_t = a_t h_{t-1} + sigmoid(beta_t) x_t.
 //
-// A run of tokens maps its start state to its end state by h -> A h + H, with A the product of its
-// decays, and such maps compose.  A cluster of 1 to 8 blocks walks one (sequence, head) from its
-// start (the backward pass from its end), a tile of 8192 values per block and step; a thread has 8
-// tokens of 4 channels.  In a step every thread forms its tokens' map, the block composes its
-// threads' maps and the cluster its blocks', through shared memory, and with the state before its
-// tokens a thread runs through them once more from registers and writes.  The data is read once.
-// Which block does what is fixed by the plan and the launch, so the same call gives the same bits.
+// A ring of warps walks one segment (a sequence, or a part of a long one) of one head, a tile of
+// 1024 values a warp at a time: the warp's own copies bring its next tiles to shared memory, it
+// forms all decays and writes of its tile, waits for the state that the warp before it leaves,
+// runs through its 8 or 16 tokens, passes the state on and only then writes its results.  So what
+// happens one after another is a wait, 8 or 16 fused multiply-adds and a hand-over (about 150 ns
+// for 1024 values), the rest runs side by side, and no barrier stops a block.  The backward pass
+// is the same walk from the end with the state's gradient, the states before the tiles given.
+//
+// Where a few long sequences would leave multiprocessors idle, the plan cuts them.  A kernel before
+// the walk then forms the map h -> A h + H of each segment, and a segment starts from the maps
+// before it.
 //
 // Both passes are bound by HBM: 6 bytes a value forward (16-bit), 10 backward.
 #include <cuda_runtime.h>
@@ -16,6 +20,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 #include <type_traits>
 
 #include "kda_args.h"
@@ -26,30 +31,28 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRows = 8;  // tokens of a thread, 4 channels each
+constexpr uint32_t kWaitLimit = 1u << 26;
 
 struct RecParams {
   kda_view_t x, g, beta, dout;  // device addresses and strides
   const int32_t* plan;
   int32_t checksum;
-  int32_t N, units;
+  int32_t N, units;   // units: segments times heads
   int32_t slot_rows;  // rows that a slot's outputs have, padding included; 0 for packed rows
-  int32_t cluster;
-  const float* h0;
+  int32_t ring;       // warps of a ring
+  const float* begin;  // [B][N][D] the walk's start (forward h0, backward dfinal), or null for zeros
   const float* A_log;
   const float* dt_bias;
   float lower_bound;
-  const float* dfinal;
   int32_t* status;
+  float* maps;    // [RH_MAPS][N][2][D] of the cut sequences
   float* states;  // [tiles][N][D] the states before the tiles: forward writes, backward reads
   void* out;      // forward: out; backward: dx
   void* dg;
   void* dbeta;
-  float* final_state;
-  float* dh0;
-  float* part_bias;   // [B][cluster][N][D]
-  float* part_A;      // [B][cluster][N]
+  float* end;        // [B][N][D] the walk's end: final_state, or dh0 (null: not wanted)
+  float* part_bias;  // [RH_PARTS][N][D]
+  float* part_A;     // [RH_PARTS][N]
   kda_view_t od, bd;  // strides of the dense outputs with and without channels
 };
 
@@ -58,89 +61,43 @@ __device__ __forceinline__ const T* at(const kda_view_t& v, long long b, long lo
   return static_cast<const T*>(v.data) + b * v.stride_b + n * v.stride_n + s * v.stride_s;
 }
 
-// Which 4 channels and 8 tokens of a tile a thread has.
+// A lane's channels and a tile's tokens.
 template <int D>
-struct Place {
-  static constexpr int kLanes = D / 4;
-  static constexpr int kGroups = kThreads / kLanes;
-  static constexpr int kTile = kGroups * kRows;
-  static_assert(kTile == rec_tile_rows(D), "a tile is the block's threads by their tokens");
-  int chan, group, r0;
-  __device__ Place()
-      : chan((threadIdx.x % kLanes) * 4), group(threadIdx.x / kLanes), r0(group * kRows) {}
+struct Shape {
+  static constexpr int V = D / 32;          // channels of a lane
+  static constexpr int K = kRecTileElems / D;  // tokens of a tile
+  using F = Pairs<V / 2>;
 };
 
-// One (sequence, head) of the walk.
-struct Unit {
-  int slot, start, len, base;  // the plan's record
-  int n, steps;
-  int place;  // of the sequence in the plan
+// Warps of a block, one block a multiprocessor, and the tiles whose copies a warp has under way or at
+// work: as many as the registers (forward 128 a thread, backward 168) and shared memory allow.
+template <class T, bool BACKWARD>
+struct Block {
+  static constexpr int kWarps = sizeof(T) == 4 ? 8 : BACKWARD ? 12 : 16;
+  static constexpr int kStages = BACKWARD ? 2 : 3;
+  static constexpr int kTensors = BACKWARD ? 3 : 2;
 };
+template <class T, int D, bool BACKWARD>
+constexpr int kStageBytes =
+    Block<T, BACKWARD>::kTensors * kRecTileElems * (int)sizeof(T) + (BACKWARD ? D * 4 : 0);
+template <class T, int D, bool BACKWARD>
+constexpr int kWalkSmem =
+    Block<T, BACKWARD>::kWarps * Block<T, BACKWARD>::kStages * kStageBytes<T, D, BACKWARD>;
 
-// A block's walk: units in rounds over the clusters, every other round in reverse, so that with the
-// plan's order (longest first) no cluster gets the longer unit of every round.  The record of the
-// unit after the current one is requested a unit ahead.
-struct Walk {
-  Unit u;
-  int step, round;
-  int4 ahead;
-
-  __device__ static int index(const RecParams& p, int round) {
-    const int clusters = gridDim.x / p.cluster, q = blockIdx.x / p.cluster;
-    const long long i = (long long)round * clusters + (round & 1 ? clusters - 1 - q : q);
-    return i < p.units ? (int)i : -1;
-  }
-  __device__ static int4 record(const RecParams& p, int round) {
-    const int i = index(p, round);
-    const int4* rec = reinterpret_cast<const int4*>(p.plan + kRecHeader);
-    return i < 0 ? make_int4(0, 0, 0, 0) : __ldg(rec + i / p.N);
-  }
-  template <int R>
-  __device__ void enter(const RecParams& p) {
-    const int i = index(p, round);
-    u.slot = ahead.x;
-    u.start = ahead.y;
-    u.len = ahead.z;
-    u.base = ahead.w;
-    u.place = i < 0 ? -1 : i / p.N;
-    u.n = i < 0 ? -1 : i - u.place * p.N;
-    const int rows = p.slot_rows ? p.slot_rows : u.len;
-    u.steps = ((rows - 1) / R) / p.cluster + 1;
-    step = 0;
-    ahead = record(p, round + 1);
-  }
-  template <int R>
-  __device__ void begin(const RecParams& p) {
-    round = 0;
-    ahead = record(p, 0);
-    enter<R>(p);
-  }
-  template <int R>
-  __device__ void next(const RecParams& p) {
-    if (++step < u.steps) return;
-    ++round;
-    enter<R>(p);
-  }
-  __device__ bool done() const { return u.n < 0; }
+// A tile as its copies' issuer describes it to the same warp later.
+struct __align__(16) Tile {
+  int slot, row, valid, place;  // row: of its first token; place: of its state
+  int n, flags, map, part;
 };
-
-// A block's tile in a step: its first row within the sequence, its rows with tokens, and whether any
-// block of the cluster has such rows.
-struct Tile {
-  int row, valid, index;
-  bool work;
+enum : int {
+  kFresh = 1,   // the warp's first tile in the unit
+  kFirst = 2,   // the segment's first tile of the walk
+  kLast = 4,    // the segment's last tile of the walk
+  kBegin = 8,   // of the segment that the walk of the sequence begins with
+  kEnd = 16,    // of the segment that it ends with
+  kCut = 32,    // of a cut sequence
+  kOrder = 6    // flags >> kOrder: the segment's place in the walk of its sequence
 };
-template <int R, bool BACKWARD>
-__device__ __forceinline__ Tile tile_of(const RecParams& p, const Walk& w, int rank) {
-  Tile t;
-  const int first = (BACKWARD ? w.u.steps - 1 - w.step : w.step) * p.cluster;
-  t.index = first + rank;
-  // the cluster's last tiles may lie behind the slot, and behind 32 bits
-  t.row = (int)min((long long)t.index * R, (long long)INT_MAX);
-  t.valid = max(0, min(R, w.u.len - t.row));
-  t.work = (long long)first * R < w.u.len;
-  return t;
-}
 
 // Whether the plan on the device is the host's; block 0 leaves the status.
 __device__ __forceinline__ bool same_plan(const RecParams& p) {
@@ -149,235 +106,270 @@ __device__ __forceinline__ bool same_plan(const RecParams& p) {
   return same;
 }
 
-// ---- clusters ----
-__device__ __forceinline__ void cluster_arrive() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  __syncwarp();
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// 4 floats at this block's shared address `p` in the block of another rank
-__device__ __forceinline__ F4 ld_rank(const float* p, int rank) {
-  uint32_t addr = (uint32_t)__cvta_generic_to_shared(p), far;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(far) : "r"(addr), "r"(rank));
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(far)
-               : "memory");
-  return f4(v);
+__device__ __forceinline__ const int4* record(const RecParams& p, int i) {
+  return reinterpret_cast<const int4*>(p.plan + kRecHeader) + 2 * i;
 }
 
-// ---- loads ----
-// 4 channels from global to the thread's own place in shared memory
-template <class T>
-__device__ __forceinline__ void copy_async(T* to, const T* from) {
-  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
-  if constexpr (sizeof(T) == 2)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(from));
-  else
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from));
-}
-template <class T>
-__device__ __forceinline__ F4 own4(const T* p) {
-  Vec4<T> v;
-  v.w = *reinterpret_cast<const decltype(v.w)*>(p);
-  float x[4];
-  widen(v, x);
-  return f4(x);
-}
+// A warp's way through the tiles of its ring's units.  The units are dealt to the blocks in rounds,
+// every other one in reverse, so that with the plan's order (longest first) no block gets the longer
+// unit of every round; a block's rings take its rounds in turn.
+template <int K, bool BACKWARD>
+struct Walk {
+  int4 r0, r1;  // the record: slot, start, len, tile; part, segment, segments, map
+  int n, t, tiles, round;
+  bool fresh, done;
 
-// Starts the loads of the thread's tokens of one tensor; every thread reads only what it copied
-// itself.  Behind the last token the channels are zeros, or -inf where they are gates: sigmoid and
-// write are then zero and the decay one, so those rows change no map.
-template <class T, int D>
-__device__ __forceinline__ void request(T* to, const kda_view_t& v, const Unit& u, const Tile& t,
-                                        const Place<D>& me, bool gate) {
-  const T* from = at<T>(v, u.slot, u.n, (long long)u.start + t.row + me.r0) + me.chan;
-  T* dst = to + me.r0 * D + me.chan;
-  const int mine = t.valid - me.r0;
-#pragma unroll
-  for (int k = 0; k < kRows; ++k) {
-    if (k < mine) {
-      copy_async(dst + k * D, from);
-      from += v.stride_s;
-    } else {
-      st4(dst + k * D, splat(gate ? -INFINITY : 0.f));
+  // zero(slot, n, row, rows): called for the rows behind a sequence's last token
+  template <class Zero>
+  __device__ void enter(const RecParams& p, int rings, Zero&& zero) {
+    for (;; round += rings) {
+      const long long base = (long long)round * gridDim.x;
+      const long long unit = base + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      done = unit >= p.units;
+      if (done) return;
+      const int i = (int)unit / p.N;
+      n = (int)unit - i * p.N;
+      r0 = __ldg(record(p, i));
+      r1 = __ldg(record(p, i) + 1);
+      tiles = (r0.z + K - 1) / K;
+      fresh = true;
+      if (p.slot_rows && r1.y + 1 == r1.z) zero(r0.x, n, r0.y + r0.z, p.slot_rows - r0.y - r0.z);
+      if (t < tiles) return;
+      t -= tiles;
     }
   }
-}
-// The write logits of a tile, one a thread.
-template <class T>
-__device__ __forceinline__ float request_beta(const RecParams& p, const Unit& u, const Tile& t) {
-  const int r = threadIdx.x;
-  return r < t.valid ? to_f32(*at<T>(p.beta, u.slot, u.n, (long long)u.start + t.row + r)) : 0.f;
+  template <class Zero>
+  __device__ void next(const RecParams& p, int rings, Zero&& zero) {
+    fresh = false;
+    t += p.ring;
+    if (t < tiles) return;
+    t -= tiles;
+    round += rings;
+    enter(p, rings, zero);
+  }
+  __device__ Tile tile(int* valid) const {
+    const int k = BACKWARD ? tiles - 1 - t : t;
+    const int order = BACKWARD ? r1.z - 1 - r1.y : r1.y;
+    *valid = min(K, r0.z - k * K);
+    return {r0.x, r0.y + k * K, *valid, r0.w + k, n,
+            (fresh ? kFresh : 0) | (t == 0 ? kFirst : 0) | (t == tiles - 1 ? kLast : 0) |
+                (order == 0 ? kBegin : 0) | (order == r1.z - 1 ? kEnd : 0) |
+                (r1.z > 1 ? kCut : 0) | order << kOrder,
+            r1.w, r1.x + t};
+  }
+};
+
+// Starts the copies of a tile's rows of one tensor, a row a lane or, where the rows lie side by side,
+// all rows at once.
+template <class T, int D>
+__device__ __forceinline__ void copy_rows(uint32_t dst, const kda_view_t& v, const Tile& t,
+                                          int first_lane, int lane, uint32_t bar) {
+  const int k = lane - first_lane;
+  if (k < 0 || k >= t.valid) return;
+  const T* from = at<T>(v, t.slot, t.n, t.row);
+  if (v.stride_s == D) {
+    if (k == 0) bulk_load(dst, from, t.valid * D * (int)sizeof(T), bar);
+  } else {
+    bulk_load(dst + k * D * (int)sizeof(T), from + k * v.stride_s, D * (int)sizeof(T), bar);
+  }
 }
 
-// Two stages of shared memory for the tile at work and the next one; fp32 tiles have one, so that
-// two blocks still fit an SM.
-template <class T>
-constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
-
-template <class T, int D>
-constexpr int forward_smem() {
-  return kStages<T> * 2 * kRecTileElems * (int)sizeof(T);
+// The state that a cut segment starts from: the maps of those before it in the walk's order, the
+// first of which is constant.
+template <int D>
+__device__ typename Shape<D>::F join(const RecParams& p, int map, int order, int n, int chan) {
+  constexpr int P = Shape<D>::V / 2;
+  auto s = splat<P>(0.f);
+  const float* m = p.maps + ((size_t)map * p.N + n) * 2 * D + chan;
+#pragma unroll 4
+  for (int k = 0; k <= order; ++k) {
+    s = fma(load<P>(m), s, load<P>(m + D));
+    m += (size_t)p.N * 2 * D;
+  }
+  return s;
 }
-template <class T, int D>
-constexpr int backward_smem() {
-  return kStages<T> * 3 * kRecTileElems * (int)sizeof(T);
-}
 
-template <class T, int D>
-__global__ void __launch_bounds__(kThreads, 2) rec_forward_kernel(const RecParams p) {
-  using P = Place<D>;
-  constexpr int R = P::kTile;
-  extern __shared__ __align__(16) unsigned char raw_smem[];
-  T* const stage = reinterpret_cast<T*>(raw_smem);  // [kStages][g, x][R][D]
-  __shared__ float sb[2][R];
-  __shared__ __align__(16) float sa[2][P::kGroups][D], sh[2][P::kGroups][D];
-  __shared__ __align__(16) float map_a[2][D], map_h[2][D], carry_in[D], carry_out[D];
-  if (!same_plan(p)) return;
-  const P me;
-  const int rank = blockIdx.x % p.cluster;
-  Walk now, next;
-  now.begin<R>(p);
-  next = now;
-  F4 h0_next = splat(0.f);
-  float beta = 0.f;
-  // the loads of `next`'s tile, and its start state where a unit begins
-  auto start = [&](int i) {
-    if (!next.done()) {
-      const Tile t = tile_of<R, false>(p, next, rank);
-      T* to = stage + (i % kStages<T>) * 2 * kRecTileElems;
-      if (t.work) {
-        request(to, p.g, next.u, t, me, true);
-        request(to + kRecTileElems, p.x, next.u, t, me, false);
-      }
-      beta = request_beta<T>(p, next.u, t);
-      if (next.step == 0) {
-        h0_next = splat(0.f);
-        if (p.h0)
-          h0_next = f4(*reinterpret_cast<const float4*>(
-              p.h0 + ((size_t)next.u.slot * p.N + next.u.n) * D + me.chan));
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  start(0);
-  if (threadIdx.x < R) sb[0][threadIdx.x] = sigmoid(beta);
+// What every warp of a walk sets up, and its waits.
+template <int STAGES>
+struct Lines {
+  uint32_t full, mine, theirs;  // barriers: a stage is loaded; this warp's turn, the next one's
+  float* inbox;                 // the state handed to this warp, and to the next one
+  float* outbox;
+  bool failed;
+  __device__ void wait(uint32_t bar, uint32_t phase) {
+    if (!failed && !mbar_wait_bounded(bar, phase & 1, kWaitLimit)) failed = true;
+  }
+};
+
+template <class T, int D, bool BACKWARD>
+__device__ __forceinline__ Lines<Block<T, BACKWARD>::kStages> lines(const RecParams& p, int warp,
+                                                                    int lane) {
+  using B = Block<T, BACKWARD>;
+  __shared__ uint64_t full[B::kWarps][B::kStages], turn[B::kWarps];
+  __shared__ __align__(16) float box[B::kWarps][D];
+  const int place = warp % p.ring, after = warp - place + (place + 1) % p.ring;
+  Lines<B::kStages> l;
+  l.full = smem_u32(full[warp]);
+  l.mine = smem_u32(&turn[warp]);
+  l.theirs = smem_u32(&turn[after]);
+  l.inbox = box[warp];
+  l.outbox = box[after];
+  l.failed = false;
+  if (lane == 0) {
+    for (int s = 0; s < B::kStages; ++s) mbar_init(l.full + 8 * s, 1);
+    mbar_init(l.mine, 1);
+    fence_barrier_init();
+  }
   __syncthreads();
-  F4 carry = splat(0.f);
-  for (int i = 0; !now.done(); ++i) {
-    const int buf = i & 1;
-    const Tile t = tile_of<R, false>(p, now, rank);
-    if (now.step == 0) carry = h0_next;
-    next.next<R>(p);
-    if (kStages<T> == 2) start(i + 1);
-    const T* const tg = stage + (i % kStages<T>) * 2 * kRecTileElems + me.r0 * D + me.chan;
-    const T* const tx = tg + kRecTileElems;
-    const GateScale gc = gate_scale(__ldg(p.A_log + now.u.n), p.lower_bound);
-    const F4 bias =
-        f4(__ldg(reinterpret_cast<const float4*>(p.dt_bias + (size_t)now.u.n * D + me.chan)));
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages<T> - 1) : "memory");
-
-    // the thread's own tokens: decays, writes and the map
-    F4 a[kRows], u[kRows], pa = splat(1.f), ph = splat(0.f);
-    if (t.work) {
-      const F4 nz = splat(gc.nz), l2 = splat(gc.l2), one = splat(1.f);
-#pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const F4 e = each((own4(tg + k * D) + bias) * nz, ex2);
-        a[k] = each(each(e + one, rcp) * l2, ex2);
-        u[k] = own4(tx + k * D) * splat(sb[buf][me.r0 + k]);
-        pa = pa * a[k];
-        ph = fma4(a[k], ph, u[k]);
-      }
-      sts4(&sa[buf][me.group][me.chan], pa);
-      sts4(&sh[buf][me.group][me.chan], ph);
-    }
-    if (kStages<T> == 1) start(i + 1);
-    if (threadIdx.x < R) sb[buf ^ 1][threadIdx.x] = sigmoid(beta);
-    __syncthreads();
-    F4 h = carry;
-    if (t.work) {
-      if (p.cluster == 1) {
-        for (int k = 0; k < P::kGroups; ++k) {
-          if (k == me.group) h = carry;
-          carry = fma4(lds4(&sa[buf][k][me.chan]), carry, lds4(&sh[buf][k][me.chan]));
-        }
-      } else {
-        // the block's map, for the other ranks; the map before the thread's own tokens meanwhile
-        if (threadIdx.x < P::kLanes) {
-          F4 ta = splat(1.f), th = splat(0.f);
-          for (int k = 0; k < P::kGroups; ++k) {
-            const F4 ka = lds4(&sa[buf][k][me.chan]);
-            ta = ta * ka;
-            th = fma4(ka, th, lds4(&sh[buf][k][me.chan]));
-          }
-          sts4(&map_a[buf][me.chan], ta);
-          sts4(&map_h[buf][me.chan], th);
-        }
-        cluster_arrive();
-        F4 qa = splat(1.f), qh = splat(0.f);
-        for (int k = 0; k < me.group; ++k) {
-          const F4 ka = lds4(&sa[buf][k][me.chan]);
-          qa = qa * ka;
-          qh = fma4(ka, qh, lds4(&sh[buf][k][me.chan]));
-        }
-        cluster_wait();
-        if (threadIdx.x < P::kLanes) {
-          for (int r = 0; r < p.cluster; ++r) {
-            if (r == rank) sts4(&carry_in[me.chan], carry);
-            carry = fma4(ld_rank(&map_a[buf][me.chan], r), carry, ld_rank(&map_h[buf][me.chan], r));
-          }
-          sts4(&carry_out[me.chan], carry);
-        }
-        __syncthreads();
-        h = lds4(&carry_in[me.chan]);
-        carry = lds4(&carry_out[me.chan]);
-        if (me.group == 0 && p.states && t.valid > 0)
-          sts4(p.states + ((size_t)(now.u.base + t.index) * p.N + now.u.n) * D + me.chan, h);
-        h = fma4(qa, h, qh);
-      }
-    }
-    if (p.cluster == 1 && me.group == 0 && p.states && t.valid > 0)
-      sts4(p.states + ((size_t)(now.u.base + t.index) * p.N + now.u.n) * D + me.chan, h);
-    // the outputs, and zeros behind the last token
-    {
-      const int rows = p.slot_rows ? min(R, p.slot_rows - t.row) : t.valid;
-      T* out = static_cast<T*>(p.out) + (long long)now.u.slot * p.od.stride_b +
-               (long long)now.u.n * p.od.stride_n +
-               ((long long)now.u.start + t.row + me.r0) * p.od.stride_s + me.chan;
-#pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        if (t.work) h = fma4(a[k], h, u[k]);
-        if (me.r0 + k < rows) st4(out, me.r0 + k < t.valid ? h : splat(0.f));
-        out += p.od.stride_s;
-      }
-    }
-    if (rank == 0 && me.group == 0 && now.step + 1 == now.u.steps)
-      sts4(p.final_state + ((size_t)now.u.slot * p.N + now.u.n) * D + me.chan, carry);
-    now = next;
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  if (p.cluster > 1) {  // no block leaves while another reads its map
-    cluster_arrive();
-    cluster_wait();
-  }
+  return l;
 }
 
-// Sums of 8 values over the LANES lanes of a group, by halving the values as the distance halves:
-// lane i of every LANES / 8 ends with the sum of value i * 8 / LANES.
-template <int LANES>
-__device__ __forceinline__ float group_sum8(float (&v)[8], int lane) {
-  int n = 8, o = LANES / 2;
+// A wait has run out: says so, and stays until the copies under way have ended.
+template <int STAGES>
+__device__ __noinline__ void give_up(const RecParams& p, const Lines<STAGES>& l, const Tile* tiles,
+                                     uint32_t i, int lane) {
+  if (lane == 0) atomicExch(p.status, DS_TIMEOUT);
+  for (uint32_t j = i; j < i + STAGES; ++j)
+    if (tiles[j % STAGES].valid)
+      mbar_wait_bounded(l.full + 8 * (j % STAGES), (j / STAGES) & 1, kWaitLimit);
+}
+
+// Rows of a partial tile that hold no token: closed gates (decay one) and zero writes.
+template <class T, int D, int TENSORS>
+__device__ __noinline__ void fill_rows(T* stage, int valid) {
+  using S = Shape<D>;
+  const int chan = (threadIdx.x & 31) * S::V;
+  for (int k = valid; k < S::K; ++k)
+    for (int i = 0; i < TENSORS; ++i)
+      store(stage + i * kRecTileElems + k * D + chan, splat<S::V / 2>(i == 0 ? -INFINITY : 0.f));
+  fence_proxy_async_smem();  // a later copy writes these rows too
+}
+
+template <class T, int D>
+__global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
+    rec_forward_kernel(const __grid_constant__ RecParams p) {
+  using B = Block<T, false>;
+  using S = Shape<D>;
+  using F = typename S::F;
+  constexpr int K = S::K, V = S::V, P = V / 2, kStages = B::kStages;
+  constexpr int kStage = kStageBytes<T, D, false>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Tile tiles[B::kWarps][kStages];
+  if (!same_plan(p)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
+  const int rings = B::kWarps / p.ring;
+  auto l = lines<T, D, false>(p, warp, lane);
+  uint8_t* const stages = smem + warp * kStages * kStage;
+  T* const out = static_cast<T*>(p.out);
+  const long long orow = p.od.stride_s;
+
+  Walk<K, false> walk;
+  auto zero = [&](int slot, int n, int row, int rows) {
+    T* o = out + slot * p.od.stride_b + n * p.od.stride_n + row * orow + chan;
+    for (int k = warp % p.ring; k < rows; k += p.ring) store(o + k * orow, splat<P>(0.f));
+  };
+  walk.round = warp / p.ring;
+  walk.t = warp % p.ring;
+  walk.enter(p, rings, zero);
+  // the copies of the next tile of the way; returns the lane's write logit of that tile
+  auto issue = [&](int s) {
+    __syncwarp();  // all lanes have read what the stage held
+    float logit = 0.f;
+    if (walk.done) {
+      if (lane == 0) tiles[warp][s].valid = 0;
+    } else {
+      int valid;
+      const Tile t = walk.tile(&valid);
+      const uint32_t bar = l.full + 8 * s, dst = smem_u32(stages + s * kStage);
+      if (lane == 0) {
+        tiles[warp][s] = t;
+        mbar_arrive_expect_tx(bar, 2 * valid * D * (int)sizeof(T));
+      }
+      __syncwarp();
+      copy_rows<T, D>(dst, p.g, t, 0, lane, bar);
+      copy_rows<T, D>(dst + kRecTileElems * sizeof(T), p.x, t, 16, lane, bar);
+      if (lane < valid) logit = to_f32(__ldg(at<T>(p.beta, t.slot, t.n, t.row + lane)));
+      walk.next(p, rings, zero);
+    }
+    return logit;
+  };
+  float logits[kStages - 1];
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) logits[s] = issue(s);
+
+  GateScale gc{};
+  F bias = splat<P>(0.f), h = splat<P>(0.f);
+  int s = 0, fill = kStages - 1;
+  uint32_t i = 0;
+  for (;; ++i) {
+    const float b = sigmoid(logits[0]);
+#pragma unroll
+    for (int k = 0; k + 1 < kStages - 1; ++k) logits[k] = logits[k + 1];
+    logits[kStages - 2] = issue(fill);
+    fill = fill + 1 == kStages ? 0 : fill + 1;
+    __syncwarp();
+    const Tile t = tiles[warp][s];
+    if (t.valid == 0) break;
+    if (t.flags & kFresh) {
+      gc = gate_scale(__ldg(p.A_log + t.n), p.lower_bound);
+      bias = load_const<P>(p.dt_bias + (size_t)t.n * D + chan);
+    }
+    F start = splat<P>(0.f);
+    if (t.flags & kFirst) {
+      if (t.flags & kCut) start = join<D>(p, t.map, t.flags >> kOrder, t.n, chan);
+      else if (p.begin) start = load<P>(p.begin + ((size_t)t.slot * p.N + t.n) * D + chan);
+    }
+    T* const tg = reinterpret_cast<T*>(stages + s * kStage);
+    l.wait(l.full + 8 * s, i / kStages);
+    if (t.valid < K) fill_rows<T, D, 2>(tg, t.valid);
+
+    // decays and writes
+    F a[K], u[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const F e = each((load<P>(tg + k * D + chan) + bias) * gc.nz, ex2);
+      a[k] = each(each(e + splat<P>(1.f), rcp) * gc.l2, ex2);
+      u[k] = load<P>(tg + kRecTileElems + k * D + chan) * __shfl_sync(0xffffffffu, b, k);
+    }
+    // the state before the tile
+    if (p.ring > 1 && (i > 0 || warp % p.ring > 0)) {
+      l.wait(l.mine, warp % p.ring > 0 ? i : i - 1);
+      h = load<P>(l.inbox + chan);
+    }
+    if (l.failed) break;
+    if (t.flags & kFirst) h = start;
+    const F before = h;
+#pragma unroll
+    for (int k = 0; k < K; ++k) h = u[k] = fma(a[k], h, u[k]);
+    if (p.ring > 1) {
+      store(l.outbox + chan, h);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(l.theirs);
+    }
+    if (p.states) store(p.states + ((size_t)t.place * p.N + t.n) * D + chan, before);
+    T* o = out + t.slot * p.od.stride_b + t.n * p.od.stride_n + t.row * orow + chan;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k < t.valid) store(o, u[k]);
+      o += orow;
+    }
+    if ((t.flags & (kLast | kEnd)) == (kLast | kEnd))
+      store(p.end + ((size_t)t.slot * p.N + t.n) * D + chan, h);
+    s = s + 1 == kStages ? 0 : s + 1;
+  }
+  if (l.failed) give_up(p, l, tiles[warp], i, lane);
+}
+
+// Sums of K values over a warp, by halving the values as the distance halves: 32 / K lanes in a row
+// end with the sum of the same value.
+template <int K>
+__device__ __forceinline__ float warp_sums(float (&v)[K], int lane) {
+  int n = K, o = 16;
 #pragma unroll
   for (; n > 1; n /= 2, o /= 2) {
     const bool upper = lane & o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < K / 2; ++i) {
       if (i >= n / 2) break;
       const float keep = upper ? v[i + n / 2] : v[i], give = upper ? v[i] : v[i + n / 2];
       v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
@@ -389,235 +381,271 @@ __device__ __forceinline__ float group_sum8(float (&v)[8], int lane) {
 }
 
 template <class T, int D>
-__global__ void __launch_bounds__(kThreads, 2) rec_backward_kernel(const RecParams p) {
-  using P = Place<D>;
-  constexpr int R = P::kTile;
-  extern __shared__ __align__(16) unsigned char raw_smem[];
-  T* const stage = reinterpret_cast<T*>(raw_smem);  // [kStages][g, x, dout][R][D]
-  __shared__ float sb[2][R], sum_a[kThreads / 32];
-  __shared__ __align__(16) float sa[P::kGroups][D], sh[P::kGroups][D], sc[P::kGroups][D];
-  __shared__ __align__(16) float map_a[D], map_c[D], carry_in[D], carry_out[D];
+__global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
+    rec_backward_kernel(const __grid_constant__ RecParams p) {
+  using B = Block<T, true>;
+  using S = Shape<D>;
+  using F = typename S::F;
+  constexpr int K = S::K, V = S::V, P = V / 2, kStages = B::kStages;
+  constexpr int kStage = kStageBytes<T, D, true>, kElems = kRecTileElems;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Tile tiles[B::kWarps][kStages];
   if (!same_plan(p)) return;
-  const P me;
-  const int rank = blockIdx.x % p.cluster;
-  Walk now, next;
-  now.begin<R>(p);
-  next = now;
-  F4 c_next = splat(0.f), h_next = splat(0.f);
-  float beta = 0.f;
-  auto start = [&](int i) {
-    if (!next.done()) {
-      const Tile t = tile_of<R, true>(p, next, rank);
-      T* to = stage + (i % kStages<T>) * 3 * kRecTileElems;
-      if (t.work) {
-        request(to, p.g, next.u, t, me, true);
-        request(to + kRecTileElems, p.x, next.u, t, me, false);
-        if (p.dout.data) {
-          request(to + 2 * kRecTileElems, p.dout, next.u, t, me, false);
-        } else {
-#pragma unroll
-          for (int k = 0; k < kRows; ++k)
-            st4(to + 2 * kRecTileElems + (me.r0 + k) * D + me.chan, splat(0.f));
-        }
-      }
-      beta = request_beta<T>(p, next.u, t);
-      h_next = splat(0.f);
-      if (t.valid > 0)
-        h_next = f4(__ldg(reinterpret_cast<const float4*>(
-            p.states + ((size_t)(next.u.base + t.index) * p.N + next.u.n) * D + me.chan)));
-      if (next.step == 0) {
-        c_next = splat(0.f);
-        if (p.dfinal)
-          c_next = f4(__ldg(reinterpret_cast<const float4*>(
-              p.dfinal + ((size_t)next.u.slot * p.N + next.u.n) * D + me.chan)));
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  start(0);
-  if (threadIdx.x < R) sb[0][threadIdx.x] = sigmoid(beta);
-  __syncthreads();
-  F4 carry = splat(0.f), sum_b = splat(0.f), sum_raw = splat(0.f);
-  for (int i = 0; !now.done(); ++i) {
-    const Tile t = tile_of<R, true>(p, now, rank);
-    const float* const b = sb[i & 1] + me.r0;
-    if (now.step == 0) {
-      carry = c_next;
-      sum_b = sum_raw = splat(0.f);
-    }
-    F4 h = h_next;
-    next.next<R>(p);
-    if (kStages<T> == 2) start(i + 1);
-    const T* const tg = stage + (i % kStages<T>) * 3 * kRecTileElems + me.r0 * D + me.chan;
-    const T* const tx = tg + kRecTileElems;
-    const T* const td = tx + kRecTileElems;
-    const GateScale gc = gate_scale(__ldg(p.A_log + now.u.n), p.lower_bound);
-    const F4 bias =
-        f4(__ldg(reinterpret_cast<const float4*>(p.dt_bias + (size_t)now.u.n * D + me.chan)));
-    const long long row = p.od.stride_s;
-    const long long first = (long long)now.u.start + t.row + me.r0;
-    const long long o0 = (long long)now.u.slot * p.od.stride_b + (long long)now.u.n * p.od.stride_n +
-                         first * row + me.chan;
-    T* const dx = static_cast<T*>(p.out) + o0;
-    T* const dg = static_cast<T*>(p.dg) + o0;
-    T* const dbeta = static_cast<T*>(p.dbeta) + (long long)now.u.slot * p.bd.stride_b +
-                     (long long)now.u.n * p.bd.stride_n + first * p.bd.stride_s;
-    const int rows = p.slot_rows ? min(R, p.slot_rows - t.row) : t.valid;
-    if (t.valid < rows) {  // zeros behind the last token
-      for (int k = 0; k < kRows; ++k)
-        if (me.r0 + k >= t.valid && me.r0 + k < rows) {
-          st4(dx + k * row, splat(0.f));
-          st4(dg + k * row, splat(0.f));
-          if (me.chan == 0) dbeta[k * p.bd.stride_s] = from_f32<T>(0.f);
-        }
-    }
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages<T> - 1) : "memory");
-
-    // decays, and the maps of the thread's tokens: of the state forwards, of a_t lam_t backwards
-    F4 a[kRows], w[kRows];
-    if (t.work) {
-      F4 pa = splat(1.f), ph = splat(0.f), pc = splat(0.f);
-      const F4 nz = splat(gc.nz), l2 = splat(gc.l2), one = splat(1.f);
-      const F4 slope = splat(p.lower_bound * gc.ea);
-#pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        // e is kept finite: 1 - sigmoid is e sigmoid, without cancellation, and where the sigmoid
-        // is zero so is their product
-        const F4 e = each((own4(tg + k * D) + bias) * nz, [](float z) { return fminf(ex2(z), 3e38f); });
-        const F4 sig = each(e + one, rcp);
-        a[k] = each(sig * l2, ex2);
-        w[k] = sig * (e * sig) * (slope * a[k]);
-        pa = pa * a[k];
-        ph = fma4(a[k], ph, own4(tx + k * D) * splat(b[k]));
-        pc = fma4(pa, own4(td + k * D), pc);
-      }
-      sts4(&sa[me.group][me.chan], pa);
-      sts4(&sh[me.group][me.chan], ph);
-      sts4(&sc[me.group][me.chan], pc);
-    }
-    if (kStages<T> == 2 && threadIdx.x < R) sb[~i & 1][threadIdx.x] = sigmoid(beta);
-    __syncthreads();
-    float dot[kRows];
-    if (t.work) {
-      if (p.cluster > 1) {
-        if (threadIdx.x < P::kLanes) {
-          F4 ta = splat(1.f), tc = splat(0.f);
-          for (int k = P::kGroups - 1; k >= 0; --k) {
-            const F4 ka = lds4(&sa[k][me.chan]);
-            ta = ta * ka;
-            tc = fma4(ka, tc, lds4(&sc[k][me.chan]));
-          }
-          sts4(&map_a[me.chan], ta);
-          sts4(&map_c[me.chan], tc);
-        }
-        cluster_arrive();
-      }
-      // the state before each token, into w: dg = lam w
-      for (int k = 0; k < me.group; ++k) h = fma4(lds4(&sa[k][me.chan]), h, lds4(&sh[k][me.chan]));
-#pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        w[k] = w[k] * h;
-        h = fma4(a[k], h, own4(tx + k * D) * splat(b[k]));
-      }
-      // a_t lam_t of what follows the thread's tokens
-      F4 c = carry;
-      if (p.cluster > 1) {
-        cluster_wait();
-        if (threadIdx.x < P::kLanes) {
-          for (int r = p.cluster - 1; r >= 0; --r) {
-            if (r == rank) sts4(&carry_in[me.chan], carry);
-            carry = fma4(ld_rank(&map_a[me.chan], r), carry, ld_rank(&map_c[me.chan], r));
-          }
-          sts4(&carry_out[me.chan], carry);
-        }
-        cluster_arrive();  // the maps have been read
-        __syncthreads();
-        c = lds4(&carry_in[me.chan]);
-        carry = lds4(&carry_out[me.chan]);
-        for (int k = P::kGroups - 1; k > me.group; --k)
-          c = fma4(lds4(&sa[k][me.chan]), c, lds4(&sc[k][me.chan]));
-        cluster_wait();
-      } else {
-        for (int k = P::kGroups - 1; k >= 0; --k) {
-          if (k == me.group) c = carry;
-          carry = fma4(lds4(&sa[k][me.chan]), carry, lds4(&sc[k][me.chan]));
-        }
-      }
-      F4 here_b = splat(0.f), here_raw = splat(0.f);
-#pragma unroll
-      for (int k = kRows - 1; k >= 0; --k) {
-        dot[k] = 0.f;
-        if (me.r0 + k < t.valid) {
-          const F4 lam = own4(td + k * D) + c;
-          c = a[k] * lam;
-          const F4 dgk = lam * w[k], lx = lam * own4(tx + k * D);
-          dot[k] = (lx.lo.x + lx.lo.y) + (lx.hi.x + lx.hi.y);
-          st4(dx + k * row, lam * splat(b[k]));
-          st4(dg + k * row, dgk);
-          here_b = here_b + dgk;
-          here_raw = fma4(dgk, own4(tg + k * D) + bias, here_raw);
-        }
-      }
-      sum_b = sum_b + here_b;
-      sum_raw = sum_raw + here_raw;
-      // dbeta: the sum over the token's channels
-      constexpr int kEach = P::kLanes / kRows;  // lanes that end with the same token
-      const int lane = threadIdx.x % P::kLanes, k = lane / kEach;
-      const float sum = group_sum8<P::kLanes>(dot, lane);
-      if (lane % kEach == 0 && me.r0 + k < t.valid)
-        dbeta[k * p.bd.stride_s] = from_f32<T>(sum * b[k] * (1.f - b[k]));
-    }
-    if (kStages<T> == 1) {
-      start(i + 1);
-      if (threadIdx.x < R) sb[~i & 1][threadIdx.x] = sigmoid(beta);
-    }
-    __syncthreads();  // the maps are read, and of one stage the next logits written
-    if (now.step + 1 == now.u.steps) {
-      if (p.dh0 && rank == 0 && me.group == 0)
-        sts4(p.dh0 + ((size_t)now.u.slot * p.N + now.u.n) * D + me.chan, carry);
-      // the unit's part of the parameters' gradients
-      float raw = (sum_raw.lo.x + sum_raw.lo.y) + (sum_raw.hi.x + sum_raw.hi.y);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) raw += __shfl_xor_sync(0xffffffffu, raw, o);
-      if ((threadIdx.x & 31) == 0) sum_a[threadIdx.x >> 5] = raw;
-      sts4(&sh[me.group][me.chan], sum_b);
-      __syncthreads();
-      const size_t part = ((size_t)now.u.place * p.cluster + rank) * p.N + now.u.n;
-      if (threadIdx.x < D) {
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < P::kGroups; ++k) sum += sh[k][threadIdx.x];
-        p.part_bias[part * D + threadIdx.x] = sum;
-      } else if (threadIdx.x == D) {
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < kThreads / 32; ++k) sum += sum_a[k];
-        p.part_A[part] = sum;
-      }
-      __syncthreads();
-    }
-    now = next;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
+  const int rings = B::kWarps / p.ring;
+  auto l = lines<T, D, true>(p, warp, lane);
+  uint8_t* const stages = smem + warp * kStages * kStage;  // a stage: g, x, dout, state
+  T* const dx = static_cast<T*>(p.out);
+  T* const dg = static_cast<T*>(p.dg);
+  T* const dbeta = static_cast<T*>(p.dbeta);
+  const long long orow = p.od.stride_s;
+  if (!p.dout.data) {
+    for (int s = 0; s < kStages; ++s)
+      for (int k = 0; k < K; ++k)
+        store(reinterpret_cast<T*>(stages + s * kStage) + 2 * kElems + k * D + chan,
+              splat<P>(0.f));
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  if (p.cluster > 1) {
-    cluster_arrive();
-    cluster_wait();
+
+  Walk<K, true> walk;
+  auto zero = [&](int slot, int n, int row, int rows) {
+    const long long o = slot * p.od.stride_b + n * p.od.stride_n + row * orow + chan;
+    T* const ob = dbeta + slot * p.bd.stride_b + n * p.bd.stride_n + row * p.bd.stride_s;
+    for (int k = warp % p.ring; k < rows; k += p.ring) {
+      store(dx + o + k * orow, splat<P>(0.f));
+      store(dg + o + k * orow, splat<P>(0.f));
+      if (lane == 0) ob[k * p.bd.stride_s] = from_f32<T>(0.f);
+    }
+  };
+  walk.round = warp / p.ring;
+  walk.t = warp % p.ring;
+  walk.enter(p, rings, zero);
+  auto issue = [&](int s) {
+    __syncwarp();  // all lanes have read what the stage held
+    float logit = 0.f;
+    if (walk.done) {
+      if (lane == 0) tiles[warp][s].valid = 0;
+    } else {
+      int valid;
+      const Tile t = walk.tile(&valid);
+      const uint32_t bar = l.full + 8 * s, dst = smem_u32(stages + s * kStage);
+      if (lane == 0) {
+        tiles[warp][s] = t;
+        mbar_arrive_expect_tx(
+            bar, (p.dout.data ? 3 : 2) * valid * D * (int)sizeof(T) + D * (int)sizeof(float));
+      }
+      __syncwarp();
+      copy_rows<T, D>(dst, p.g, t, 0, lane, bar);
+      copy_rows<T, D>(dst + kElems * sizeof(T), p.x, t, 16, lane, bar);
+      if (p.dout.data) copy_rows<T, D>(dst + 2 * kElems * sizeof(T), p.dout, t, K == 8 ? 8 : 0, lane, bar);
+      if (lane == 31)
+        bulk_load(dst + 3 * kElems * sizeof(T), p.states + ((size_t)t.place * p.N + t.n) * D, D * 4, bar);
+      if (lane < valid) logit = to_f32(__ldg(at<T>(p.beta, t.slot, t.n, t.row + lane)));
+      walk.next(p, rings, zero);
+    }
+    return logit;
+  };
+  float logits[kStages - 1];
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) logits[s] = issue(s);
+
+  // the warp's part of the parameters' gradients in the unit, and where it goes
+  F sum_b = splat<P>(0.f), sum_raw = splat<P>(0.f);
+  int part = -1, part_n = 0;
+  auto flush = [&]() {
+    if (part < 0) return;
+    float raw = sum(sum_raw);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) raw += __shfl_xor_sync(0xffffffffu, raw, o);
+    const size_t to = (size_t)part * p.N + part_n;
+    store(p.part_bias + to * D + chan, sum_b);
+    if (lane == 0) p.part_A[to] = raw;
+    sum_b = sum_raw = splat<P>(0.f);
+  };
+
+  GateScale gc{};
+  F bias = splat<P>(0.f), c = splat<P>(0.f);
+  int s = 0, fill = kStages - 1;
+  uint32_t i = 0;
+  for (;; ++i) {
+    const float b_own = sigmoid(logits[0]), slope_own = b_own * sigmoid(-logits[0]);
+#pragma unroll
+    for (int k = 0; k + 1 < kStages - 1; ++k) logits[k] = logits[k + 1];
+    logits[kStages - 2] = issue(fill);
+    fill = fill + 1 == kStages ? 0 : fill + 1;
+    __syncwarp();
+    const Tile t = tiles[warp][s];
+    if (t.valid == 0) break;
+    if (t.flags & kFresh) {
+      gc = gate_scale(__ldg(p.A_log + t.n), p.lower_bound);
+      bias = load_const<P>(p.dt_bias + (size_t)t.n * D + chan);
+      flush();
+      part = t.part;
+      part_n = t.n;
+    }
+    F start = splat<P>(0.f);
+    if (t.flags & kFirst) {
+      if (t.flags & kCut) start = join<D>(p, t.map, t.flags >> kOrder, t.n, chan);
+      else if (p.begin) start = load<P>(p.begin + ((size_t)t.slot * p.N + t.n) * D + chan);
+    }
+    T* const tg = reinterpret_cast<T*>(stages + s * kStage);
+    const T* const tx = tg + kElems + chan;
+    const T* const td = tx + kElems;
+    l.wait(l.full + 8 * s, i / kStages);
+    if (t.valid < K) fill_rows<T, D, 3>(tg, t.valid);
+
+    // decays, and the factors w of dg = lam w
+    F a[K], w[K];
+    F h = load<P>(reinterpret_cast<const float*>(tg + 3 * kElems) + chan);
+    const float slope = p.lower_bound * gc.ea;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      // e is kept finite: 1 - sigmoid is e sigmoid, without cancellation, and where the sigmoid
+      // is zero so is their product
+      const F e = each((load<P>(tg + k * D + chan) + bias) * gc.nz,
+                       [](float z) { return fminf(ex2(z), 3e38f); });
+      const F sig = each(e + splat<P>(1.f), rcp);
+      a[k] = each(sig * gc.l2, ex2);
+      w[k] = sig * (e * sig) * (a[k] * slope) * h;
+      h = fma(a[k], h, load<P>(tx + k * D) * __shfl_sync(0xffffffffu, b_own, k));
+    }
+    // a lam of the token behind the tile
+    if (p.ring > 1 && (i > 0 || warp % p.ring > 0)) {
+      l.wait(l.mine, warp % p.ring > 0 ? i : i - 1);
+      c = load<P>(l.inbox + chan);
+    }
+    if (l.failed) break;
+    if (t.flags & kFirst) c = start;
+    // a becomes lam
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+      const F lam = load<P>(td + k * D) + c;
+      c = a[k] * lam;
+      a[k] = lam;
+    }
+    if (p.ring > 1) {
+      store(l.outbox + chan, c);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(l.theirs);
+    }
+    if ((t.flags & (kLast | kEnd)) == (kLast | kEnd) && p.end)
+      store(p.end + ((size_t)t.slot * p.N + t.n) * D + chan, c);
+    const long long o = t.slot * p.od.stride_b + t.n * p.od.stride_n + t.row * orow + chan;
+    T* ox = dx + o;
+    T* og = dg + o;
+    float dot[K];
+    F here_b = splat<P>(0.f), here_raw = splat<P>(0.f);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const F d = a[k] * w[k];
+      if (k < t.valid) {
+        store(ox, a[k] * __shfl_sync(0xffffffffu, b_own, k));
+        store(og, d);
+        here_b = here_b + d;
+        here_raw = fma(d, load<P>(tg + k * D + chan) + bias, here_raw);
+      }
+      dot[k] = sum(a[k] * load<P>(tx + k * D));
+      ox += orow;
+      og += orow;
+    }
+    sum_b = sum_b + here_b;
+    sum_raw = sum_raw + here_raw;
+    constexpr int kEach = 32 / K;  // lanes that end with the same token
+    const int k = lane / kEach;
+    const float total = warp_sums<K>(dot, lane) * __shfl_sync(0xffffffffu, slope_own, k);
+    if (lane % kEach == 0 && k < t.valid)
+      dbeta[t.slot * p.bd.stride_b + t.n * p.bd.stride_n + (t.row + k) * p.bd.stride_s] =
+          from_f32<T>(total);
+    s = s + 1 == kStages ? 0 : s + 1;
+  }
+  flush();
+  if (l.failed) give_up(p, l, tiles[warp], i, lane);
+}
+
+// The maps of the segments of cut sequences, one block each: row 0 of a sequence is its start, row
+// k + 1 the map of the walk's k-th segment (the last one's is not needed).  A warp takes an eighth
+// of the tokens.
+template <class T, int D, bool BACKWARD>
+__global__ void __launch_bounds__(256) rec_maps_kernel(const __grid_constant__ RecParams p) {
+  using S = Shape<D>;
+  using F = typename S::F;
+  constexpr int V = S::V, P = V / 2;
+  __shared__ __align__(16) float sa[8][D], sh[8][D];
+  if (p.plan[RH_CHECKSUM] != p.checksum) return;
+  const int i = blockIdx.x / p.N, n = blockIdx.x - i * p.N;
+  const int4 r0 = __ldg(record(p, i)), r1 = __ldg(record(p, i) + 1);
+  const int order = BACKWARD ? r1.z - 1 - r1.y : r1.y;
+  if (order + 1 == r1.z) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
+  const GateScale gc = gate_scale(__ldg(p.A_log + n), p.lower_bound);
+  const F bias = load_const<P>(p.dt_bias + (size_t)n * D + chan);
+  const kda_view_t& second = BACKWARD ? p.dout : p.x;
+  const int each_warp = (r0.z + 7) / 8, lo = min(r0.z, warp * each_warp), hi = min(r0.z, lo + each_warp);
+  F pa = splat<P>(1.f), ph = splat<P>(0.f);
+  for (int c0 = 0; c0 < hi - lo; c0 += 32) {
+    // up to 32 tokens, in the walk's order
+    const int count = min(32, hi - lo - c0), first = BACKWARD ? hi - 1 - c0 : lo + c0;
+    const int step = BACKWARD ? -1 : 1;
+    float b = 0.f;
+    if (!BACKWARD && lane < count)
+      b = sigmoid(to_f32(__ldg(at<T>(p.beta, r0.x, n, r0.y + first + lane))));
+    const T* g = at<T>(p.g, r0.x, n, r0.y + first) + chan;
+    const T* x = second.data ? at<T>(second, r0.x, n, r0.y + first) + chan : nullptr;
+#pragma unroll 8
+    for (int k = 0; k < count; ++k) {
+      const F raw = load_const<P>(g) + bias;
+      F v = x ? load_const<P>(x) : splat<P>(0.f);
+      const F a = each(each(each(raw * gc.nz, ex2) + splat<P>(1.f), rcp) * gc.l2, ex2);
+      pa = pa * a;
+      if (BACKWARD) {
+        ph = a * (ph + v);
+      } else {
+        ph = fma(a, ph, v * __shfl_sync(0xffffffffu, b, k));
+      }
+      g += step * p.g.stride_s;
+      if (x) x += step * second.stride_s;
+    }
+  }
+  store(&sa[warp][chan], pa);
+  store(&sh[warp][chan], ph);
+  __syncthreads();
+  if (warp > 0) return;
+  pa = splat<P>(1.f);
+  ph = splat<P>(0.f);
+  for (int k = 0; k < 8; ++k) {
+    const int w = BACKWARD ? 7 - k : k;
+    const F ka = load<P>(&sa[w][chan]);
+    pa = pa * ka;
+    ph = fma(ka, ph, load<P>(&sh[w][chan]));
+  }
+  float* m = p.maps + ((size_t)(r1.w + order + 1) * p.N + n) * 2 * D + chan;
+  store(m, pa);
+  store(m + D, ph);
+  if (order == 0) {
+    m -= (size_t)p.N * 2 * D;
+    store(m, splat<P>(0.f));
+    store(m + D, p.begin ? load<P>(p.begin + ((size_t)r0.x * p.N + n) * D + chan) : splat<P>(0.f));
   }
 }
 
-// ddt_bias and dA_log: the units' parts in a fixed order, in fp64.  A block has 32 channels of a
-// head (the first one of a head its dA_log too), 32 threads a channel.
+// ddt_bias and dA_log: the warps' parts in a fixed order, in fp64.  A block has 32 channels of a
+// head (the first one of a head its dA_log too); 32 threads a channel take the segments in turn.
 template <int D>
-__global__ void __launch_bounds__(1024) rec_params_kernel(const float* part_bias,
-                                                          const float* part_A, int parts, int N,
+__global__ void __launch_bounds__(1024) rec_params_kernel(const __grid_constant__ RecParams p,
                                                           float* dA_log, float* ddt_bias) {
   __shared__ double red[32][33];
-  constexpr int kBlocks = D / 32;
+  constexpr int kBlocks = D / 32, K = Shape<D>::K;
   const int n = blockIdx.x / kBlocks, d = (blockIdx.x % kBlocks) * 32 + (threadIdx.x & 31);
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-  double sum = 0;
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, records = p.units / p.N;
+  if (p.plan[RH_CHECKSUM] != p.checksum) return;
+  double sum = 0, raw = 0;
+  for (int k = row; k < records; k += 32) {
+    const int4 r0 = __ldg(record(p, k)), r1 = __ldg(record(p, k) + 1);
+    const int parts = min(p.ring, (r0.z + K - 1) / K);
+    const float* b = p.part_bias + ((size_t)r1.x * p.N + n) * D + d;
 #pragma unroll 4
-  for (int k = row; k < parts; k += 32) sum += part_bias[((size_t)k * N + n) * D + d];
+    for (int i = 0; i < parts; ++i) sum += b[(size_t)i * p.N * D];
+    if (lane < parts) raw += p.part_A[(size_t)(r1.x + lane) * p.N + n];
+  }
   red[row][lane] = sum;
   __syncthreads();
   if (row == 0) {
@@ -626,15 +654,12 @@ __global__ void __launch_bounds__(1024) rec_params_kernel(const float* part_bias
   }
   if (blockIdx.x % kBlocks != 0) return;
   __syncthreads();
-  sum = 0;
-  for (int k = threadIdx.x; k < parts; k += 1024) sum += part_A[(size_t)k * N + n];
-  red[row][lane] = sum;
+  red[row][lane] = raw;
   __syncthreads();
   if (row == 0) {
-    sum = 0;
-    for (int k = 0; k < 32; ++k) sum += red[k][lane];
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_down_sync(0xffffffffu, sum, o);
-    if (lane == 0) dA_log[n] = (float)sum;
+    for (int k = 1; k < 32; ++k) raw += red[k][lane];
+    for (int o = 16; o > 0; o >>= 1) raw += __shfl_down_sync(0xffffffffu, raw, o);
+    if (lane == 0) dA_log[n] = (float)raw;
   }
 }
 
@@ -704,13 +729,13 @@ kda_status_t prepare(const kda_recurrence_shape_t* shape, const int32_t* plan_ho
   p->plan = plan_dev;
   p->checksum = plan_host[RH_CHECKSUM];
   p->N = shape->N;
-  p->units = shape->B * shape->N;
+  p->units = plan_host[RH_RECORDS] * shape->N;
   p->slot_rows = shape->layout == KDA_LAYOUT_TND ? 0 : shape->S;
-  p->h0 = h0;
   p->A_log = A_log;
   p->dt_bias = dt_bias;
   p->lower_bound = lower_bound;
   p->status = static_cast<int32_t*>(workspace);
+  p->maps = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHeaderBytes);
   p->od = dense_view(nullptr, shape->layout, shape->N, shape->S, shape->D);
   p->bd = dense_view(nullptr, shape->layout, shape->N, shape->S, 1);
   if (nb == 1) p->od.stride_b = p->bd.stride_b = 0;
@@ -718,95 +743,60 @@ kda_status_t prepare(const kda_recurrence_shape_t* shape, const int32_t* plan_ho
 }
 
 size_t states_floats(const int32_t* plan) {
-  return (size_t)plan[RH_CHAIN] * plan[RH_N] * plan[RH_D];
+  return (size_t)plan[RH_TILES] * plan[RH_N] * plan[RH_D];
 }
 
-// The workspace after its header: the parameters' partial gradients of a backward pass, one of each
-// block of a cluster at the most.
+// The workspace after its header: the maps of cut sequences, and the parameters' partial gradients of
+// a backward pass.
 struct Scratch {
-  size_t part_A, total;
+  size_t bias, A, total;
   Scratch(const int32_t* plan, bool backward) {
-    const size_t heads = (size_t)plan[RH_B] * (1 << (kRecClusters - 1)) * plan[RH_N];
-    part_A = kWsHeaderBytes + heads * plan[RH_D] * 4;
-    total = backward ? part_A + heads * 4 : kWsHeaderBytes;
+    const size_t N = plan[RH_N], row = N * plan[RH_D] * 4;
+    bias = kWsHeaderBytes + plan[RH_MAPS] * 2 * row;
+    A = bias + (backward ? plan[RH_PARTS] * row : 0);
+    total = A + (backward ? plan[RH_PARTS] * N * 4 : 0);
   }
 };
 
-// What a kernel's launches need to know of a device: the blocks that it holds at a time, as clusters
-// of each size.
-struct Resident {
-  PerDevice of[kRecClusters];
-};
-
-void configure(int smem, int cluster, unsigned blocks, cudaStream_t s, cudaLaunchConfig_t* cfg,
-               cudaLaunchAttribute* attr) {
-  *cfg = cudaLaunchConfig_t{};
-  cfg->gridDim = dim3(blocks);
-  cfg->blockDim = dim3(kThreads);
-  cfg->dynamicSmemBytes = (size_t)smem;
-  cfg->stream = s;
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = (unsigned)cluster;
-  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
-  cfg->attrs = attr;
-  cfg->numAttrs = 1;
-}
-
-// Clusters of 2^c blocks that the current device holds at a time.
-template <class K>
-cudaError_t resident_clusters(K kernel, Resident& r, int smem, int c, int* clusters) {
-  int dev = 0;
+// Launches a pass: the maps where sequences are cut, and the walk, a block on every multiprocessor
+// that has a unit.
+template <class T, int D, bool BACKWARD, class Kernel>
+cudaError_t launch(Kernel kernel, PerDevice& once, RecParams& p, const int32_t* plan,
+                   cudaStream_t s) {
+  using B = Block<T, BACKWARD>;
+  constexpr int kSmem = kWalkSmem<T, D, BACKWARD>;
+  int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  return once_per_device(r.of[c], dev, clusters, [&](int, int* n) {
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr;
-    configure(smem, 1 << c, 1u << c, nullptr, &cfg, &attr);
-    err = cudaOccupancyMaxActiveClusters(n, kernel, &cfg);
-    return err == cudaSuccess && *n < 1 ? cudaErrorLaunchOutOfResources : err;
+  e = once_per_device(once, dev, &sms, [&](int d, int* n) {
+    const cudaError_t err =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    return err == cudaSuccess ? cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, d) : err;
   });
-}
-
-// Launches a pass on clusters of the size that takes the fewest steps one after another: those of
-// the longest unit, or, where that is more, of all units over the clusters that run at a time.  The
-// exchange between blocks makes a step of a cluster longer by about a third.
-template <class K>
-cudaError_t launch(K kernel, Resident& r, int smem, RecParams& p, const int32_t* plan,
-                   cudaStream_t s) {
-  int best = 0, best_clusters = 0;
-  double least = 0;
-  for (int c = 0; c < kRecClusters; ++c) {
-    int clusters = 0;
-    const cudaError_t e = resident_clusters(kernel, r, smem, c, &clusters);
+  if (e != cudaSuccess) return e;
+  const int blocks = std::min(sms, p.units), rounds = (p.units - 1) / blocks + 1;
+  p.ring = B::kWarps;
+  while (p.ring > 1 && (B::kWarps % p.ring || p.ring * std::min(rounds, 2) > B::kWarps)) --p.ring;
+  if (const char* r = getenv(BACKWARD ? "RB" : "RF")) p.ring = atoi(r);
+  if (plan[RH_MAPS]) {
+    rec_maps_kernel<T, D, BACKWARD><<<(unsigned)p.units, 256, 0, s>>>(p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const double all = (double)plan[RH_STEPS + c] * p.N / std::min(clusters, p.units);
-    const double one = (double)((plan[RH_MAX_TILES] + (1 << c) - 1) >> c);
-    const double cost = std::max(all, one) * (c == 0 ? 3 : 4);
-    if (c == 0 || cost < least) {
-      least = cost;
-      best = c;
-      best_clusters = clusters;
-    }
   }
-  p.cluster = 1 << best;
-  cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr;
-  configure(smem, p.cluster, (unsigned)std::min(best_clusters, p.units) * p.cluster, s, &cfg, &attr);
-  return cudaLaunchKernelEx(&cfg, kernel, (const RecParams)p);
+  kernel<<<(unsigned)blocks, 32 * B::kWarps, kSmem, s>>>(p);
+  return cudaGetLastError();
 }
 
 template <class T, int D>
 cudaError_t launch_forward(RecParams& p, const int32_t* plan, cudaStream_t s) {
-  static Resident resident;
-  return launch(rec_forward_kernel<T, D>, resident, forward_smem<T, D>(), p, plan, s);
+  static PerDevice once;
+  return launch<T, D, false>(rec_forward_kernel<T, D>, once, p, plan, s);
 }
 
 template <class T, int D>
 cudaError_t launch_backward(RecParams& p, const int32_t* plan, cudaStream_t s) {
-  static Resident resident;
-  return launch(rec_backward_kernel<T, D>, resident, backward_smem<T, D>(), p, plan, s);
+  static PerDevice once;
+  return launch<T, D, true>(rec_backward_kernel<T, D>, once, p, plan, s);
 }
 
 template <class F>
@@ -868,8 +858,8 @@ extern "C" kda_status_t kda_recurrence_forward(
   if (!out || !final_state) return KDA_ERR_NULL;
   if (!aligned16(out) || !aligned16(final_state) || !aligned16(states)) return KDA_ERR_ALIGN;
   const Sizes z = sizes_of(*shape);
-  // final_state may be initial_state itself: a unit's blocks have read its start state before the
-  // barrier of its first step, and its end state is written after that of its last
+  // final_state may be initial_state itself: the end of a sequence that is not cut follows from its
+  // start, and of one that is cut the start is among the maps, which are done before the walk
   if (final_state == initial_state) in[3] = ByteRange{};
   const ByteRange outs[] = {dense_range(out, z.x), dense_range(final_state, z.state),
                             dense_range(states, states_floats(plan_host) * 4)};
@@ -879,7 +869,8 @@ extern "C" kda_status_t kda_recurrence_forward(
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   p.states = states;
   p.out = out;
-  p.final_state = final_state;
+  p.begin = initial_state;
+  p.end = final_state;
   const cudaError_t e = dispatch(*shape, [&](auto* tag, auto d) {
     return launch_forward<std::remove_pointer_t<decltype(tag)>, decltype(d)::value>(p, plan_host, s);
   });
@@ -922,21 +913,20 @@ extern "C" kda_status_t kda_recurrence_backward(
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const Scratch scratch(plan_host, true);
   uint8_t* const ws = static_cast<uint8_t*>(workspace);
-  p.part_bias = reinterpret_cast<float*>(ws + kWsHeaderBytes);
-  p.part_A = reinterpret_cast<float*>(ws + scratch.part_A);
+  p.part_bias = reinterpret_cast<float*>(ws + scratch.bias);
+  p.part_A = reinterpret_cast<float*>(ws + scratch.A);
   p.states = const_cast<float*>(states);
-  p.dfinal = dfinal_state;
+  p.begin = dfinal_state;
   p.out = dx;
   p.dg = dg;
   p.dbeta = dbeta;
-  p.dh0 = dinitial_state;
+  p.end = dinitial_state;
   const cudaError_t e = dispatch(*shape, [&](auto* tag, auto d) {
     constexpr int D = decltype(d)::value;
     using T = std::remove_pointer_t<decltype(tag)>;
     const cudaError_t err = launch_backward<T, D>(p, plan_host, s);
     if (err != cudaSuccess) return err;
-    rec_params_kernel<D><<<(unsigned)shape->N * (D / 32), 1024, 0, s>>>(
-        p.part_bias, p.part_A, shape->B * p.cluster, p.N, dA_log, ddt_bias);
+    rec_params_kernel<D><<<(unsigned)shape->N * (D / 32), 1024, 0, s>>>(p, dA_log, ddt_bias);
     return cudaGetLastError();
   });
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

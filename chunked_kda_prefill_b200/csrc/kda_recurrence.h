@@ -5,28 +5,33 @@
 
 namespace kda {
 
-// A plan is an int32 header followed by one record per sequence, longest first.  A tile is
-// kRecTileElems / D consecutive tokens of one (sequence, head); a cluster of blocks walks one
-// (sequence, head) at a time, a tile per block and step.
+// A plan is an int32 header followed by one record per segment, longest first.  A segment is a
+// sequence, or one of the equal parts of a long one; a tile is kRecTileElems / D consecutive tokens
+// of a segment in one head.
 constexpr int32_t kRecMagic = 0x4B524331;  // "KRC1"
-constexpr int32_t kRecVersion = 1;
+constexpr int32_t kRecVersion = 2;
 constexpr int kRecHeader = 24;
-constexpr int kRecRecord = 4;
-constexpr int kRecTileElems = 8192;
+constexpr int kRecRecord = 8;
+constexpr int kRecTileElems = 1024;
 constexpr int rec_tile_rows(int D) { return kRecTileElems / D; }
-// Cluster sizes that a launch chooses from: 1, 2, 4, 8.
-constexpr int kRecClusters = 4;
+constexpr int kRecRing = 16;     // warps that walk a segment together, at the most
+constexpr int kRecSpread = 148;  // multiprocessors that a plan spreads long sequences over
 
-// RH_CHAIN is the number of tiles with tokens, RH_MAX_TILES that of the sequence with most tiles
-// (padding rows included), RH_STEPS + c the steps of one head of every sequence on clusters of 2^c.
+// RH_TILES is the number of tiles in one head, RH_MAPS the rows of maps that the segments of cut
+// sequences need (0: none is cut), RH_PARTS the rows of the parameters' partial gradients,
+// RH_LONGEST the tiles of the longest segment.
 enum RecHeader : int {
   RH_MAGIC = 0, RH_VERSION, RH_HEADER_WORDS, RH_RECORD_WORDS, RH_LAYOUT, RH_B, RH_N, RH_S, RH_D,
-  RH_TILE_ROWS, RH_CHAIN, RH_MAX_TILES, RH_STEPS, RH_TABLE_HASH = RH_STEPS + kRecClusters,
+  RH_TILE_ROWS, RH_TILES, RH_RECORDS, RH_MAPS, RH_PARTS, RH_LONGEST, RH_TABLE_HASH = 16,
   RH_CHECKSUM = kRecHeader - 1
 };
-// RR_SLOT is the sequence, RR_START its first token within its slot (or in the packed rows),
-// RR_LEN its tokens and RR_BASE the place of its first tile in the states.
-enum RecRecord : int { RR_SLOT = 0, RR_START, RR_LEN, RR_BASE };
+// RR_SLOT is the sequence, RR_START the segment's first token within its slot (or in the packed
+// rows), RR_LEN its tokens, RR_TILE its first tile, RR_PART its first row of partial gradients (it
+// has one for each of its tiles, kRecRing at the most), RR_SEGMENT its place among the RR_SEGMENTS
+// of its sequence and RR_MAP the sequence's first row of maps.
+enum RecRecord : int {
+  RR_SLOT = 0, RR_START, RR_LEN, RR_TILE, RR_PART, RR_SEGMENT, RR_SEGMENTS, RR_MAP
+};
 
 kda_status_t validate_recurrence_shape(const kda_recurrence_shape_t* s);
 // Checks a host plan's header (its own checksum, which covers a hash of the records) and, when

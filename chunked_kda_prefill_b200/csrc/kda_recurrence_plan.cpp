@@ -1,5 +1,5 @@
-// kda_recurrence_plan.cpp -- host planner of the gated recurrence: the sequences, longest first, and
-// how many steps they take.  Reads lengths only; never touches the GPU.
+// kda_recurrence_plan.cpp -- host planner of the gated recurrence: which sequences are cut, and the
+// segments, longest first.  Reads lengths only; never touches the GPU.
 #include <algorithm>
 #include <climits>
 #include <cstring>
@@ -47,42 +47,99 @@ kda_status_t each_length(const kda_recurrence_shape_t& s, const int32_t* cu, F&&
 
 long long tiles_of(long long rows, int R) { return (rows + R - 1) / R; }
 
-// Whether the lengths are well formed and everything fits the kernels' 32-bit counters.
-kda_status_t check_lengths(const kda_recurrence_shape_t& s, const int32_t* cu) {
-  const int R = rec_tile_rows(s.D);
-  long long tiles = 0;
-  const kda_status_t st = each_length(s, cu, [&](int, int32_t len) {
-    tiles += tiles_of(s.layout == KDA_LAYOUT_TND ? len : s.S, R);
-  });
-  if (st != KDA_OK) return st;
-  return tiles > INT_MAX / 2 ? KDA_ERR_SHAPE : KDA_OK;
+struct Cut {
+  long long most = 0;      // tiles of a segment, at the most; 0: no sequence is cut
+  long long segments = 0;  // of all sequences
+};
+
+long long segments_of(long long tiles, long long most) {
+  return most ? (tiles + most - 1) / most : 1;
 }
 
-kda_status_t build(const kda_recurrence_shape_t& s, const int32_t* cu, int32_t* plan, size_t n) {
-  kda_status_t st = check_lengths(s, cu);
+// Whether the lengths are well formed and everything fits the kernels' 32-bit counters, and how the
+// sequences are cut.
+//
+// Uncut, a pass takes as long as its longest sequence, one tile after another, or as the busiest of
+// the multiprocessors.  Cut, the segments' maps come first, from data that is then read again: about
+// 1.8 times the work, and 50 tiles' time for the second launch and the joins (both measured).  Of
+// the cuts into segments for one to eight rounds over the multiprocessors the cheapest is taken.
+kda_status_t check_lengths(const kda_recurrence_shape_t& s, const int32_t* cu, Cut* cut) {
+  const int R = rec_tile_rows(s.D);
+  long long tiles = 0, longest = 0;
+  const kda_status_t st = each_length(s, cu, [&](int, int32_t len) {
+    tiles += tiles_of(len, R);
+    longest = std::max(longest, tiles_of(len, R));
+  });
   if (st != KDA_OK) return st;
-  if (n < (size_t)kRecHeader + (size_t)s.B * kRecRecord) return KDA_ERR_PLAN;
+  if (tiles > INT_MAX / 64) return KDA_ERR_SHAPE;
+  *cut = Cut{0, s.B};
+  const double all = (double)tiles * s.N / kRecSpread;
+  double least = std::max(all, (double)longest);
+  for (int rounds = 1; rounds <= 8; ++rounds) {
+    // the smallest segments of which every multiprocessor has `rounds`
+    const long long room = (long long)kRecSpread * rounds / s.N;
+    if (room < s.B) continue;
+    long long lo = 1, hi = longest, count = 0;
+    auto segments = [&](long long most) {
+      long long n = 0;
+      each_length(s, cu, [&](int, int32_t len) { n += segments_of(tiles_of(len, R), most); });
+      return n;
+    };
+    while (lo < hi) {
+      const long long mid = (lo + hi) / 2;
+      if (segments(mid) <= room) hi = mid;
+      else lo = mid + 1;
+    }
+    count = segments(lo);
+    const double cost = 1.8 * rounds * (double)lo + 50;
+    if (count > s.B && cost < least) {
+      least = cost;
+      *cut = Cut{lo, count};
+    }
+  }
+  return KDA_OK;
+}
+
+size_t plan_words(const Cut& cut) { return (size_t)kRecHeader + (size_t)cut.segments * kRecRecord; }
+
+kda_status_t build(const kda_recurrence_shape_t& s, const int32_t* cu, int32_t* plan, size_t n) {
+  Cut cut;
+  kda_status_t st = check_lengths(s, cu, &cut);
+  if (st != KDA_OK) return st;
+  if (n < plan_words(cut)) return KDA_ERR_PLAN;
   const int R = rec_tile_rows(s.D);
   const bool tnd = s.layout == KDA_LAYOUT_TND;
-  struct Seq { int32_t b, start, len; };
-  std::vector<Seq> seqs;
-  seqs.reserve(s.B);
-  each_length(s, cu, [&](int b, int32_t len) { seqs.push_back({b, tnd ? cu[b] : 0, len}); });
-  std::stable_sort(seqs.begin(), seqs.end(),
-                   [](const Seq& a, const Seq& d) { return a.len > d.len; });
+  struct Segment { int32_t b, start, len, index, count, map; };
+  std::vector<Segment> segs;
+  segs.reserve(cut.segments);
+  long long maps = 0;
+  each_length(s, cu, [&](int b, int32_t len) {
+    const long long tiles = tiles_of(len, R), count = segments_of(tiles, cut.most);
+    for (long long k = 0; k < count; ++k) {
+      const long long lo = tiles * k / count * R, hi = std::min((long long)len, tiles * (k + 1) / count * R);
+      segs.push_back({b, (int32_t)((tnd ? cu[b] : 0) + lo), (int32_t)(hi - lo), (int32_t)k,
+                      (int32_t)count, (int32_t)maps});
+    }
+    if (count > 1) maps += count;
+  });
+  std::stable_sort(segs.begin(), segs.end(),
+                   [](const Segment& a, const Segment& d) { return a.len > d.len; });
   std::memset(plan, 0, kRecHeader * sizeof(int32_t));
   int32_t* rec = plan + kRecHeader;
-  long long base = 0, most = 0, steps[kRecClusters] = {};
-  for (const Seq& q : seqs) {
+  long long tile = 0, part = 0;
+  for (const Segment& q : segs) {
+    const long long tiles = tiles_of(q.len, R);
     rec[RR_SLOT] = q.b;
     rec[RR_START] = q.start;
     rec[RR_LEN] = q.len;
-    rec[RR_BASE] = (int32_t)base;
+    rec[RR_TILE] = (int32_t)tile;
+    rec[RR_PART] = (int32_t)part;
+    rec[RR_SEGMENT] = q.index;
+    rec[RR_SEGMENTS] = q.count;
+    rec[RR_MAP] = q.map;
     rec += kRecRecord;
-    base += tiles_of(q.len, R);
-    const long long all = tiles_of(tnd ? q.len : s.S, R);
-    most = std::max(most, all);
-    for (int c = 0; c < kRecClusters; ++c) steps[c] += tiles_of(all, 1 << c);
+    tile += tiles;
+    part += std::min<long long>(tiles, kRecRing);
   }
   plan[RH_MAGIC] = kRecMagic;
   plan[RH_VERSION] = kRecVersion;
@@ -94,10 +151,12 @@ kda_status_t build(const kda_recurrence_shape_t& s, const int32_t* cu, int32_t* 
   plan[RH_S] = s.S;
   plan[RH_D] = s.D;
   plan[RH_TILE_ROWS] = R;
-  plan[RH_CHAIN] = (int32_t)base;
-  plan[RH_MAX_TILES] = (int32_t)most;
-  for (int c = 0; c < kRecClusters; ++c) plan[RH_STEPS + c] = (int32_t)steps[c];
-  plan[RH_TABLE_HASH] = (int32_t)(fnv(plan + kRecHeader, (size_t)s.B * kRecRecord) & 0x7fffffff);
+  plan[RH_TILES] = (int32_t)tile;
+  plan[RH_RECORDS] = (int32_t)segs.size();
+  plan[RH_MAPS] = (int32_t)maps;
+  plan[RH_PARTS] = (int32_t)part;
+  plan[RH_LONGEST] = (int32_t)tiles_of(segs[0].len, R);
+  plan[RH_TABLE_HASH] = (int32_t)(fnv(plan + kRecHeader, segs.size() * kRecRecord) & 0x7fffffff);
   plan[RH_CHECKSUM] = (int32_t)(fnv(plan, RH_CHECKSUM) & 0x7fffffff);
   return KDA_OK;
 }
@@ -111,7 +170,8 @@ kda_status_t validate_recurrence_plan(const int32_t* p, size_t n, const kda_recu
       p[RH_HEADER_WORDS] != kRecHeader || p[RH_RECORD_WORDS] != kRecRecord)
     return KDA_ERR_PLAN;
   if ((int32_t)(fnv(p, RH_CHECKSUM) & 0x7fffffff) != p[RH_CHECKSUM]) return KDA_ERR_PLAN;
-  if (p[RH_B] < 1 || n < (size_t)kRecHeader + (size_t)p[RH_B] * kRecRecord) return KDA_ERR_PLAN;
+  if (p[RH_RECORDS] < 1 || n < (size_t)kRecHeader + (size_t)p[RH_RECORDS] * kRecRecord)
+    return KDA_ERR_PLAN;
   if (s && (p[RH_LAYOUT] != s->layout || p[RH_B] != s->B || p[RH_N] != s->N || p[RH_S] != s->S ||
             p[RH_D] != s->D))
     return KDA_ERR_PLAN;
@@ -127,9 +187,10 @@ extern "C" kda_status_t kda_recurrence_plan_size(const kda_recurrence_shape_t* s
   if (!n_int32) return KDA_ERR_NULL;
   kda_status_t st = validate_recurrence_shape(shape);
   if (st != KDA_OK) return st;
-  st = check_lengths(*shape, cu);
+  Cut cut;
+  st = check_lengths(*shape, cu, &cut);
   if (st != KDA_OK) return st;
-  *n_int32 = (size_t)kRecHeader + (size_t)shape->B * kRecRecord;
+  *n_int32 = plan_words(cut);
   return KDA_OK;
 }
 

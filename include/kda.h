@@ -321,7 +321,7 @@ KDA_API kda_status_t kda_recurrence_plan(const kda_recurrence_shape_t* shape,
 KDA_API kda_status_t kda_recurrence_workspace_size(const int32_t* plan_host, size_t n_int32,
                                                    int32_t backward, size_t* bytes);
 
-/* fp32 values of the `states` buffer: the [N, D] states before every 8192 / D tokens of each
+/* fp32 values of the `states` buffer: the [N, D] states before every 1024 / D tokens of each
  * sequence, from its first one. */
 KDA_API kda_status_t kda_recurrence_states_size(const int32_t* plan_host, size_t n_int32,
                                                 size_t* n_floats);

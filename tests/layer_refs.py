@@ -104,9 +104,9 @@ def recurrence(x, g, beta, h0, A_log, dt_bias, lb, layout, lengths, dout=None, d
               + (C + 26 + 8 * (ea * raw).abs()) * U * dg.abs())
         pick(res["dg"][0])[:] = dg
         pick(res["dg"][1])[:] = Eg
-        # sums over tokens: the terms' bounds, and the roundings on a term's way: 8 tokens in order,
-        # one for each of the walk's steps of at least 64 tokens, 16 threads, 4 channels and 32 lanes
-        K = 64 + n // 64
+        # sums over tokens: the terms' bounds, and the roundings on a term's way: 16 tokens in order
+        # at the most, one for each tile of at least 8 tokens, 4 channels and 32 lanes
+        K = 64 + n // 8
         res["ddt_bias"][0].add_(dg.sum(0))
         res["ddt_bias"][1].add_((Eg + K * U * dg.abs()).sum(0))
         res["dA_log"][0].add_((dg * raw).sum((0, 2)))

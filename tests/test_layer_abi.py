@@ -57,29 +57,52 @@ def test_recurrence_lengths(L, layout, B, S, cu, code):
 
 
 @pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("N", [1, 3, 32])
 @pytest.mark.parametrize("layout,S,lengths", [
-    (2, None, [1]), (2, None, [130, 1, 700, 64, 65, 63]), (1, 300, [300, 1, 128]), (0, 129, [129, 64])])
-def test_plan_records(L, D, layout, S, lengths):
-    """Sequences longest first, ties in order, with their rows and their places in the states; the
-    steps of clusters of 1, 2, 4 and 8 blocks."""
+    (2, None, [1]), (2, None, [130, 1, 700, 64, 65, 63]), (1, 300, [300, 1, 128]), (0, 129, [129, 64]),
+    (0, 8192, [8192]), (2, None, [65536]), (1, 4000, [4000, 2777]), (2, None, [9000] + [3] * 400)])
+def test_plan_records(L, D, N, layout, S, lengths):
+    """The segments, longest first, cover every sequence in order, in whole tiles but the last; their
+    tiles, parts and maps lie side by side."""
     cu = np.concatenate([[0], np.cumsum(lengths)])
     S = S or int(cu[-1])
-    st, p = rec_plan(L, rec_shape(layout=layout, B=len(lengths), S=S, D=D), cu)
+    st, p = rec_plan(L, rec_shape(layout=layout, B=len(lengths), S=S, D=D, N=N), cu)
     assert st == 0
-    R, rec = 8192 // D, p[24:].reshape(-1, 4).tolist()
+    R, rec = 1024 // D, p[24:].reshape(-1, 8).tolist()
     tiles = lambda n: -(-n // R)  # noqa: E731
-    order = sorted(range(len(lengths)), key=lambda b: -lengths[b])
-    base = 0
-    for (slot, start, n, at), b in zip(rec, order, strict=True):
-        assert (slot, start, n, at) == (b, int(cu[b]) if layout == 2 else 0, lengths[b], base)
-        base += tiles(n)
-    assert int(p[10]) == base
-    walked = [tiles(n if layout == 2 else S) for n in lengths]
-    assert int(p[11]) == max(walked)
-    assert p[12:16].tolist() == [sum(-(-t // c) for t in walked) for c in (1, 2, 4, 8)]
+    assert int(p[11]) == len(rec) and int(p[9]) == R
+    assert [r[2] for r in rec] == sorted((r[2] for r in rec), reverse=True)
+    tile = part = 0
+    for r in rec:
+        assert r[3:5] == [tile, part]
+        tile, part = tile + tiles(r[2]), part + min(16, tiles(r[2]))
+    assert (int(p[10]), int(p[13]), int(p[14])) == (tile, part, tiles(rec[0][2]))
+    maps = 0
+    for b, n in enumerate(lengths):
+        mine = sorted((r for r in rec if r[0] == b), key=lambda r: r[5])
+        at = int(cu[b]) if layout == 2 else 0
+        for k, (_, start, length, _, _, index, count, first) in enumerate(mine):
+            assert (start, index, count, first) == (at, k, len(mine), maps)
+            assert length % R == 0 or k + 1 == len(mine)
+            at += length
+        assert at == (int(cu[b]) if layout == 2 else 0) + n
+        lens = [tiles(r[2]) for r in mine]
+        assert max(lens) - min(lens) <= 1
+        maps += len(mine) if len(mine) > 1 else 0
+    assert int(p[12]) == maps
+    if maps:  # a cut pays only where it fills the machine
+        assert len(rec) * N <= 8 * 148
     floats = ctypes.c_size_t(0)
     assert L.kda_recurrence_states_size(p.ctypes.data_as(P_I32), p.size, ctypes.byref(floats)) == 0
-    assert floats.value == base * 3 * D
+    assert floats.value == tile * N * D
+    sizes = []
+    for backward in (0, 1):
+        n = ctypes.c_size_t(0)
+        assert L.kda_recurrence_workspace_size(p.ctypes.data_as(P_I32), p.size, backward,
+                                               ctypes.byref(n)) == 0
+        sizes.append(n.value)
+    assert sizes[0] == 256 + maps * N * 2 * D * 4
+    assert sizes[1] == sizes[0] + part * N * (D + 1) * 4
 
 
 def test_recurrence_plan_capacity_and_corruption(L):
@@ -90,7 +113,7 @@ def test_recurrence_plan_capacity_and_corruption(L):
         a.ctypes.data_as(P_I32), a.size if k is None else k, 0, ctypes.byref(n))
     assert ok(p) == 0 and n.value >= 256
     assert ok(p, p.size - 1) == PLAN and ok(p, 3) == PLAN
-    for word in (0, 4, 5, 10, 11, 12, 16, 23):
+    for word in (0, 4, 5, 10, 11, 12, 13, 14, 16, 23):
         bad = p.copy()
         bad[word] += 1
         assert ok(bad) == PLAN, word
