@@ -20,7 +20,6 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
-#include <cstdlib>
 #include <type_traits>
 
 #include "kda_args.h"
@@ -39,7 +38,6 @@ struct RecParams {
   int32_t checksum;
   int32_t N, units;   // units: segments times heads
   int32_t slot_rows;  // rows that a slot's outputs have, padding included; 0 for packed rows
-  int32_t ring;       // warps of a ring
   const float* begin;  // [B][N][D] the walk's start (forward h0, backward dfinal), or null for zeros
   const float* A_log;
   const float* dt_bias;
@@ -69,8 +67,8 @@ struct Shape {
   using F = Pairs<V / 2>;
 };
 
-// Warps of a block, one block a multiprocessor, and the tiles whose copies a warp has under way or at
-// work: as many as the registers (forward 128 a thread, backward 168) and shared memory allow.
+// The warps of a block, one block a multiprocessor, are a ring.  A warp has the copies of kStages tiles
+// under way or at work: as many as shared memory allows, with the warps that the registers allow.
 template <class T, bool BACKWARD>
 struct Block {
   static constexpr int kWarps = sizeof(T) == 4 ? 8 : BACKWARD ? 12 : 16;
@@ -86,16 +84,16 @@ constexpr int kWalkSmem =
 
 // A tile as its copies' issuer describes it to the same warp later.
 struct __align__(16) Tile {
-  int slot, row, valid, place;  // row: of its first token; place: of its state
-  int n, flags, map, part;
+  int valid, flags, slot, row;  // row: of its first token
+  int n, place, map, part;      // place: of its state
 };
 enum : int {
   kFresh = 1,   // the warp's first tile in the unit
   kFirst = 2,   // the segment's first tile of the walk
   kLast = 4,    // the segment's last tile of the walk
-  kBegin = 8,   // of the segment that the walk of the sequence begins with
-  kEnd = 16,    // of the segment that it ends with
-  kCut = 32,    // of a cut sequence
+  kEnd = 8,     // of the segment that the walk of the sequence ends with
+  kCut = 16,    // of a cut sequence
+  kStop = 32,   // the ring's last tile
   kOrder = 6    // flags >> kOrder: the segment's place in the walk of its sequence
 };
 
@@ -110,129 +108,194 @@ __device__ __forceinline__ const int4* record(const RecParams& p, int i) {
   return reinterpret_cast<const int4*>(p.plan + kRecHeader) + 2 * i;
 }
 
-// A warp's way through the tiles of its ring's units.  The units are dealt to the blocks in rounds,
-// every other one in reverse, so that with the plan's order (longest first) no block gets the longer
-// unit of every round; a block's rings take its rounds in turn.
-template <int K, bool BACKWARD>
+// A warp's way through the tiles of its block's units, and the copies of the next one.  The units
+// are dealt to the blocks in rounds, every other one in reverse, so that with the plan's order
+// (longest first) no block gets the longer unit of every round.  Lanes 0-15 copy the gates' rows and
+// lanes 16-31 those of x, one each, or the first of them all at once where the rows lie side by side.
+template <class T, int D, bool BACKWARD>
 struct Walk {
-  int4 r0, r1;  // the record: slot, start, len, tile; part, segment, segments, map
+  using B = Block<T, BACKWARD>;
+  static constexpr int K = Shape<D>::K, W = B::kWarps, kRow = D * (int)sizeof(T);
+  static constexpr int kSign = BACKWARD ? -1 : 1;
+  int slot, start, len, tile0;        // the record
+  int part, segment, segments, map;
   int n, t, tiles, round;
-  bool fresh, done;
+  bool fresh, done, whole, whole_dout;
+  const T *rows, *dout, *beta;        // the lane's, of the next tile
+  long long rows_step, dout_step, beta_step;
+  const float* state;
 
+  __device__ static long long unit_of(int round) {
+    return (long long)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  }
   // zero(slot, n, row, rows): called for the rows behind a sequence's last token
   template <class Zero>
-  __device__ void enter(const RecParams& p, int rings, Zero&& zero) {
-    for (;; round += rings) {
-      const long long base = (long long)round * gridDim.x;
-      const long long unit = base + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  __device__ void enter(const RecParams& p, Zero&& zero) {
+    const int lane = threadIdx.x & 31;
+    for (;; ++round) {
+      const long long unit = unit_of(round);
       done = unit >= p.units;
       if (done) return;
       const int i = (int)unit / p.N;
       n = (int)unit - i * p.N;
-      r0 = __ldg(record(p, i));
-      r1 = __ldg(record(p, i) + 1);
-      tiles = (r0.z + K - 1) / K;
-      fresh = true;
-      if (p.slot_rows && r1.y + 1 == r1.z) zero(r0.x, n, r0.y + r0.z, p.slot_rows - r0.y - r0.z);
-      if (t < tiles) return;
+      const int4 r0 = __ldg(record(p, i)), r1 = __ldg(record(p, i) + 1);
+      slot = r0.x; start = r0.y; len = r0.z; tile0 = r0.w;
+      part = r1.x; segment = r1.y; segments = r1.z; map = r1.w;
+      tiles = (len + K - 1) / K;
+      if (p.slot_rows && segment + 1 == segments)
+        zero(slot, n, start + len, p.slot_rows - start - len);
+      if (t < tiles) break;
       t -= tiles;
+    }
+    fresh = true;
+    const int k = BACKWARD ? tiles - 1 - t : t, row = start + k * K;
+    const kda_view_t& v = lane < 16 ? p.g : p.x;
+    rows = at<T>(v, slot, n, row) + (whole ? 0 : (lane & 15) * v.stride_s);
+    beta = at<T>(p.beta, slot, n, row) + lane * p.beta.stride_s;
+    if (BACKWARD) {
+      if (p.dout.data)
+        dout = at<T>(p.dout, slot, n, row) + (whole_dout ? 0 : lane * p.dout.stride_s);
+      state = p.states + ((size_t)(tile0 + k) * p.N + n) * D;
     }
   }
   template <class Zero>
-  __device__ void next(const RecParams& p, int rings, Zero&& zero) {
-    fresh = false;
-    t += p.ring;
-    if (t < tiles) return;
-    t -= tiles;
-    round += rings;
-    enter(p, rings, zero);
+  __device__ void begin(const RecParams& p, int warp, Zero&& zero) {
+    const bool low = (threadIdx.x & 31) < 16;
+    const long long stride = low ? p.g.stride_s : p.x.stride_s;
+    whole = stride == D;
+    rows_step = kSign * W * K * stride;
+    beta_step = kSign * W * K * p.beta.stride_s;
+    whole_dout = p.dout.stride_s == D;
+    dout_step = kSign * W * K * p.dout.stride_s;
+    dout = nullptr;
+    state = nullptr;
+    round = 0;
+    t = warp;
+    enter(p, zero);
   }
-  __device__ Tile tile(int* valid) const {
+  template <class Zero>
+  __device__ void next(const RecParams& p, Zero&& zero) {
+    fresh = false;
+    t += W;
+    if (t < tiles) {
+      rows += rows_step;
+      beta += beta_step;
+      if (BACKWARD) {
+        dout += dout_step;
+        state -= (size_t)W * p.N * D;
+      }
+      return;
+    }
+    t -= tiles;
+    ++round;
+    enter(p, zero);
+  }
+  // Describes the next tile and starts its copies to `stage`; returns the lane's write logit.
+  template <class Zero>
+  __device__ float issue(const RecParams& p, uint32_t stage, uint32_t bar, Tile* tile, Zero&& zero) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();  // all lanes have read what the stage held
+    if (done) {
+      if (lane == 0) tile->valid = 0;
+      return 0.f;
+    }
     const int k = BACKWARD ? tiles - 1 - t : t;
-    const int order = BACKWARD ? r1.z - 1 - r1.y : r1.y;
-    *valid = min(K, r0.z - k * K);
-    return {r0.x, r0.y + k * K, *valid, r0.w + k, n,
-            (fresh ? kFresh : 0) | (t == 0 ? kFirst : 0) | (t == tiles - 1 ? kLast : 0) |
-                (order == 0 ? kBegin : 0) | (order == r1.z - 1 ? kEnd : 0) |
-                (r1.z > 1 ? kCut : 0) | order << kOrder,
-            r1.w, r1.x + t};
+    const int valid = min(K, len - k * K);
+    if (lane == 0) {
+      const int order = BACKWARD ? segments - 1 - segment : segment;
+      const bool last = t == tiles - 1;
+      int4* const to = reinterpret_cast<int4*>(tile);
+      to[0] = make_int4(valid,
+                        (fresh ? kFresh : 0) | (t == 0 ? kFirst : 0) | (last ? kLast : 0) |
+                            (order == segments - 1 ? kEnd : 0) | (segments > 1 ? kCut : 0) |
+                            (last && unit_of(round + 1) >= p.units ? kStop : 0) | order << kOrder,
+                        slot, start + k * K);
+      if (fresh) to[1] = make_int4(n, tile0 + k, map, part + t);
+      mbar_arrive_expect_tx(bar, (BACKWARD && p.dout.data ? 3 : 2) * valid * kRow +
+                                     (BACKWARD ? D * (int)sizeof(float) : 0));
+    }
+    __syncwarp();
+    const int r = lane & 15, bytes = whole ? valid * kRow : kRow;
+    if (r < (whole ? 1 : valid))
+      bulk_load(stage + (lane < 16 ? 0 : K * kRow) + r * kRow, rows, bytes, bar);
+    if (BACKWARD) {
+      if (p.dout.data && lane < (whole_dout ? 1 : valid))
+        bulk_load(stage + (2 * K + lane) * kRow, dout, whole_dout ? valid * kRow : kRow, bar);
+      if (lane == 31) bulk_load(stage + 3 * K * kRow, state, D * 4, bar);
+    }
+    const float logit = lane < valid ? to_f32(__ldg(beta)) : 0.f;
+    next(p, zero);
+    return logit;
   }
 };
-
-// Starts the copies of a tile's rows of one tensor, a row a lane or, where the rows lie side by side,
-// all rows at once.
-template <class T, int D>
-__device__ __forceinline__ void copy_rows(uint32_t dst, const kda_view_t& v, const Tile& t,
-                                          int first_lane, int lane, uint32_t bar) {
-  const int k = lane - first_lane;
-  if (k < 0 || k >= t.valid) return;
-  const T* from = at<T>(v, t.slot, t.n, t.row);
-  if (v.stride_s == D) {
-    if (k == 0) bulk_load(dst, from, t.valid * D * (int)sizeof(T), bar);
-  } else {
-    bulk_load(dst + k * D * (int)sizeof(T), from + k * v.stride_s, D * (int)sizeof(T), bar);
-  }
-}
 
 // The state that a cut segment starts from: the maps of those before it in the walk's order, the
 // first of which is constant.
 template <int D>
-__device__ typename Shape<D>::F join(const RecParams& p, int map, int order, int n, int chan) {
-  constexpr int P = Shape<D>::V / 2;
-  auto s = splat<P>(0.f);
+__device__ __noinline__ Pairs<D / 64> join(const RecParams& p, int map, int order, int n, int chan) {
+  constexpr int P = D / 64;
+  using F = Pairs<P>;
+  F s = splat<P>(0.f);
   const float* m = p.maps + ((size_t)map * p.N + n) * 2 * D + chan;
-#pragma unroll 4
-  for (int k = 0; k <= order; ++k) {
-    s = fma(load<P>(m), s, load<P>(m + D));
-    m += (size_t)p.N * 2 * D;
+  const size_t row = (size_t)p.N * 2 * D;
+  constexpr int kAhead = 8;  // loads under way at a time
+  for (int k = 0; k <= order; k += kAhead) {
+    F a[kAhead], h[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const float* const from = m + min(k + i, order) * row;
+      a[i] = load<P>(from);
+      h[i] = load<P>(from + D);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (k + i <= order) s = fma(a[i], s, h[i]);
   }
   return s;
 }
 
-// What every warp of a walk sets up, and its waits.
-template <int STAGES>
+// What a warp of a walk waits with and hands over through.
+template <class T, int D, bool BACKWARD>
 struct Lines {
-  uint32_t full, mine, theirs;  // barriers: a stage is loaded; this warp's turn, the next one's
-  float* inbox;                 // the state handed to this warp, and to the next one
-  float* outbox;
+  using B = Block<T, BACKWARD>;
+  uint32_t full;          // barriers: a stage is loaded
+  float *inbox, *outbox;  // the state handed to this warp, and to the next one
+  int warp;
   bool failed;
-  __device__ void wait(uint32_t bar, uint32_t phase) {
-    if (!failed && !mbar_wait_bounded(bar, phase & 1, kWaitLimit)) failed = true;
+
+  __device__ Lines(int w) : warp(w), failed(false) {
+    __shared__ uint64_t bars[B::kWarps][B::kStages];
+    __shared__ __align__(16) float box[B::kWarps][D];
+    full = smem_u32(bars[warp]);
+    inbox = box[warp];
+    outbox = box[(warp + 1) % B::kWarps];
+    if ((threadIdx.x & 31) == 0) {
+      for (int s = 0; s < B::kStages; ++s) mbar_init(full + 8 * s, 1);
+      fence_barrier_init();
+    }
+    __syncthreads();
+  }
+  // After a wait that ran out the warp goes on without waiting, so that the others are not kept; the
+  // results are void and the status says so.
+  __device__ void wait_full(int stage, uint32_t use) {
+    if (!failed && !mbar_wait_bounded(full + 8 * stage, use & 1, kWaitLimit)) failed = true;
+  }
+  // The hand-over: a barrier of the two warps that only the later one waits at.
+  __device__ void wait_turn() const { named_bar_sync(warp, 64); }
+  __device__ void pass_turn() const { named_bar_arrive((warp + 1) % B::kWarps, 64); }
+  // The end: copies under way (of the uses from `i` on, after a failure) end before their memory may
+  // be left.
+  __device__ void close(const RecParams& p, const Tile* tiles, uint32_t i) const {
+    if (!failed) return;
+    if ((threadIdx.x & 31) == 0) atomicExch(p.status, DS_TIMEOUT);
+    for (int s = 0; s < B::kStages; ++s) {
+      // a stage's last use: the greatest j < i with j % kStages == s
+      if (i <= (uint32_t)s) continue;
+      const uint32_t j = (i - 1 - s) / B::kStages;
+      mbar_wait_bounded(full + 8 * s, j & 1, kWaitLimit);
+    }
   }
 };
-
-template <class T, int D, bool BACKWARD>
-__device__ __forceinline__ Lines<Block<T, BACKWARD>::kStages> lines(const RecParams& p, int warp,
-                                                                    int lane) {
-  using B = Block<T, BACKWARD>;
-  __shared__ uint64_t full[B::kWarps][B::kStages], turn[B::kWarps];
-  __shared__ __align__(16) float box[B::kWarps][D];
-  const int place = warp % p.ring, after = warp - place + (place + 1) % p.ring;
-  Lines<B::kStages> l;
-  l.full = smem_u32(full[warp]);
-  l.mine = smem_u32(&turn[warp]);
-  l.theirs = smem_u32(&turn[after]);
-  l.inbox = box[warp];
-  l.outbox = box[after];
-  l.failed = false;
-  if (lane == 0) {
-    for (int s = 0; s < B::kStages; ++s) mbar_init(l.full + 8 * s, 1);
-    mbar_init(l.mine, 1);
-    fence_barrier_init();
-  }
-  __syncthreads();
-  return l;
-}
-
-// A wait has run out: says so, and stays until the copies under way have ended.
-template <int STAGES>
-__device__ __noinline__ void give_up(const RecParams& p, const Lines<STAGES>& l, const Tile* tiles,
-                                     uint32_t i, int lane) {
-  if (lane == 0) atomicExch(p.status, DS_TIMEOUT);
-  for (uint32_t j = i; j < i + STAGES; ++j)
-    if (tiles[j % STAGES].valid)
-      mbar_wait_bounded(l.full + 8 * (j % STAGES), (j / STAGES) & 1, kWaitLimit);
-}
 
 // Rows of a partial tile that hold no token: closed gates (decay one) and zero writes.
 template <class T, int D, int TENSORS>
@@ -245,61 +308,55 @@ __device__ __noinline__ void fill_rows(T* stage, int valid) {
   fence_proxy_async_smem();  // a later copy writes these rows too
 }
 
+// Stores a tile's rows; `next` is the distance of two rows.
+template <class T, int D, int K, int P>
+__device__ __forceinline__ void store_rows(T* to, long long next, int valid, const Pairs<P> (&v)[K]) {
+  if (valid == K && next == D) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) store(to + k * D, v[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (k < valid) store(to, v[k]);
+      to += next;
+    }
+  }
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     rec_forward_kernel(const __grid_constant__ RecParams p) {
   using B = Block<T, false>;
   using S = Shape<D>;
   using F = typename S::F;
-  constexpr int K = S::K, V = S::V, P = V / 2, kStages = B::kStages;
+  constexpr int K = S::K, V = S::V, P = V / 2, kStages = B::kStages, W = B::kWarps;
   constexpr int kStage = kStageBytes<T, D, false>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Tile tiles[B::kWarps][kStages];
+  __shared__ Tile tiles[W][kStages];
   if (!same_plan(p)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
-  const int rings = B::kWarps / p.ring;
-  auto l = lines<T, D, false>(p, warp, lane);
+  Lines<T, D, false> lines(warp);
   uint8_t* const stages = smem + warp * kStages * kStage;
   T* const out = static_cast<T*>(p.out);
   const long long orow = p.od.stride_s;
-
-  Walk<K, false> walk;
   auto zero = [&](int slot, int n, int row, int rows) {
-    T* o = out + slot * p.od.stride_b + n * p.od.stride_n + row * orow + chan;
-    for (int k = warp % p.ring; k < rows; k += p.ring) store(o + k * orow, splat<P>(0.f));
+    T* const o = out + slot * p.od.stride_b + n * p.od.stride_n + row * orow + chan;
+    for (int k = warp; k < rows; k += W) store(o + k * orow, splat<P>(0.f));
   };
-  walk.round = warp / p.ring;
-  walk.t = warp % p.ring;
-  walk.enter(p, rings, zero);
-  // the copies of the next tile of the way; returns the lane's write logit of that tile
+  Walk<T, D, false> walk;
+  walk.begin(p, warp, zero);
   auto issue = [&](int s) {
-    __syncwarp();  // all lanes have read what the stage held
-    float logit = 0.f;
-    if (walk.done) {
-      if (lane == 0) tiles[warp][s].valid = 0;
-    } else {
-      int valid;
-      const Tile t = walk.tile(&valid);
-      const uint32_t bar = l.full + 8 * s, dst = smem_u32(stages + s * kStage);
-      if (lane == 0) {
-        tiles[warp][s] = t;
-        mbar_arrive_expect_tx(bar, 2 * valid * D * (int)sizeof(T));
-      }
-      __syncwarp();
-      copy_rows<T, D>(dst, p.g, t, 0, lane, bar);
-      copy_rows<T, D>(dst + kRecTileElems * sizeof(T), p.x, t, 16, lane, bar);
-      if (lane < valid) logit = to_f32(__ldg(at<T>(p.beta, t.slot, t.n, t.row + lane)));
-      walk.next(p, rings, zero);
-    }
-    return logit;
+    return walk.issue(p, smem_u32(stages + s * kStage), lines.full + 8 * s, &tiles[warp][s], zero);
   };
   float logits[kStages - 1];
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) logits[s] = issue(s);
 
   GateScale gc{};
-  F bias = splat<P>(0.f), h = splat<P>(0.f);
-  int s = 0, fill = kStages - 1;
+  F bias = splat<P>(0.f);
+  T* o = nullptr;
+  float* state = nullptr;
+  int slot = 0, n = 0, s = 0, fill = kStages - 1;
   uint32_t i = 0;
   for (;; ++i) {
     const float b = sigmoid(logits[0]);
@@ -308,20 +365,26 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     logits[kStages - 2] = issue(fill);
     fill = fill + 1 == kStages ? 0 : fill + 1;
     __syncwarp();
-    const Tile t = tiles[warp][s];
-    if (t.valid == 0) break;
-    if (t.flags & kFresh) {
-      gc = gate_scale(__ldg(p.A_log + t.n), p.lower_bound);
-      bias = load_const<P>(p.dt_bias + (size_t)t.n * D + chan);
+    const int4 t = *reinterpret_cast<const int4*>(&tiles[warp][s]);
+    const int valid = t.x, flags = t.y;
+    if (valid == 0) break;
+    if (flags & kFresh) {
+      const int4 u = reinterpret_cast<const int4*>(&tiles[warp][s])[1];
+      slot = t.z;
+      n = u.x;
+      gc = gate_scale(__ldg(p.A_log + n), p.lower_bound);
+      bias = load_const<P>(p.dt_bias + (size_t)n * D + chan);
+      o = out + slot * p.od.stride_b + n * p.od.stride_n + t.w * orow + chan;
+      state = p.states + ((size_t)u.y * p.N + n) * D + chan;
     }
     F start = splat<P>(0.f);
-    if (t.flags & kFirst) {
-      if (t.flags & kCut) start = join<D>(p, t.map, t.flags >> kOrder, t.n, chan);
-      else if (p.begin) start = load<P>(p.begin + ((size_t)t.slot * p.N + t.n) * D + chan);
+    if (flags & kFirst) {
+      if (flags & kCut) start = join<D>(p, tiles[warp][s].map, flags >> kOrder, n, chan);
+      else if (p.begin) start = load<P>(p.begin + ((size_t)slot * p.N + n) * D + chan);
     }
     T* const tg = reinterpret_cast<T*>(stages + s * kStage);
-    l.wait(l.full + 8 * s, i / kStages);
-    if (t.valid < K) fill_rows<T, D, 2>(tg, t.valid);
+    lines.wait_full(s, i / kStages);
+    if (valid < K) fill_rows<T, D, 2>(tg, valid);
 
     // decays and writes
     F a[K], u[K];
@@ -332,32 +395,27 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
       u[k] = load<P>(tg + kRecTileElems + k * D + chan) * __shfl_sync(0xffffffffu, b, k);
     }
     // the state before the tile
-    if (p.ring > 1 && (i > 0 || warp % p.ring > 0)) {
-      l.wait(l.mine, warp % p.ring > 0 ? i : i - 1);
-      h = load<P>(l.inbox + chan);
+    F h = start;
+    if (i > 0 || warp > 0) {
+      lines.wait_turn();
+      if (!(flags & kFirst)) h = load<P>(lines.inbox + chan);
     }
-    if (l.failed) break;
-    if (t.flags & kFirst) h = start;
     const F before = h;
 #pragma unroll
     for (int k = 0; k < K; ++k) h = u[k] = fma(a[k], h, u[k]);
-    if (p.ring > 1) {
-      store(l.outbox + chan, h);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(l.theirs);
+    store(lines.outbox + chan, h);
+    if (!(flags & kStop)) lines.pass_turn();
+    if (p.states) {
+      store(state, before);
+      state += (size_t)W * p.N * D;
     }
-    if (p.states) store(p.states + ((size_t)t.place * p.N + t.n) * D + chan, before);
-    T* o = out + t.slot * p.od.stride_b + t.n * p.od.stride_n + t.row * orow + chan;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      if (k < t.valid) store(o, u[k]);
-      o += orow;
-    }
-    if ((t.flags & (kLast | kEnd)) == (kLast | kEnd))
-      store(p.end + ((size_t)t.slot * p.N + t.n) * D + chan, h);
+    store_rows<T, D>(o, orow, valid, u);
+    o += W * K * orow;
+    if ((flags & (kLast | kEnd)) == (kLast | kEnd))
+      store(p.end + ((size_t)slot * p.N + n) * D + chan, h);
     s = s + 1 == kStages ? 0 : s + 1;
   }
-  if (l.failed) give_up(p, l, tiles[warp], i, lane);
+  lines.close(p, tiles[warp], i);
 }
 
 // Sums of K values over a warp, by halving the values as the distance halves: 32 / K lanes in a row
@@ -386,18 +444,14 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   using B = Block<T, true>;
   using S = Shape<D>;
   using F = typename S::F;
-  constexpr int K = S::K, V = S::V, P = V / 2, kStages = B::kStages;
+  constexpr int K = S::K, V = S::V, P = V / 2, kStages = B::kStages, W = B::kWarps;
   constexpr int kStage = kStageBytes<T, D, true>, kElems = kRecTileElems;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Tile tiles[B::kWarps][kStages];
+  __shared__ Tile tiles[W][kStages];
   if (!same_plan(p)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
-  const int rings = B::kWarps / p.ring;
-  auto l = lines<T, D, true>(p, warp, lane);
+  Lines<T, D, true> lines(warp);
   uint8_t* const stages = smem + warp * kStages * kStage;  // a stage: g, x, dout, state
-  T* const dx = static_cast<T*>(p.out);
-  T* const dg = static_cast<T*>(p.dg);
-  T* const dbeta = static_cast<T*>(p.dbeta);
   const long long orow = p.od.stride_s;
   if (!p.dout.data) {
     for (int s = 0; s < kStages; ++s)
@@ -405,44 +459,20 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
         store(reinterpret_cast<T*>(stages + s * kStage) + 2 * kElems + k * D + chan,
               splat<P>(0.f));
   }
-
-  Walk<K, true> walk;
   auto zero = [&](int slot, int n, int row, int rows) {
     const long long o = slot * p.od.stride_b + n * p.od.stride_n + row * orow + chan;
-    T* const ob = dbeta + slot * p.bd.stride_b + n * p.bd.stride_n + row * p.bd.stride_s;
-    for (int k = warp % p.ring; k < rows; k += p.ring) {
-      store(dx + o + k * orow, splat<P>(0.f));
-      store(dg + o + k * orow, splat<P>(0.f));
+    T* const ob = static_cast<T*>(p.dbeta) + slot * p.bd.stride_b + n * p.bd.stride_n +
+                  row * p.bd.stride_s;
+    for (int k = warp; k < rows; k += W) {
+      store(static_cast<T*>(p.out) + o + k * orow, splat<P>(0.f));
+      store(static_cast<T*>(p.dg) + o + k * orow, splat<P>(0.f));
       if (lane == 0) ob[k * p.bd.stride_s] = from_f32<T>(0.f);
     }
   };
-  walk.round = warp / p.ring;
-  walk.t = warp % p.ring;
-  walk.enter(p, rings, zero);
+  Walk<T, D, true> walk;
+  walk.begin(p, warp, zero);
   auto issue = [&](int s) {
-    __syncwarp();  // all lanes have read what the stage held
-    float logit = 0.f;
-    if (walk.done) {
-      if (lane == 0) tiles[warp][s].valid = 0;
-    } else {
-      int valid;
-      const Tile t = walk.tile(&valid);
-      const uint32_t bar = l.full + 8 * s, dst = smem_u32(stages + s * kStage);
-      if (lane == 0) {
-        tiles[warp][s] = t;
-        mbar_arrive_expect_tx(
-            bar, (p.dout.data ? 3 : 2) * valid * D * (int)sizeof(T) + D * (int)sizeof(float));
-      }
-      __syncwarp();
-      copy_rows<T, D>(dst, p.g, t, 0, lane, bar);
-      copy_rows<T, D>(dst + kElems * sizeof(T), p.x, t, 16, lane, bar);
-      if (p.dout.data) copy_rows<T, D>(dst + 2 * kElems * sizeof(T), p.dout, t, K == 8 ? 8 : 0, lane, bar);
-      if (lane == 31)
-        bulk_load(dst + 3 * kElems * sizeof(T), p.states + ((size_t)t.place * p.N + t.n) * D, D * 4, bar);
-      if (lane < valid) logit = to_f32(__ldg(at<T>(p.beta, t.slot, t.n, t.row + lane)));
-      walk.next(p, rings, zero);
-    }
-    return logit;
+    return walk.issue(p, smem_u32(stages + s * kStage), lines.full + 8 * s, &tiles[warp][s], zero);
   };
   float logits[kStages - 1];
 #pragma unroll
@@ -450,21 +480,22 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
 
   // the warp's part of the parameters' gradients in the unit, and where it goes
   F sum_b = splat<P>(0.f), sum_raw = splat<P>(0.f);
-  int part = -1, part_n = 0;
+  size_t part = 0;
   auto flush = [&]() {
-    if (part < 0) return;
     float raw = sum(sum_raw);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) raw += __shfl_xor_sync(0xffffffffu, raw, o);
-    const size_t to = (size_t)part * p.N + part_n;
-    store(p.part_bias + to * D + chan, sum_b);
-    if (lane == 0) p.part_A[to] = raw;
+    store(p.part_bias + part * D + chan, sum_b);
+    if (lane == 0) p.part_A[part] = raw;
     sum_b = sum_raw = splat<P>(0.f);
   };
 
   GateScale gc{};
-  F bias = splat<P>(0.f), c = splat<P>(0.f);
-  int s = 0, fill = kStages - 1;
+  F bias = splat<P>(0.f);
+  long long o = 0;        // of the tile's rows in dx and dg
+  T* dbeta = nullptr;     // of the lane's token
+  constexpr int kEach = 32 / K;  // lanes that end with the same token's sum
+  int slot = 0, n = 0, s = 0, fill = kStages - 1;
   uint32_t i = 0;
   for (;; ++i) {
     const float b_own = sigmoid(logits[0]), slope_own = b_own * sigmoid(-logits[0]);
@@ -473,25 +504,31 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
     logits[kStages - 2] = issue(fill);
     fill = fill + 1 == kStages ? 0 : fill + 1;
     __syncwarp();
-    const Tile t = tiles[warp][s];
-    if (t.valid == 0) break;
-    if (t.flags & kFresh) {
-      gc = gate_scale(__ldg(p.A_log + t.n), p.lower_bound);
-      bias = load_const<P>(p.dt_bias + (size_t)t.n * D + chan);
-      flush();
-      part = t.part;
-      part_n = t.n;
+    const int4 t = *reinterpret_cast<const int4*>(&tiles[warp][s]);
+    const int valid = t.x, flags = t.y;
+    if (valid == 0) break;
+    if (flags & kFresh) {
+      const int4 u = reinterpret_cast<const int4*>(&tiles[warp][s])[1];
+      if (i > 0) flush();
+      slot = t.z;
+      n = u.x;
+      part = (size_t)u.w * p.N + n;
+      gc = gate_scale(__ldg(p.A_log + n), p.lower_bound);
+      bias = load_const<P>(p.dt_bias + (size_t)n * D + chan);
+      o = slot * p.od.stride_b + n * p.od.stride_n + t.w * orow + chan;
+      dbeta = static_cast<T*>(p.dbeta) + slot * p.bd.stride_b + n * p.bd.stride_n +
+              (t.w + lane / kEach) * p.bd.stride_s;
     }
     F start = splat<P>(0.f);
-    if (t.flags & kFirst) {
-      if (t.flags & kCut) start = join<D>(p, t.map, t.flags >> kOrder, t.n, chan);
-      else if (p.begin) start = load<P>(p.begin + ((size_t)t.slot * p.N + t.n) * D + chan);
+    if (flags & kFirst) {
+      if (flags & kCut) start = join<D>(p, tiles[warp][s].map, flags >> kOrder, n, chan);
+      else if (p.begin) start = load<P>(p.begin + ((size_t)slot * p.N + n) * D + chan);
     }
     T* const tg = reinterpret_cast<T*>(stages + s * kStage);
     const T* const tx = tg + kElems + chan;
     const T* const td = tx + kElems;
-    l.wait(l.full + 8 * s, i / kStages);
-    if (t.valid < K) fill_rows<T, D, 3>(tg, t.valid);
+    lines.wait_full(s, i / kStages);
+    if (valid < K) fill_rows<T, D, 3>(tg, valid);
 
     // decays, and the factors w of dg = lam w
     F a[K], w[K];
@@ -509,12 +546,11 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
       h = fma(a[k], h, load<P>(tx + k * D) * __shfl_sync(0xffffffffu, b_own, k));
     }
     // a lam of the token behind the tile
-    if (p.ring > 1 && (i > 0 || warp % p.ring > 0)) {
-      l.wait(l.mine, warp % p.ring > 0 ? i : i - 1);
-      c = load<P>(l.inbox + chan);
+    F c = start;
+    if (i > 0 || warp > 0) {
+      lines.wait_turn();
+      if (!(flags & kFirst)) c = load<P>(lines.inbox + chan);
     }
-    if (l.failed) break;
-    if (t.flags & kFirst) c = start;
     // a becomes lam
 #pragma unroll
     for (int k = K - 1; k >= 0; --k) {
@@ -522,43 +558,34 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
       c = a[k] * lam;
       a[k] = lam;
     }
-    if (p.ring > 1) {
-      store(l.outbox + chan, c);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(l.theirs);
-    }
-    if ((t.flags & (kLast | kEnd)) == (kLast | kEnd) && p.end)
-      store(p.end + ((size_t)t.slot * p.N + t.n) * D + chan, c);
-    const long long o = t.slot * p.od.stride_b + t.n * p.od.stride_n + t.row * orow + chan;
-    T* ox = dx + o;
-    T* og = dg + o;
+    store(lines.outbox + chan, c);
+    if (!(flags & kStop)) lines.pass_turn();
+    if ((flags & (kLast | kEnd)) == (kLast | kEnd) && p.end)
+      store(p.end + ((size_t)slot * p.N + n) * D + chan, c);
     float dot[K];
     F here_b = splat<P>(0.f), here_raw = splat<P>(0.f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const F d = a[k] * w[k];
-      if (k < t.valid) {
-        store(ox, a[k] * __shfl_sync(0xffffffffu, b_own, k));
-        store(og, d);
-        here_b = here_b + d;
-        here_raw = fma(d, load<P>(tg + k * D + chan) + bias, here_raw);
-      }
+      // of rows behind the last token w is zero (the sigmoid is)
+      w[k] = a[k] * w[k];
+      here_b = here_b + w[k];
+      if (k < valid) here_raw = fma(w[k], load<P>(tg + k * D + chan) + bias, here_raw);
       dot[k] = sum(a[k] * load<P>(tx + k * D));
-      ox += orow;
-      og += orow;
+      a[k] = a[k] * __shfl_sync(0xffffffffu, b_own, k);
     }
+    store_rows<T, D>(static_cast<T*>(p.out) + o, orow, valid, a);
+    store_rows<T, D>(static_cast<T*>(p.dg) + o, orow, valid, w);
     sum_b = sum_b + here_b;
     sum_raw = sum_raw + here_raw;
-    constexpr int kEach = 32 / K;  // lanes that end with the same token
     const int k = lane / kEach;
     const float total = warp_sums<K>(dot, lane) * __shfl_sync(0xffffffffu, slope_own, k);
-    if (lane % kEach == 0 && k < t.valid)
-      dbeta[t.slot * p.bd.stride_b + t.n * p.bd.stride_n + (t.row + k) * p.bd.stride_s] =
-          from_f32<T>(total);
+    if (lane % kEach == 0 && k < valid) *dbeta = from_f32<T>(total);
+    o -= W * K * orow;
+    dbeta -= W * K * p.bd.stride_s;
     s = s + 1 == kStages ? 0 : s + 1;
   }
-  flush();
-  if (l.failed) give_up(p, l, tiles[warp], i, lane);
+  if (i > 0) flush();
+  lines.close(p, tiles[warp], i);
 }
 
 // The maps of the segments of cut sequences, one block each: row 0 of a sequence is its start, row
@@ -629,7 +656,7 @@ __global__ void __launch_bounds__(256) rec_maps_kernel(const __grid_constant__ R
 
 // ddt_bias and dA_log: the warps' parts in a fixed order, in fp64.  A block has 32 channels of a
 // head (the first one of a head its dA_log too); 32 threads a channel take the segments in turn.
-template <int D>
+template <int D, int W>
 __global__ void __launch_bounds__(1024) rec_params_kernel(const __grid_constant__ RecParams p,
                                                           float* dA_log, float* ddt_bias) {
   __shared__ double red[32][33];
@@ -640,7 +667,7 @@ __global__ void __launch_bounds__(1024) rec_params_kernel(const __grid_constant_
   double sum = 0, raw = 0;
   for (int k = row; k < records; k += 32) {
     const int4 r0 = __ldg(record(p, k)), r1 = __ldg(record(p, k) + 1);
-    const int parts = min(p.ring, (r0.z + K - 1) / K);
+    const int parts = min(W, (r0.z + K - 1) / K);
     const float* b = p.part_bias + ((size_t)r1.x * p.N + n) * D + d;
 #pragma unroll 4
     for (int i = 0; i < parts; ++i) sum += b[(size_t)i * p.N * D];
@@ -774,10 +801,7 @@ cudaError_t launch(Kernel kernel, PerDevice& once, RecParams& p, const int32_t* 
     return err == cudaSuccess ? cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, d) : err;
   });
   if (e != cudaSuccess) return e;
-  const int blocks = std::min(sms, p.units), rounds = (p.units - 1) / blocks + 1;
-  p.ring = B::kWarps;
-  while (p.ring > 1 && (B::kWarps % p.ring || p.ring * std::min(rounds, 2) > B::kWarps)) --p.ring;
-  if (const char* r = getenv(BACKWARD ? "RB" : "RF")) p.ring = atoi(r);
+  const int blocks = std::min(sms, p.units);
   if (plan[RH_MAPS]) {
     rec_maps_kernel<T, D, BACKWARD><<<(unsigned)p.units, 256, 0, s>>>(p);
     e = cudaGetLastError();
@@ -926,7 +950,7 @@ extern "C" kda_status_t kda_recurrence_backward(
     using T = std::remove_pointer_t<decltype(tag)>;
     const cudaError_t err = launch_backward<T, D>(p, plan_host, s);
     if (err != cudaSuccess) return err;
-    rec_params_kernel<D><<<(unsigned)shape->N * (D / 32), 1024, 0, s>>>(p, dA_log, ddt_bias);
+    rec_params_kernel<D, Block<T, true>::kWarps><<<(unsigned)shape->N * (D / 32), 1024, 0, s>>>(p, dA_log, ddt_bias);
     return cudaGetLastError();
   });
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
