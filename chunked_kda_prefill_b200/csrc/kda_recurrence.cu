@@ -30,8 +30,6 @@
 namespace kda {
 namespace {
 
-constexpr uint32_t kWaitLimit = 1u << 26;
-
 struct RecParams {
   kda_view_t x, g, beta, dout;  // device addresses and strides
   const int32_t* plan;
@@ -52,6 +50,9 @@ struct RecParams {
   float* part_bias;  // [RH_PARTS][N][D]
   float* part_A;     // [RH_PARTS][N]
   kda_view_t od, bd;  // strides of the dense outputs with and without channels
+  // bytes from a copy's rows to the next copy's, and from a warp's tile to its next one, of g, x, dout
+  // and (tiles only) beta
+  long long copy_step[3], tile_step[4];
 };
 
 template <class T>
@@ -108,25 +109,41 @@ __device__ __forceinline__ const int4* record(const RecParams& p, int i) {
   return reinterpret_cast<const int4*>(p.plan + kRecHeader) + 2 * i;
 }
 
+// 16 bytes from global to shared memory
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the warp's last PENDING groups of copies have arrived.
+template <int PENDING>
+__device__ __forceinline__ void copies_arrived() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+  __syncwarp();
+}
+
 // A warp's way through the tiles of its block's units, and the copies of the next one.  The units
 // are dealt to the blocks in rounds, every other one in reverse, so that with the plan's order
-// (longest first) no block gets the longer unit of every round.  Lanes 0-15 copy the gates' rows and
-// lanes 16-31 those of x, one each, or the first of them all at once where the rows lie side by side.
+// (longest first) no block gets the longer unit of every round.
 template <class T, int D, bool BACKWARD>
 struct Walk {
   using B = Block<T, BACKWARD>;
   static constexpr int K = Shape<D>::K, W = B::kWarps, kRow = D * (int)sizeof(T);
-  static constexpr int kSign = BACKWARD ? -1 : 1;
+  static constexpr int kLanes = kRow / 16;    // lanes of a row's copy
+  static constexpr int kRows = 32 / kLanes;   // rows of a copy
   int slot, start, len, tile0;        // the record
   int part, segment, segments, map;
   int n, t, tiles, round;
-  bool fresh, done, whole, whole_dout;
-  const T *rows, *dout, *beta;        // the lane's, of the next tile
-  long long rows_step, dout_step, beta_step;
-  const float* state;
+  bool fresh, done;
+  const char *g, *x, *dout, *beta, *state;  // the lane's, of the next tile
 
   __device__ static long long unit_of(int round) {
     return (long long)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  }
+  // the lane's part of a tile's first copy
+  __device__ const char* lane_rows(const kda_view_t& v, int row) const {
+    const int lane = threadIdx.x & 31;
+    return reinterpret_cast<const char*>(at<T>(v, slot, n, row + lane / kLanes)) +
+           lane % kLanes * 16;
   }
   // zero(slot, n, row, rows): called for the rows behind a sequence's last token
   template <class Zero>
@@ -149,26 +166,17 @@ struct Walk {
     }
     fresh = true;
     const int k = BACKWARD ? tiles - 1 - t : t, row = start + k * K;
-    const kda_view_t& v = lane < 16 ? p.g : p.x;
-    rows = at<T>(v, slot, n, row) + (whole ? 0 : (lane & 15) * v.stride_s);
-    beta = at<T>(p.beta, slot, n, row) + lane * p.beta.stride_s;
+    g = lane_rows(p.g, row);
+    x = lane_rows(p.x, row);
+    beta = reinterpret_cast<const char*>(at<T>(p.beta, slot, n, row + lane));
     if (BACKWARD) {
-      if (p.dout.data)
-        dout = at<T>(p.dout, slot, n, row) + (whole_dout ? 0 : lane * p.dout.stride_s);
-      state = p.states + ((size_t)(tile0 + k) * p.N + n) * D;
+      if (p.dout.data) dout = lane_rows(p.dout, row);
+      state = reinterpret_cast<const char*>(p.states + ((size_t)(tile0 + k) * p.N + n) * D) + lane * 16;
     }
   }
   template <class Zero>
   __device__ void begin(const RecParams& p, int warp, Zero&& zero) {
-    const bool low = (threadIdx.x & 31) < 16;
-    const long long stride = low ? p.g.stride_s : p.x.stride_s;
-    whole = stride == D;
-    rows_step = kSign * W * K * stride;
-    beta_step = kSign * W * K * p.beta.stride_s;
-    whole_dout = p.dout.stride_s == D;
-    dout_step = kSign * W * K * p.dout.stride_s;
-    dout = nullptr;
-    state = nullptr;
+    dout = state = nullptr;
     round = 0;
     t = warp;
     enter(p, zero);
@@ -178,11 +186,12 @@ struct Walk {
     fresh = false;
     t += W;
     if (t < tiles) {
-      rows += rows_step;
-      beta += beta_step;
+      g += p.tile_step[0];
+      x += p.tile_step[1];
+      beta += p.tile_step[3];
       if (BACKWARD) {
-        dout += dout_step;
-        state -= (size_t)W * p.N * D;
+        dout += p.tile_step[2];
+        state -= (size_t)W * p.N * D * 4;
       }
       return;
     }
@@ -190,41 +199,48 @@ struct Walk {
     ++round;
     enter(p, zero);
   }
+  __device__ static void copy_rows(uint32_t to, const char* from, long long step, int valid) {
+    const int lane = threadIdx.x & 31;
+    to += lane * 16;
+#pragma unroll
+    for (int k = 0; k < K; k += kRows) {
+      if (valid == K || k + lane / kLanes < valid) copy16(to + k * kRow, from);
+      from += step;
+    }
+  }
   // Describes the next tile and starts its copies to `stage`; returns the lane's write logit.
   template <class Zero>
-  __device__ float issue(const RecParams& p, uint32_t stage, uint32_t bar, Tile* tile, Zero&& zero) {
+  __device__ float issue(const RecParams& p, uint32_t stage, Tile* tile, Zero&& zero) {
     const int lane = threadIdx.x & 31;
     __syncwarp();  // all lanes have read what the stage held
+    float logit = 0.f;
     if (done) {
       if (lane == 0) tile->valid = 0;
-      return 0.f;
+    } else {
+      const int k = BACKWARD ? tiles - 1 - t : t;
+      const int valid = min(K, len - k * K);
+      if (lane == 0) {
+        const int order = BACKWARD ? segments - 1 - segment : segment;
+        const bool last = t == tiles - 1;
+        int4* const to = reinterpret_cast<int4*>(tile);
+        to[0] = make_int4(valid,
+                          (fresh ? kFresh : 0) | (t == 0 ? kFirst : 0) | (last ? kLast : 0) |
+                              (order == segments - 1 ? kEnd : 0) | (segments > 1 ? kCut : 0) |
+                              (last && unit_of(round + 1) >= p.units ? kStop : 0) |
+                              order << kOrder,
+                          slot, start + k * K);
+        if (fresh) to[1] = make_int4(n, tile0 + k, map, part + t);
+      }
+      copy_rows(stage, g, p.copy_step[0], valid);
+      copy_rows(stage + K * kRow, x, p.copy_step[1], valid);
+      if (BACKWARD) {
+        if (p.dout.data) copy_rows(stage + 2 * K * kRow, dout, p.copy_step[2], valid);
+        if (lane < D / 4) copy16(stage + 3 * K * kRow + lane * 16, state);
+      }
+      if (lane < valid) logit = to_f32(__ldg(reinterpret_cast<const T*>(beta)));
+      next(p, zero);
     }
-    const int k = BACKWARD ? tiles - 1 - t : t;
-    const int valid = min(K, len - k * K);
-    if (lane == 0) {
-      const int order = BACKWARD ? segments - 1 - segment : segment;
-      const bool last = t == tiles - 1;
-      int4* const to = reinterpret_cast<int4*>(tile);
-      to[0] = make_int4(valid,
-                        (fresh ? kFresh : 0) | (t == 0 ? kFirst : 0) | (last ? kLast : 0) |
-                            (order == segments - 1 ? kEnd : 0) | (segments > 1 ? kCut : 0) |
-                            (last && unit_of(round + 1) >= p.units ? kStop : 0) | order << kOrder,
-                        slot, start + k * K);
-      if (fresh) to[1] = make_int4(n, tile0 + k, map, part + t);
-      mbar_arrive_expect_tx(bar, (BACKWARD && p.dout.data ? 3 : 2) * valid * kRow +
-                                     (BACKWARD ? D * (int)sizeof(float) : 0));
-    }
-    __syncwarp();
-    const int r = lane & 15, bytes = whole ? valid * kRow : kRow;
-    if (r < (whole ? 1 : valid))
-      bulk_load(stage + (lane < 16 ? 0 : K * kRow) + r * kRow, rows, bytes, bar);
-    if (BACKWARD) {
-      if (p.dout.data && lane < (whole_dout ? 1 : valid))
-        bulk_load(stage + (2 * K + lane) * kRow, dout, whole_dout ? valid * kRow : kRow, bar);
-      if (lane == 31) bulk_load(stage + 3 * K * kRow, state, D * 4, bar);
-    }
-    const float logit = lane < valid ? to_f32(__ldg(beta)) : 0.f;
-    next(p, zero);
+    copies_issued();
     return logit;
   }
 };
@@ -254,47 +270,19 @@ __device__ __noinline__ Pairs<D / 64> join(const RecParams& p, int map, int orde
   return s;
 }
 
-// What a warp of a walk waits with and hands over through.
-template <class T, int D, bool BACKWARD>
-struct Lines {
-  using B = Block<T, BACKWARD>;
-  uint32_t full;          // barriers: a stage is loaded
+// A warp's place in its block's ring: the state is handed on through shared memory, with a barrier of
+// the two warps that only the later one waits at.
+template <int W, int D>
+struct Ring {
   float *inbox, *outbox;  // the state handed to this warp, and to the next one
   int warp;
-  bool failed;
-
-  __device__ Lines(int w) : warp(w), failed(false) {
-    __shared__ uint64_t bars[B::kWarps][B::kStages];
-    __shared__ __align__(16) float box[B::kWarps][D];
-    full = smem_u32(bars[warp]);
+  __device__ explicit Ring(int w) : warp(w) {
+    __shared__ __align__(16) float box[W][D];
     inbox = box[warp];
-    outbox = box[(warp + 1) % B::kWarps];
-    if ((threadIdx.x & 31) == 0) {
-      for (int s = 0; s < B::kStages; ++s) mbar_init(full + 8 * s, 1);
-      fence_barrier_init();
-    }
-    __syncthreads();
+    outbox = box[(warp + 1) % W];
   }
-  // After a wait that ran out the warp goes on without waiting, so that the others are not kept; the
-  // results are void and the status says so.
-  __device__ void wait_full(int stage, uint32_t use) {
-    if (!failed && !mbar_wait_bounded(full + 8 * stage, use & 1, kWaitLimit)) failed = true;
-  }
-  // The hand-over: a barrier of the two warps that only the later one waits at.
-  __device__ void wait_turn() const { named_bar_sync(warp, 64); }
-  __device__ void pass_turn() const { named_bar_arrive((warp + 1) % B::kWarps, 64); }
-  // The end: copies under way (of the uses from `i` on, after a failure) end before their memory may
-  // be left.
-  __device__ void close(const RecParams& p, const Tile* tiles, uint32_t i) const {
-    if (!failed) return;
-    if ((threadIdx.x & 31) == 0) atomicExch(p.status, DS_TIMEOUT);
-    for (int s = 0; s < B::kStages; ++s) {
-      // a stage's last use: the greatest j < i with j % kStages == s
-      if (i <= (uint32_t)s) continue;
-      const uint32_t j = (i - 1 - s) / B::kStages;
-      mbar_wait_bounded(full + 8 * s, j & 1, kWaitLimit);
-    }
-  }
+  __device__ void wait() const { named_bar_sync(warp, 64); }
+  __device__ void pass() const { named_bar_arrive((warp + 1) % W, 64); }
 };
 
 // Rows of a partial tile that hold no token: closed gates (decay one) and zero writes.
@@ -305,7 +293,6 @@ __device__ __noinline__ void fill_rows(T* stage, int valid) {
   for (int k = valid; k < S::K; ++k)
     for (int i = 0; i < TENSORS; ++i)
       store(stage + i * kRecTileElems + k * D + chan, splat<S::V / 2>(i == 0 ? -INFINITY : 0.f));
-  fence_proxy_async_smem();  // a later copy writes these rows too
 }
 
 // Stores a tile's rows; `next` is the distance of two rows.
@@ -335,7 +322,7 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
   __shared__ Tile tiles[W][kStages];
   if (!same_plan(p)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
-  Lines<T, D, false> lines(warp);
+  const Ring<W, D> ring(warp);
   uint8_t* const stages = smem + warp * kStages * kStage;
   T* const out = static_cast<T*>(p.out);
   const long long orow = p.od.stride_s;
@@ -346,7 +333,7 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
   Walk<T, D, false> walk;
   walk.begin(p, warp, zero);
   auto issue = [&](int s) {
-    return walk.issue(p, smem_u32(stages + s * kStage), lines.full + 8 * s, &tiles[warp][s], zero);
+    return walk.issue(p, smem_u32(stages + s * kStage), &tiles[warp][s], zero);
   };
   float logits[kStages - 1];
 #pragma unroll
@@ -357,8 +344,7 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
   T* o = nullptr;
   float* state = nullptr;
   int slot = 0, n = 0, s = 0, fill = kStages - 1;
-  uint32_t i = 0;
-  for (;; ++i) {
+  for (bool begun = warp > 0;; begun = true) {  // the ring's first tile has none before it
     const float b = sigmoid(logits[0]);
 #pragma unroll
     for (int k = 0; k + 1 < kStages - 1; ++k) logits[k] = logits[k + 1];
@@ -383,7 +369,7 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
       else if (p.begin) start = load<P>(p.begin + ((size_t)slot * p.N + n) * D + chan);
     }
     T* const tg = reinterpret_cast<T*>(stages + s * kStage);
-    lines.wait_full(s, i / kStages);
+    copies_arrived<kStages - 1>();
     if (valid < K) fill_rows<T, D, 2>(tg, valid);
 
     // decays and writes
@@ -396,15 +382,15 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     }
     // the state before the tile
     F h = start;
-    if (i > 0 || warp > 0) {
-      lines.wait_turn();
-      if (!(flags & kFirst)) h = load<P>(lines.inbox + chan);
+    if (begun) {
+      ring.wait();
+      if (!(flags & kFirst)) h = load<P>(ring.inbox + chan);
     }
     const F before = h;
 #pragma unroll
     for (int k = 0; k < K; ++k) h = u[k] = fma(a[k], h, u[k]);
-    store(lines.outbox + chan, h);
-    if (!(flags & kStop)) lines.pass_turn();
+    store(ring.outbox + chan, h);
+    if (!(flags & kStop)) ring.pass();
     if (p.states) {
       store(state, before);
       state += (size_t)W * p.N * D;
@@ -415,7 +401,6 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
       store(p.end + ((size_t)slot * p.N + n) * D + chan, h);
     s = s + 1 == kStages ? 0 : s + 1;
   }
-  lines.close(p, tiles[warp], i);
 }
 
 // Sums of K values over a warp, by halving the values as the distance halves: 32 / K lanes in a row
@@ -450,7 +435,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   __shared__ Tile tiles[W][kStages];
   if (!same_plan(p)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
-  Lines<T, D, true> lines(warp);
+  const Ring<W, D> ring(warp);
   uint8_t* const stages = smem + warp * kStages * kStage;  // a stage: g, x, dout, state
   const long long orow = p.od.stride_s;
   if (!p.dout.data) {
@@ -472,7 +457,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   Walk<T, D, true> walk;
   walk.begin(p, warp, zero);
   auto issue = [&](int s) {
-    return walk.issue(p, smem_u32(stages + s * kStage), lines.full + 8 * s, &tiles[warp][s], zero);
+    return walk.issue(p, smem_u32(stages + s * kStage), &tiles[warp][s], zero);
   };
   float logits[kStages - 1];
 #pragma unroll
@@ -480,7 +465,8 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
 
   // the warp's part of the parameters' gradients in the unit, and where it goes
   F sum_b = splat<P>(0.f), sum_raw = splat<P>(0.f);
-  size_t part = 0;
+  constexpr size_t kNone = ~(size_t)0;
+  size_t part = kNone;
   auto flush = [&]() {
     float raw = sum(sum_raw);
 #pragma unroll
@@ -496,8 +482,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   T* dbeta = nullptr;     // of the lane's token
   constexpr int kEach = 32 / K;  // lanes that end with the same token's sum
   int slot = 0, n = 0, s = 0, fill = kStages - 1;
-  uint32_t i = 0;
-  for (;; ++i) {
+  for (bool begun = warp > 0;; begun = true) {  // the ring's first tile has none before it
     const float b_own = sigmoid(logits[0]), slope_own = b_own * sigmoid(-logits[0]);
 #pragma unroll
     for (int k = 0; k + 1 < kStages - 1; ++k) logits[k] = logits[k + 1];
@@ -509,7 +494,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
     if (valid == 0) break;
     if (flags & kFresh) {
       const int4 u = reinterpret_cast<const int4*>(&tiles[warp][s])[1];
-      if (i > 0) flush();
+      if (part != kNone) flush();
       slot = t.z;
       n = u.x;
       part = (size_t)u.w * p.N + n;
@@ -527,7 +512,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
     T* const tg = reinterpret_cast<T*>(stages + s * kStage);
     const T* const tx = tg + kElems + chan;
     const T* const td = tx + kElems;
-    lines.wait_full(s, i / kStages);
+    copies_arrived<kStages - 1>();
     if (valid < K) fill_rows<T, D, 3>(tg, valid);
 
     // decays, and the factors w of dg = lam w
@@ -547,9 +532,9 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
     }
     // a lam of the token behind the tile
     F c = start;
-    if (i > 0 || warp > 0) {
-      lines.wait_turn();
-      if (!(flags & kFirst)) c = load<P>(lines.inbox + chan);
+    if (begun) {
+      ring.wait();
+      if (!(flags & kFirst)) c = load<P>(ring.inbox + chan);
     }
     // a becomes lam
 #pragma unroll
@@ -558,8 +543,8 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
       c = a[k] * lam;
       a[k] = lam;
     }
-    store(lines.outbox + chan, c);
-    if (!(flags & kStop)) lines.pass_turn();
+    store(ring.outbox + chan, c);
+    if (!(flags & kStop)) ring.pass();
     if ((flags & (kLast | kEnd)) == (kLast | kEnd) && p.end)
       store(p.end + ((size_t)slot * p.N + n) * D + chan, c);
     float dot[K];
@@ -584,8 +569,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
     dbeta -= W * K * p.bd.stride_s;
     s = s + 1 == kStages ? 0 : s + 1;
   }
-  if (i > 0) flush();
-  lines.close(p, tiles[warp], i);
+  if (part != kNone) flush();
 }
 
 // The maps of the segments of cut sequences, one block each: row 0 of a sequence is its start, row
@@ -802,6 +786,13 @@ cudaError_t launch(Kernel kernel, PerDevice& once, RecParams& p, const int32_t* 
   });
   if (e != cudaSuccess) return e;
   const int blocks = std::min(sms, p.units);
+  constexpr int K = Shape<D>::K, kCopy = 512 / (D * (int)sizeof(T));
+  const kda_view_t* const views[] = {&p.g, &p.x, &p.dout, &p.beta};
+  for (int i = 0; i < 4; ++i) {
+    const long long row = views[i]->stride_s * (long long)sizeof(T);
+    if (i < 3) p.copy_step[i] = kCopy * row;
+    p.tile_step[i] = (BACKWARD ? -B::kWarps : B::kWarps) * K * row;
+  }
   if (plan[RH_MAPS]) {
     rec_maps_kernel<T, D, BACKWARD><<<(unsigned)p.units, 256, 0, s>>>(p);
     e = cudaGetLastError();
