@@ -67,7 +67,8 @@ def launch_on(device: torch.device, stream):
     """(context, cuda stream handle): inside the context the call's device is the current one, and
     what is allocated belongs to the stream that the kernels run on."""
     if stream is None and device.index == torch.cuda.current_device():
-        return _here, torch.cuda.current_stream(device).cuda_stream
+        # the handle alone: a Stream object would cost a call 2 us
+        return _here, torch._C._cuda_getCurrentRawStream(device.index)
     s = stream if stream is not None else torch.cuda.current_stream(device)
     if s.device != device:
         raise ValueError(f"stream is on {s.device}, the tensors on {device}")
@@ -75,4 +76,12 @@ def launch_on(device: torch.device, stream):
 
 
 def needs_grad(*tensors) -> bool:
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            return torch.is_grad_enabled()
+    return False
+
+
+def dense_like(t: torch.Tensor) -> torch.Tensor:
+    """An empty dense tensor of t's shape, type and device (less than half the time of empty())."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)

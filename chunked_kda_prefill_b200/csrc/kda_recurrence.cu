@@ -40,7 +40,7 @@ struct RecParams {
   const float* A_log;
   const float* dt_bias;
   float lower_bound;
-  int32_t* status;
+  int32_t* status;  // or null
   float* maps;    // [RH_MAPS][N][2][D] of the cut sequences
   float* states;  // [tiles][N][D] the states before the tiles: forward writes, backward reads
   void* out;      // forward: out; backward: dx
@@ -101,12 +101,21 @@ enum : int {
 // Whether the plan on the device is the host's; block 0 leaves the status.
 __device__ __forceinline__ bool same_plan(const RecParams& p) {
   const bool same = p.plan[RH_CHECKSUM] == p.checksum;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = same ? DS_OK : DS_PLAN;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) *p.status = same ? DS_OK : DS_PLAN;
   return same;
 }
 
 __device__ __forceinline__ const int4* record(const RecParams& p, int i) {
   return reinterpret_cast<const int4*>(p.plan + kRecHeader) + 2 * i;
+}
+
+// Kernels of a call that follow one another start while the one before is still running
+// (programmatic dependent launch), and wait for its end before they read what it writes.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_dependencies() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // 16 bytes from global to shared memory
@@ -252,6 +261,7 @@ __device__ __noinline__ Pairs<D / 64> join(const RecParams& p, int map, int orde
   constexpr int P = D / 64;
   using F = Pairs<P>;
   F s = splat<P>(0.f);
+  wait_dependencies();
   const float* m = p.maps + ((size_t)map * p.N + n) * 2 * D + chan;
   const size_t row = (size_t)p.N * 2 * D;
   constexpr int kAhead = 8;  // loads under way at a time
@@ -372,13 +382,18 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     copies_arrived<kStages - 1>();
     if (valid < K) fill_rows<T, D, 2>(tg, valid);
 
-    // decays and writes
+    // decays and writes, and what the tile makes of a state of zero; a becomes the decay since the
+    // tile's start
     F a[K], u[K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const F e = each((load<P>(tg + k * D + chan) + bias) * gc.nz, ex2);
       a[k] = each(each(e + splat<P>(1.f), rcp) * gc.l2, ex2);
       u[k] = load<P>(tg + kRecTileElems + k * D + chan) * __shfl_sync(0xffffffffu, b, k);
+      if (k > 0) {
+        u[k] = fma(a[k], u[k - 1], u[k]);
+        a[k] = a[k] * a[k - 1];
+      }
     }
     // the state before the tile
     F h = start;
@@ -387,10 +402,12 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
       if (!(flags & kFirst)) h = load<P>(ring.inbox + chan);
     }
     const F before = h;
-#pragma unroll
-    for (int k = 0; k < K; ++k) h = u[k] = fma(a[k], h, u[k]);
+    h = fma(a[K - 1], h, u[K - 1]);
     store(ring.outbox + chan, h);
     if (!(flags & kStop)) ring.pass();
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) u[k] = fma(a[k], before, u[k]);
+    u[K - 1] = h;
     if (p.states) {
       store(state, before);
       state += (size_t)W * p.N * D;
@@ -433,6 +450,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   constexpr int kStage = kStageBytes<T, D, true>, kElems = kRecTileElems;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Tile tiles[W][kStages];
+  launch_dependents();
   if (!same_plan(p)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
   const Ring<W, D> ring(warp);
@@ -530,21 +548,27 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
       w[k] = sig * (e * sig) * (a[k] * slope) * h;
       h = fma(a[k], h, load<P>(tx + k * D) * __shfl_sync(0xffffffffu, b_own, k));
     }
+    // lam of a tile with nothing behind it, and the decays from its end
+    F lam[K], c0 = splat<P>(0.f);
+#pragma unroll
+    for (int k = K - 1; k >= 0; --k) {
+      lam[k] = load<P>(td + k * D) + c0;
+      c0 = a[k] * lam[k];
+      if (k < K - 1) a[k] = a[k] * a[k + 1];
+    }
     // a lam of the token behind the tile
     F c = start;
     if (begun) {
       ring.wait();
       if (!(flags & kFirst)) c = load<P>(ring.inbox + chan);
     }
-    // a becomes lam
-#pragma unroll
-    for (int k = K - 1; k >= 0; --k) {
-      const F lam = load<P>(td + k * D) + c;
-      c = a[k] * lam;
-      a[k] = lam;
-    }
+    const F behind = c;
+    c = fma(a[0], c, c0);
     store(ring.outbox + chan, c);
     if (!(flags & kStop)) ring.pass();
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k) lam[k] = fma(a[k + 1], behind, lam[k]);
+    lam[K - 1] = lam[K - 1] + behind;
     if ((flags & (kLast | kEnd)) == (kLast | kEnd) && p.end)
       store(p.end + ((size_t)slot * p.N + n) * D + chan, c);
     float dot[K];
@@ -552,13 +576,13 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       // of rows behind the last token w is zero (the sigmoid is)
-      w[k] = a[k] * w[k];
+      w[k] = lam[k] * w[k];
       here_b = here_b + w[k];
       if (k < valid) here_raw = fma(w[k], load<P>(tg + k * D + chan) + bias, here_raw);
-      dot[k] = sum(a[k] * load<P>(tx + k * D));
-      a[k] = a[k] * __shfl_sync(0xffffffffu, b_own, k);
+      dot[k] = sum(lam[k] * load<P>(tx + k * D));
+      lam[k] = lam[k] * __shfl_sync(0xffffffffu, b_own, k);
     }
-    store_rows<T, D>(static_cast<T*>(p.out) + o, orow, valid, a);
+    store_rows<T, D>(static_cast<T*>(p.out) + o, orow, valid, lam);
     store_rows<T, D>(static_cast<T*>(p.dg) + o, orow, valid, w);
     sum_b = sum_b + here_b;
     sum_raw = sum_raw + here_raw;
@@ -572,48 +596,69 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   if (part != kNone) flush();
 }
 
+constexpr int kMapWarps = 16;
+
 // The maps of the segments of cut sequences, one block each: row 0 of a sequence is its start, row
-// k + 1 the map of the walk's k-th segment (the last one's is not needed).  A warp takes an eighth
-// of the tokens.
+// k + 1 the map of the walk's k-th segment (the last one's is not needed).  A warp takes a
+// sixteenth of the tokens, a batch at a time with the next one's loads under way.
 template <class T, int D, bool BACKWARD>
-__global__ void __launch_bounds__(256) rec_maps_kernel(const __grid_constant__ RecParams p) {
+__global__ void __launch_bounds__(32 * kMapWarps, 1) rec_maps_kernel(const __grid_constant__ RecParams p) {
   using S = Shape<D>;
   using F = typename S::F;
-  constexpr int V = S::V, P = V / 2;
-  __shared__ __align__(16) float sa[8][D], sh[8][D];
+  constexpr int V = S::V, P = V / 2, kBatch = 16 / (int)sizeof(T);
+  __shared__ __align__(16) float sa[kMapWarps][D], sh[kMapWarps][D];
+  launch_dependents();
   if (p.plan[RH_CHECKSUM] != p.checksum) return;
   const int i = blockIdx.x / p.N, n = blockIdx.x - i * p.N;
   const int4 r0 = __ldg(record(p, i)), r1 = __ldg(record(p, i) + 1);
   const int order = BACKWARD ? r1.z - 1 - r1.y : r1.y;
   if (order + 1 == r1.z) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
-  const GateScale gc = gate_scale(__ldg(p.A_log + n), p.lower_bound);
-  const F bias = load_const<P>(p.dt_bias + (size_t)n * D + chan);
   const kda_view_t& second = BACKWARD ? p.dout : p.x;
-  const int each_warp = (r0.z + 7) / 8, lo = min(r0.z, warp * each_warp), hi = min(r0.z, lo + each_warp);
+  const bool have = second.data != nullptr;
+  const int share = (r0.z + kMapWarps - 1) / kMapWarps, lo = min(r0.z, warp * share), count = min(r0.z - lo, share);
+  // the walk's first token of the share, and the way to the next one
+  const int first = r0.y + (BACKWARD ? lo + count - 1 : lo), step = BACKWARD ? -1 : 1;
   F pa = splat<P>(1.f), ph = splat<P>(0.f);
-  for (int c0 = 0; c0 < hi - lo; c0 += 32) {
-    // up to 32 tokens, in the walk's order
-    const int count = min(32, hi - lo - c0), first = BACKWARD ? hi - 1 - c0 : lo + c0;
-    const int step = BACKWARD ? -1 : 1;
-    float b = 0.f;
-    if (!BACKWARD && lane < count)
-      b = sigmoid(to_f32(__ldg(at<T>(p.beta, r0.x, n, r0.y + first + lane))));
-    const T* g = at<T>(p.g, r0.x, n, r0.y + first) + chan;
-    const T* x = second.data ? at<T>(second, r0.x, n, r0.y + first) + chan : nullptr;
-#pragma unroll 8
-    for (int k = 0; k < count; ++k) {
-      const F raw = load_const<P>(g) + bias;
-      F v = x ? load_const<P>(x) : splat<P>(0.f);
-      const F a = each(each(each(raw * gc.nz, ex2) + splat<P>(1.f), rcp) * gc.l2, ex2);
-      pa = pa * a;
-      if (BACKWARD) {
-        ph = a * (ph + v);
-      } else {
-        ph = fma(a, ph, v * __shfl_sync(0xffffffffu, b, k));
+  if (count > 0) {
+    const T* const g = at<T>(p.g, r0.x, n, first) + chan;
+    const T* const x = have ? at<T>(second, r0.x, n, first) + chan : nullptr;
+    const T* const beta = at<T>(p.beta, r0.x, n, first);
+    struct Batch {
+      Bits<T, V> g[kBatch], x[kBatch];
+      float logit;
+    };
+    auto fetch = [&](int from) {
+      Batch b;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const long long token = step * min(from + k, count - 1);
+        b.g[k] = __ldg(reinterpret_cast<const Bits<T, V>*>(g + token * p.g.stride_s));
+        b.x[k] = Bits<T, V>{};
+        if (have) b.x[k] = __ldg(reinterpret_cast<const Bits<T, V>*>(x + token * second.stride_s));
       }
-      g += step * p.g.stride_s;
-      if (x) x += step * second.stride_s;
+      b.logit = 0.f;
+      if (!BACKWARD && from + lane < count && lane < kBatch)
+        b.logit = to_f32(__ldg(beta + (long long)(from + lane) * p.beta.stride_s));
+      return b;
+    };
+    Batch now = fetch(0);
+    const GateScale gc = gate_scale(__ldg(p.A_log + n), p.lower_bound);
+    const F bias = load_const<P>(p.dt_bias + (size_t)n * D + chan);
+    for (int from = 0; from < count; from += kBatch) {
+      const Batch next = fetch(min(from + kBatch, count - 1));
+      const float own = BACKWARD ? 0.f : sigmoid(now.logit);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float b = BACKWARD ? 0.f : __shfl_sync(0xffffffffu, own, k);
+        if (from + k < count) {
+          const F raw = widen<T, V>(now.g[k]) + bias, v = widen<T, V>(now.x[k]);
+          const F a = each(each(each(raw * gc.nz, ex2) + splat<P>(1.f), rcp) * gc.l2, ex2);
+          pa = pa * a;
+          ph = BACKWARD ? a * (ph + v) : fma(a, ph, v * b);
+        }
+      }
+      now = next;
     }
   }
   store(&sa[warp][chan], pa);
@@ -622,8 +667,9 @@ __global__ void __launch_bounds__(256) rec_maps_kernel(const __grid_constant__ R
   if (warp > 0) return;
   pa = splat<P>(1.f);
   ph = splat<P>(0.f);
-  for (int k = 0; k < 8; ++k) {
-    const int w = BACKWARD ? 7 - k : k;
+#pragma unroll
+  for (int k = 0; k < kMapWarps; ++k) {
+    const int w = BACKWARD ? kMapWarps - 1 - k : k;
     const F ka = load<P>(&sa[w][chan]);
     pa = pa * ka;
     ph = fma(ka, ph, load<P>(&sh[w][chan]));
@@ -638,40 +684,46 @@ __global__ void __launch_bounds__(256) rec_maps_kernel(const __grid_constant__ R
   }
 }
 
+// Sum over a warp, in every lane.
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 // ddt_bias and dA_log: the warps' parts in a fixed order, in fp64.  A block has 32 channels of a
-// head (the first one of a head its dA_log too); 32 threads a channel take the segments in turn.
+// head (the first one of a head its dA_log too); 32 threads a channel take the parts in turn.
 template <int D, int W>
 __global__ void __launch_bounds__(1024) rec_params_kernel(const __grid_constant__ RecParams p,
                                                           float* dA_log, float* ddt_bias) {
   __shared__ double red[32][33];
   constexpr int kBlocks = D / 32, K = Shape<D>::K;
-  const int n = blockIdx.x / kBlocks, d = (blockIdx.x % kBlocks) * 32 + (threadIdx.x & 31);
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, records = p.units / p.N;
+  const int n = blockIdx.x / kBlocks, d0 = blockIdx.x % kBlocks * 32;
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, parts = p.units / p.N * W;
+  wait_dependencies();
   if (p.plan[RH_CHECKSUM] != p.checksum) return;
   double sum = 0, raw = 0;
-  for (int k = row; k < records; k += 32) {
-    const int4 r0 = __ldg(record(p, k)), r1 = __ldg(record(p, k) + 1);
-    const int parts = min(W, (r0.z + K - 1) / K);
-    const float* b = p.part_bias + ((size_t)r1.x * p.N + n) * D + d;
 #pragma unroll 4
-    for (int i = 0; i < parts; ++i) sum += b[(size_t)i * p.N * D];
-    if (lane < parts) raw += p.part_A[(size_t)(r1.x + lane) * p.N + n];
+  for (int i = row; i < parts; i += 32) {
+    const int r = i / W, j = i - r * W;
+    const int4 r0 = __ldg(record(p, r));
+    if (j < (r0.z + K - 1) / K) {
+      const size_t part = (size_t)(__ldg(&record(p, r)[1].x) + j) * p.N + n;
+      sum += p.part_bias[part * D + d0 + lane];
+      if (lane == 0) raw += p.part_A[part];
+    }
   }
   red[row][lane] = sum;
   __syncthreads();
-  if (row == 0) {
-    for (int k = 1; k < 32; ++k) sum += red[k][lane];
-    ddt_bias[(size_t)n * D + d] = (float)sum;
-  }
-  if (blockIdx.x % kBlocks != 0) return;
+  sum = warp_sum(red[lane][row]);
+  if (lane == 0) ddt_bias[(size_t)n * D + d0 + row] = (float)sum;
+  if (d0 != 0) return;
   __syncthreads();
-  red[row][lane] = raw;
+  if (lane == 0) red[0][row] = raw;
   __syncthreads();
-  if (row == 0) {
-    for (int k = 1; k < 32; ++k) raw += red[k][lane];
-    for (int o = 16; o > 0; o >>= 1) raw += __shfl_down_sync(0xffffffffu, raw, o);
-    if (lane == 0) dA_log[n] = (float)raw;
-  }
+  if (row > 0) return;
+  raw = warp_sum(red[0][lane]);
+  if (lane == 0) dA_log[n] = (float)raw;
 }
 
 template <class T>
@@ -710,7 +762,7 @@ kda_status_t prepare(const kda_recurrence_shape_t* shape, const int32_t* plan_ho
                      size_t workspace_bytes, bool backward, RecParams* p, ByteRange (&in)[9]) {
   kda_status_t st = validate_recurrence_shape(shape);
   if (st != KDA_OK) return st;
-  if (!plan_host || !plan_dev || !x || !g || !beta || !A_log || !dt_bias || !workspace)
+  if (!plan_host || !plan_dev || !x || !g || !beta || !A_log || !dt_bias)
     return KDA_ERR_NULL;
   st = validate_recurrence_plan(plan_host, n_int32, shape);
   if (st != KDA_OK) return st;
@@ -718,7 +770,9 @@ kda_status_t prepare(const kda_recurrence_shape_t* shape, const int32_t* plan_ho
   size_t need = 0;
   st = kda_recurrence_workspace_size(plan_host, n_int32, backward, &need);
   if (st != KDA_OK) return st;
-  if (workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+  // a workspace of the status word alone may be left out
+  if (!workspace && need > kWsHeaderBytes) return KDA_ERR_NULL;
+  if ((workspace && workspace_bytes < need) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return KDA_ERR_WORKSPACE;
   for (const void* ptr : {(const void*)h0, (const void*)A_log, (const void*)dt_bias,
                           (const void*)plan_dev})
@@ -736,7 +790,7 @@ kda_status_t prepare(const kda_recurrence_shape_t* shape, const int32_t* plan_ho
   in[4] = dense_range(A_log, (size_t)shape->N * 4);
   in[5] = dense_range(dt_bias, z.params);
   in[6] = dense_range(plan_dev, n_int32 * 4);
-  in[7] = dense_range(workspace, need);
+  in[7] = dense_range(workspace, workspace ? need : 0);
   p->plan = plan_dev;
   p->checksum = plan_host[RH_CHECKSUM];
   p->N = shape->N;
@@ -769,6 +823,23 @@ struct Scratch {
   }
 };
 
+// A launch that may start before its stream's last kernel has ended.
+template <class... Params, class... Args>
+cudaError_t launch_early(void (*kernel)(Params...), int blocks, int threads, int smem,
+                         cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr;
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, (Params)args...);
+}
+
 // Launches a pass: the maps where sequences are cut, and the walk, a block on every multiprocessor
 // that has a unit.
 template <class T, int D, bool BACKWARD, class Kernel>
@@ -794,9 +865,9 @@ cudaError_t launch(Kernel kernel, PerDevice& once, RecParams& p, const int32_t* 
     p.tile_step[i] = (BACKWARD ? -B::kWarps : B::kWarps) * K * row;
   }
   if (plan[RH_MAPS]) {
-    rec_maps_kernel<T, D, BACKWARD><<<(unsigned)p.units, 256, 0, s>>>(p);
+    rec_maps_kernel<T, D, BACKWARD><<<(unsigned)p.units, 32 * kMapWarps, 0, s>>>(p);
     e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    return e != cudaSuccess ? e : launch_early(kernel, blocks, 32 * B::kWarps, kSmem, s, p);
   }
   kernel<<<(unsigned)blocks, 32 * B::kWarps, kSmem, s>>>(p);
   return cudaGetLastError();
@@ -941,8 +1012,8 @@ extern "C" kda_status_t kda_recurrence_backward(
     using T = std::remove_pointer_t<decltype(tag)>;
     const cudaError_t err = launch_backward<T, D>(p, plan_host, s);
     if (err != cudaSuccess) return err;
-    rec_params_kernel<D, Block<T, true>::kWarps><<<(unsigned)shape->N * (D / 32), 1024, 0, s>>>(p, dA_log, ddt_bias);
-    return cudaGetLastError();
+    return launch_early(rec_params_kernel<D, Block<T, true>::kWarps>, shape->N * (D / 32), 1024, 0,
+                        s, p, dA_log, ddt_bias);
   });
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -59,10 +59,11 @@ long long segments_of(long long tiles, long long most) {
 // Whether the lengths are well formed and everything fits the kernels' 32-bit counters, and how the
 // sequences are cut.
 //
-// Uncut, a pass takes as long as its longest sequence, one tile after another, or as the busiest of
-// the multiprocessors.  Cut, the segments' maps come first, from data that is then read again: about
-// 1.8 times the work, and 50 tiles' time for the second launch and the joins (both measured).  Of
-// the cuts into segments for one to eight rounds over the multiprocessors the cheapest is taken.
+// Counted in tiles of a multiprocessor (about 0.16 us each), a pass takes as long, uncut, as its
+// longest sequence, one tile after another, or as all tiles over the multiprocessors.  Cut, a segment
+// costs 8 more for filling its ring, the maps 0.6 of all tiles and 25 for their launch, and the joins
+// 0.3 for each segment before (all measured).  Of the cuts into segments for one to eight rounds over
+// the multiprocessors the cheapest is taken.
 kda_status_t check_lengths(const kda_recurrence_shape_t& s, const int32_t* cu, Cut* cut) {
   const int R = rec_tile_rows(s.D);
   long long tiles = 0, longest = 0;
@@ -91,7 +92,7 @@ kda_status_t check_lengths(const kda_recurrence_shape_t& s, const int32_t* cu, C
       else lo = mid + 1;
     }
     count = segments(lo);
-    const double cost = 1.8 * rounds * (double)lo + 50;
+    const double cost = rounds * (lo + 8.0 + 0.3 * segments_of(longest, lo)) + 0.6 * all + 25;
     if (count > s.B && cost < least) {
       least = cost;
       *cut = Cut{lo, count};

@@ -18,7 +18,8 @@ import torch
 
 from . import _lib
 from ._lib import KdaError, KdaQkShape, check
-from ._views import (dtype_code, expect, expect_dense, launch_on, needs_grad, view, viewable)
+from ._views import (dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, view,
+                     viewable)
 from .api import LAYOUTS, _ptr
 
 
@@ -67,9 +68,9 @@ def _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interle
     ctx, handle = launch_on(dev, stream)
     with ctx:
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            q_out = dense_like(q)
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+            k_out = dense_like(k)
         check(_lib.load().kda_qk_norm_rope(
             ctypes.byref(shape), ctypes.byref(view(q, "q", layout)),
             ctypes.byref(view(k, "k", layout)), _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
@@ -101,9 +102,9 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k
     ctx, handle = launch_on(dev, stream)
     with ctx:
         if dq is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            dq = dense_like(q)
         if dk is None:
-            dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+            dk = dense_like(k)
         dqw = torch.empty_like(q_weight) if q_weight is not None else None
         dkw = torch.empty_like(k_weight) if k_weight is not None else None
         ws = torch.empty(ws_bytes.value, dtype=torch.uint8, device=dev)

@@ -23,9 +23,11 @@ import torch
 
 from . import _lib
 from ._lib import KdaError, KdaRecurrenceShape, check
-from ._views import (dtype_code, expect, expect_dense, launch_on, needs_grad, view, viewable)
+from ._views import (dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, view,
+                     viewable)
 from .api import LAYOUTS, _ptr
 
+_STATUS_BYTES = 256  # a workspace that holds the device status alone
 _P_I32 = ctypes.POINTER(ctypes.c_int32)
 
 
@@ -158,17 +160,21 @@ def _forward(x, g, beta, initial_state, A_log, dt_bias, lower_bound, layout, pla
     ctx, handle = launch_on(dev, stream)
     with ctx:
         if out is None:
-            out = torch.empty(plan._x, dtype=x.dtype, device=dev)
+            out = dense_like(x)
         if final_state is None:
-            final_state = torch.empty(plan._state, dtype=torch.float32, device=dev)
-        states = (torch.empty(plan.states_shape, dtype=torch.float32, device=dev)
-                  if want_states else None)
-        ws, ws_bytes = _workspace(workspace, plan.workspace_bytes, dev)
+            final_state = (dense_like(initial_state) if initial_state is not None else
+                           torch.empty(plan._state, dtype=torch.float32, device=dev))
+        states = A_log.new_empty(plan.states_shape) if want_states else None
+        if workspace is None and plan.workspace_bytes == _STATUS_BYTES:
+            ws_ptr, ws_bytes = None, 0  # nobody could read the status
+        else:
+            workspace, ws_bytes = _workspace(workspace, plan.workspace_bytes, dev)
+            ws_ptr = workspace.data_ptr()
         check(_lib.load().kda_recurrence_forward(
             ctypes.byref(plan._shape_for(code)), plan._host_ptr, plan.dev.data_ptr(),
             plan.host.size, ctypes.byref(view(x, "x", layout)), ctypes.byref(view(g, "g", layout)),
             ctypes.byref(view(beta, "beta", layout, channels=False)), _ptr(initial_state),
-            A_log.data_ptr(), dt_bias.data_ptr(), float(lower_bound), _ptr(states), ws.data_ptr(),
+            A_log.data_ptr(), dt_bias.data_ptr(), float(lower_bound), _ptr(states), ws_ptr,
             ws_bytes, out.data_ptr(), final_state.data_ptr(), handle), "kda_recurrence_forward")
     return out, final_state, states
 
@@ -192,9 +198,7 @@ def gated_recurrence_backward(dout, dfinal_state, x, g, beta, initial_state, A_l
     expect_dense(states, "states", torch.float32, dev, plan.states_shape)
     ctx, handle = launch_on(dev, stream)
     with ctx:
-        dx = torch.empty(plan._x, dtype=x.dtype, device=dev)
-        dg = torch.empty_like(dx)
-        dbeta = torch.empty(plan._rows, dtype=x.dtype, device=dev)
+        dx, dg, dbeta = dense_like(x), dense_like(x), dense_like(beta)
         dh0 = torch.empty_like(initial_state) if initial_state is not None else None
         dA_log = torch.empty_like(A_log)
         ddt_bias = torch.empty_like(dt_bias)
@@ -300,9 +304,10 @@ def gated_recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound: float,
     ctx, handle = launch_on(dev, stream)
     with ctx:
         if out is None:
-            out = torch.empty_like(x)
+            out = dense_like(x)
         if state_out is None:
-            state_out = torch.empty(shape, dtype=torch.float32, device=dev)
+            state_out = (dense_like(state) if state is not None else
+                         torch.empty(shape, dtype=torch.float32, device=dev))
         check(_lib.load().kda_recurrence_step(
             B, N, D, code, x.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state),
             A_log.data_ptr(), dt_bias.data_ptr(), float(lower_bound), out.data_ptr(),

@@ -334,6 +334,7 @@ KDA_API kda_status_t kda_recurrence_states_size(const int32_t* plan_host, size_t
  *   states         : fp32, kda_recurrence_states_size values, for kda_recurrence_backward; or
  *                    NULL.
  *   workspace      : device scratch, 256-byte aligned; kda_device_status reads its status word.
+ *                    NULL is allowed where kda_recurrence_workspace_size is 256, the status alone.
  *   out            : dense, x's shape, one rounding to nearest even; rows past a sequence's valid
  *                    length are written as zeros, and the inputs' rows there are never read.
  *   final_state    : fp32 [B, N, D], the unrounded state after each sequence's last token; may be

@@ -164,11 +164,13 @@ def test_recurrence_argument_checks(L):
         for name in ("x", "g", "beta"):
             assert c(**{name: None}) == NULL
             assert c(**{name: (None, *row)}) == NULL
-        for name in ("A", "bias", "ws", "plan_dev") + (("dx", "dg", "dbeta", "dA", "dbias", "states")
-                                                       if backward else ("out", "fs")):
+        for name in ("A", "bias", "plan_dev") + (("dx", "dg", "dbeta", "dA", "dbias", "states")
+                                                 if backward else ("out", "fs")):
             assert c(**{name: None}) == NULL, name
         assert c(lb=0.5) == BOUND and c(lb=-6.0) == BOUND and c(lb=float("nan")) == BOUND
         assert c(ws=0x70000010) == WORKSPACE and c(ws_bytes=8) == WORKSPACE
+        # without a workspace there is no place for more than the status
+        assert c(ws=None) == (NULL if backward else c())
         assert c(x=(0x10000008, *row)) == ALIGN
         assert c(g=(0x20000000, row[0], row[1], row[2] + 4)) == ALIGN   # rows off 16 bytes
         assert c(x=(0x10000000, -row[0], row[1], row[2])) == SHAPE      # negative stride
