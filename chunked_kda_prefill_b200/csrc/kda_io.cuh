@@ -1,5 +1,5 @@
-// kda_io.cuh -- loads and stores of 4 consecutive channels, one value, and the gate, for the
-// operators that take bf16, fp16 or fp32.
+// kda_io.cuh -- what the operators around the prefill share on the device: channels of bf16, fp16 or
+// fp32 as fp32 pairs, the gate, sums, copies to shared memory and dependent launches.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -12,53 +12,6 @@
 namespace kda {
 
 using namespace sm100;
-
-// 4 consecutive channels as they lie in memory (8 bytes, or 16 for fp32)
-template <class T>
-struct Vec4 {
-  uint2 w;
-};
-template <>
-struct Vec4<float> {
-  float4 w;
-};
-
-template <class T>
-__device__ __forceinline__ Vec4<T> ld4(const T* p) {
-  Vec4<T> v;
-  v.w = __ldg(reinterpret_cast<const decltype(v.w)*>(p));
-  return v;
-}
-
-__device__ __forceinline__ void widen(const Vec4<__nv_bfloat16>& v, float (&x)[4]) {
-  x[0] = __uint_as_float(v.w.x << 16);
-  x[1] = __uint_as_float(v.w.x & 0xFFFF0000u);
-  x[2] = __uint_as_float(v.w.y << 16);
-  x[3] = __uint_as_float(v.w.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ void widen(const Vec4<__half>& v, float (&x)[4]) {
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.w.x));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.w.y));
-  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
-}
-__device__ __forceinline__ void widen(const Vec4<float>& v, float (&x)[4]) {
-  x[0] = v.w.x; x[1] = v.w.y; x[2] = v.w.z; x[3] = v.w.w;
-}
-
-// round to nearest even and store
-__device__ __forceinline__ void st4(__nv_bfloat16* p, const float (&x)[4]) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                            *reinterpret_cast<const uint32_t*>(&b));
-}
-__device__ __forceinline__ void st4(__half* p, const float (&x)[4]) {
-  const __half2 a = __floats2half2_rn(x[0], x[1]), b = __floats2half2_rn(x[2], x[3]);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                            *reinterpret_cast<const uint32_t*>(&b));
-}
-__device__ __forceinline__ void st4(float* p, const float (&x)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
 
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
@@ -222,6 +175,47 @@ __device__ __forceinline__ Pairs<P> load(const T* p) {
 template <int P, class T>
 __device__ __forceinline__ Pairs<P> load_const(const T* p) {
   return widen<T, 2 * P>(__ldg(reinterpret_cast<const Bits<T, 2 * P>*>(p)));
+}
+
+// Sum over a warp, in every lane.
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Kernels of a call that follow one another start while the one before is still running
+// (programmatic dependent launch), and wait for its end before they read what it writes.
+__device__ __forceinline__ void launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_dependencies() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the warp's last PENDING groups of copies have arrived.
+template <int PENDING>
+__device__ __forceinline__ void copies_arrived() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
+  __syncwarp();
+}
+
+// A launch that may start before its stream's last kernel has ended.
+template <class... Params, class... Args>
+inline cudaError_t launch_early(void (*kernel)(Params...), dim3 blocks, int threads, int smem,
+                         cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr;
+  cfg.gridDim = blocks;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, (Params)args...);
 }
 
 }  // namespace kda

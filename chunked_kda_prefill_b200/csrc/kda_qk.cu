@@ -6,9 +6,11 @@
 // the opposite angles, so with dn = R^T dy and xh = x r the backward pass is
 //     dx = r (dn w - xh mean(dn w xh)),    dw = sum over rows of dn xh.
 //
-// D/8 lanes hold a row, 8 channels each: one 16-byte access per lane and row (two for fp32), the
-// row's sums and the exchange of half-split pairs by shuffles.  Such a group of lanes keeps its
-// token and walks the token's heads, so a token's cosines and sines are formed once, in registers.
+// D/8 lanes hold a row, 8 channels each, chosen so that both channels of a pair lie in one lane: 4
+// channels of either half of the turned ones, or 8 in a row.  Such a group of lanes keeps its token
+// and walks the token's heads, so a token's cosines and sines are formed once, in registers.  The
+// rows of the next steps are on their way to shared memory meanwhile (without them in registers more
+// blocks fit a multiprocessor), and only the sums over a row cross lanes.
 // Both passes are bound by HBM: 4 bytes a value forward (16-bit), 6 backward.
 #include <cuda_runtime.h>
 
@@ -20,13 +22,15 @@
 #include "kda_args.h"
 #include "kda_internal.h"
 #include "kda_io.cuh"
+#include "kda_once.h"
 
 namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-// Blocks of the backward pass at most; each leaves one partial sum of the weights' gradients.
-constexpr int kMaxBlocks = 592;
+// Multiprocessors that the grids are made for.  In the backward pass each block leaves one partial sum
+// of the weights' gradients.
+constexpr int kSpread = 148;
 // Blocks wanted before heads stop being split over blocks (about two for each SM).
 constexpr int kWantBlocks = 296;
 
@@ -44,56 +48,23 @@ struct QkParams {
   const float* inv_freq;
   long long tokens;
   int S;
-  int turned8;     // rotary_dim / 16: chunks of 8 channels in one half of the turned channels
+  int turned;      // rotary_dim
   int heads_per;   // heads of one block (grid.y splits the Nq + Nk heads)
   float eps;
   float* part;     // backward: [blocks][2][D] partial weight gradients
 };
 
-// 8 consecutive channels as they lie in memory
+// Rows of a step (so that their sums over lanes overlap), blocks that fit a multiprocessor by their
+// registers, and the steps whose copies a warp has under way or at work.
 template <class T>
-struct Vec8 {
-  Vec4<T> lo, hi;
-};
-// plain loads: a row may be turned in place
-template <class T>
-__device__ __forceinline__ Vec8<T> ld8(const T* p) {
-  Vec8<T> v;
-  if constexpr (sizeof(T) == 2) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    v.lo.w = make_uint2(w.x, w.y);
-    v.hi.w = make_uint2(w.z, w.w);
-  } else {
-    v.lo.w = *reinterpret_cast<const float4*>(p);
-    v.hi.w = *reinterpret_cast<const float4*>(p + 4);
-  }
-  return v;
-}
-template <class T>
-__device__ __forceinline__ void widen8(const Vec8<T>& v, float (&x)[8]) {
-  float a[4], b[4];
-  widen(v.lo, a);
-  widen(v.hi, b);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    x[e] = a[e];
-    x[4 + e] = b[e];
-  }
-}
-template <class T>
-__device__ __forceinline__ void st8(T* p, const float (&x)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
-    uint4 w;
-    st4(reinterpret_cast<T*>(&w.x), a);
-    st4(reinterpret_cast<T*>(&w.z), b);
-    *reinterpret_cast<uint4*>(p) = w;
-  } else {
-    const float a[4] = {x[0], x[1], x[2], x[3]}, b[4] = {x[4], x[5], x[6], x[7]};
-    st4(p, a);
-    st4(p + 4, b);
-  }
-}
+constexpr int kRows = sizeof(T) == 2 ? 2 : 1;
+template <bool BACKWARD>
+constexpr int kResident = BACKWARD ? 2 : 3;
+template <bool BACKWARD>
+constexpr int kStages = BACKWARD ? 6 : 4;
+
+template <class T, int D, bool BACKWARD>
+constexpr int kQkSmem = kStages<BACKWARD> * (BACKWARD ? 2 : 1) * kRows<T> * kThreads * 8 * (int)sizeof(T);
 
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v) {
@@ -102,70 +73,105 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// Cosine and signed sine of this lane's channels at a position: out = own * cs + partner * sn.
-// Channels that do not turn get 1 and 0.
-template <bool INTER>
-__device__ __forceinline__ void angles(const QkParams& p, int chunk, int pos, float (&cs)[8],
-                                       float (&sn)[8]) {
-  constexpr double kInv2Pi = 0.15915494309189533577;
-  constexpr int kPairs = INTER ? 4 : 8;
-  const bool second = !INTER && chunk >= p.turned8;
-  const int first = INTER ? chunk * 4 : (second ? chunk - p.turned8 : chunk) * 8;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    cs[e] = 1.f;
-    sn[e] = 0.f;
-  }
-  if (chunk >= 2 * p.turned8) return;
-#pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    // whole turns drop out in fp64: the product is off by at most 2^-53 of up to 2^31 radians
-    double turns = (double)pos * ((double)__ldg(p.inv_freq + first + i) * kInv2Pi);
-    turns -= rint(turns);
-    float s, c;
-    sincospif(2.f * (float)turns, &s, &c);
-    if (INTER) {
-      cs[2 * i] = cs[2 * i + 1] = c;
-      sn[2 * i] = -s;
-      sn[2 * i + 1] = s;
-    } else {
-      cs[i] = c;
-      sn[i] = second ? s : -s;
-    }
-  }
+// A lane's 8 channels: 4 from `a` on and 4 from `b` on.
+using F = Pairs<2>;
+struct Eight {
+  F a, b;
+};
+__device__ __forceinline__ Eight operator*(Eight x, Eight y) { return {x.a * y.a, x.b * y.b}; }
+__device__ __forceinline__ Eight operator*(Eight x, float y) { return {x.a * y, x.b * y}; }
+__device__ __forceinline__ Eight fma(Eight x, Eight y, Eight z) {
+  return {fma(x.a, y.a, z.a), fma(x.b, y.b, z.b)};
 }
+__device__ __forceinline__ float dot(Eight x, Eight y) { return sum(fma(x.a, y.a, x.b * y.b)); }
 
-// own * cs + DIR * partner * sn: the rotation (DIR = 1) or its transpose (-1)
-template <bool INTER, int DIR>
-__device__ __forceinline__ void turn(float (&v)[8], const float (&cs)[8], const float (&sn)[8],
-                                     int partner_lane) {
-  float o[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    o[e] = INTER ? v[e ^ 1] : __shfl_sync(0xffffffffu, v[e], partner_lane);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = fmaf(v[e], cs[e], (DIR > 0 ? o[e] : -o[e]) * sn[e]);
-}
-
-template <int D>
+// A lane's place: its row's group, its part of the row's copy, its channels, and whether they turn.
+template <int D, bool INTER>
 struct Place {
   static constexpr int kLanes = D / 8;
   static constexpr int kGroups = kThreads / kLanes;
-  int chunk, group, partner;
-  __device__ explicit Place(int turned8) {
-    chunk = threadIdx.x % kLanes;
+  int lane, group, a, b;
+  bool turns;
+  __device__ explicit Place(int turned) {
+    lane = threadIdx.x % kLanes;
     group = threadIdx.x / kLanes;
-    const int other = chunk < turned8 ? chunk + turned8
-                                      : (chunk < 2 * turned8 ? chunk - turned8 : chunk);
-    partner = (threadIdx.x & 31) - chunk + other;
+    turns = lane * 8 < turned;
+    a = lane * 8;
+    b = a + 4;
+    if (!INTER && turns) {
+      a = lane * 4;
+      b = turned / 2 + lane * 4;
+    }
+  }
+  template <class T>
+  __device__ Eight read(const T* row) const {
+    return {load<2>(row + a), load<2>(row + b)};
+  }
+  template <class T>
+  __device__ void write(T* row, const Eight& v) const {
+    store(row + a, v.a);
+    store(row + b, v.b);
   }
 };
 
-// this lane's 8 weights of a side
-template <int D>
-__device__ __forceinline__ void load_weight(const QkSide& a, int chunk, float (&w)[8]) {
+// Cosines and sines of the lane's 4 pairs at a position; a lane whose channels do not turn gets ones
+// and zeros.
+struct Angles {
+  F c, s;
+};
+template <class P>
+__device__ __forceinline__ Angles angles(const QkParams& p, const P& me, int pos) {
+  constexpr double kInv2Pi = 0.15915494309189533577;
+  Angles r{splat<2>(1.f), splat<2>(0.f)};
+  if (!me.turns) return r;
+  float c[4], s[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[e] = a.w ? __ldg(a.w + chunk * 8 + e) : 1.f;
+  for (int i = 0; i < 4; ++i) {
+    // whole turns drop out in fp64: the product is off by at most 2^-53 of up to 2^31 radians
+    double turns = (double)pos * ((double)__ldg(p.inv_freq + me.lane * 4 + i) * kInv2Pi);
+    turns -= rint(turns);
+    sincospif(2.f * (float)turns, &s[i], &c[i]);
+  }
+  r.c.v[0] = make_float2(c[0], c[1]);
+  r.c.v[1] = make_float2(c[2], c[3]);
+  r.s.v[0] = make_float2(s[0], s[1]);
+  r.s.v[1] = make_float2(s[2], s[3]);
+  return r;
+}
+
+// The rotation, or its transpose (the angles negated).
+template <bool INTER, bool BACK>
+__device__ __forceinline__ Eight turn(Eight v, const Angles& t) {
+  const F s = BACK ? t.s * -1.f : t.s;
+  if constexpr (!INTER) {
+    const F n = s * -1.f;
+    return {fma(v.a, t.c, v.b * n), fma(v.b, t.c, v.a * s)};
+  } else {
+    // pairs (2i, 2i + 1): those of v.a take the first two angles
+    auto two = [](float2 x, float c, float sn) {
+      return make_float2(fmaf(x.x, c, -x.y * sn), fmaf(x.y, c, x.x * sn));
+    };
+    Eight r;
+    r.a.v[0] = two(v.a.v[0], t.c.v[0].x, s.v[0].x);
+    r.a.v[1] = two(v.a.v[1], t.c.v[0].y, s.v[0].y);
+    r.b.v[0] = two(v.b.v[0], t.c.v[1].x, s.v[1].x);
+    r.b.v[1] = two(v.b.v[1], t.c.v[1].y, s.v[1].y);
+    return r;
+  }
+}
+
+// this lane's 8 weights of a side
+template <class P>
+__device__ __forceinline__ Eight load_weight(const QkSide& a, const P& me) {
+  Eight w{splat<2>(1.f), splat<2>(1.f)};
+  if (!a.w) return w;
+  auto four = [](const float* f) {  // of any address
+    F r;
+    r.v[0] = make_float2(__ldg(f), __ldg(f + 1));
+    r.v[1] = make_float2(__ldg(f + 2), __ldg(f + 3));
+    return r;
+  };
+  return {four(a.w + me.a), four(a.w + me.b)};
 }
 
 // the heads [lo, hi) of a side that a block of this grid.y works on
@@ -175,157 +181,196 @@ __device__ __forceinline__ void head_range(const QkParams& p, int side, int* lo,
   *hi = min(n, ((int)blockIdx.y + 1) * p.heads_per - before);
 }
 
-template <class T, int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) qk_forward_kernel(const QkParams p) {
-  using P = Place<D>;
-  constexpr int U = sizeof(T) == 2 ? 4 : 2;  // rows requested before the first is used
-  const P me(p.turned8);
-  const long long tk = (long long)blockIdx.x * P::kGroups + me.group;
-  const bool mine = tk < p.tokens;
-  const long long b = mine ? tk / p.S : 0;
-  const int s = (int)(mine ? tk - b * p.S : 0);
-  const int pos = !mine ? -1 : (p.positions ? __ldg(p.positions + tk) : s);
-  const bool live = pos >= 0;
-  float cs[8], sn[8];
-  angles<INTER>(p, me.chunk, live ? pos : 0, cs, sn);
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
+// A token of a group: its slot, its place there and its position (negative: padding, or none left).
+struct Token {
+  long long b;
+  int s, pos;
+  bool mine;
+  __device__ Token(const QkParams& p, long long t) {
+    mine = t < p.tokens;
+    if (!mine) t = 0;
+    b = p.tokens <= UINT32_MAX ? (uint32_t)t / (uint32_t)p.S : t / p.S;
+    s = (int)(t - b * p.S);
+    pos = !mine ? -1 : p.positions ? __ldg(p.positions + t) : s;
+  }
+};
+
+// The copies that run ahead: a warp's way through its groups' tokens, sides and heads, kRows heads of
+// one side a step.  The bounds are the block's, so that a warp's lanes stay together.
+template <class T, int D, bool INTER, bool BACKWARD>
+struct Ahead {
+  using P = Place<D, INTER>;
+  static constexpr int U = kRows<T>, kTensors = BACKWARD ? 2 : 1;
+  static constexpr int kRowBytes = D * (int)sizeof(T), kCopies = (int)sizeof(T) / 2;
+  long long t0;
+  int side, h, end;
+  bool done, live;
+  const char *x, *y;
+
+  __device__ void enter(const QkParams& p, const P& me, const Token& t) {
     const QkSide& a = p.side[side];
-    int h, end;
     head_range(p, side, &h, &end);
-    float w[8];
-    if (h < end) load_weight<D>(a, me.chunk, w);
-    const T* src = static_cast<const T*>(a.x.data) + b * a.x.stride_b + s * a.x.stride_s +
-                   me.chunk * 8;
-    T* dst = static_cast<T*>(a.out) + b * a.od.stride_b + s * a.od.stride_s + me.chunk * 8;
-    for (; h < end; h += U) {
-      Vec8<T> raw[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        raw[u] = Vec8<T>{};
-        if (live && h + u < end) raw[u] = ld8(src + (h + u) * a.x.stride_n);
+    x = static_cast<const char*>(a.x.data) +
+        (t.b * a.x.stride_b + t.s * a.x.stride_s + h * a.x.stride_n) * (long long)sizeof(T) +
+        me.lane * 16;
+    if (BACKWARD)
+      y = static_cast<const char*>(a.dy.data) +
+          (t.b * a.dy.stride_b + t.s * a.dy.stride_s + h * a.dy.stride_n) * (long long)sizeof(T) +
+          me.lane * 16;
+  }
+  // to the first side with heads of the next token that has one
+  __device__ void settle(const QkParams& p, const P& me) {
+    for (;;) {
+      done = t0 >= p.tokens;
+      if (done) return;
+      const Token t(p, t0 + me.group);
+      live = t.pos >= 0;
+      for (; side < 2; ++side) {
+        enter(p, me, t);
+        if (h < end) return;
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (h + u >= end) break;
-        float x[8];
-        widen8(raw[u], x);
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-        const float r = rsqrtf(group_sum<P::kLanes>(ss) * (1.f / D) + p.eps);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
-        turn<INTER, 1>(x, cs, sn, me.partner);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = live ? x[e] : 0.f;
-        if (mine) st8(dst + (h + u) * a.od.stride_n, x);
-      }
+      side = 0;
+      t0 += (long long)gridDim.x * P::kGroups;
     }
   }
-}
+  __device__ void begin(const QkParams& p, const P& me) {
+    x = y = nullptr;
+    t0 = (long long)blockIdx.x * P::kGroups;
+    side = 0;
+    settle(p, me);
+  }
+  // Starts the copies of a step; rows of padding become zeros.
+  __device__ void issue(const QkParams& p, const P& me, uint32_t stage) {
+    if (!done) {
+      const QkSide& a = p.side[side];
+      uint32_t to = stage + me.group * kRowBytes + me.lane * 16;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int bytes = live && h + u < end ? 16 : 0;
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c) {
+          copy16(to + c * 16 * P::kLanes, x + c * 16 * P::kLanes, bytes);
+          if (BACKWARD)
+            copy16(to + kThreads * 16 * kCopies + c * 16 * P::kLanes, y + c * 16 * P::kLanes, bytes);
+        }
+        to += kTensors * kThreads * 16 * kCopies;
+        x += a.x.stride_n * (long long)sizeof(T);
+        if (BACKWARD) y += a.dy.stride_n * (long long)sizeof(T);
+      }
+      h += U;
+      if (h >= end) {
+        if (++side == 2) {
+          side = 0;
+          t0 += (long long)gridDim.x * P::kGroups;
+        }
+        settle(p, me);
+      }
+    }
+    copies_issued();
+  }
+  // 16 bytes, or zeros where `bytes` is 0
+  __device__ static void copy16(uint32_t to, const char* from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+                 : "memory");
+  }
+};
 
-template <class T, int D, bool INTER>
-__global__ void __launch_bounds__(kThreads) qk_backward_kernel(const QkParams p) {
-  using P = Place<D>;
-  constexpr int U = 2;
-  __shared__ float red[P::kGroups][D];
-  const P me(p.turned8);
-  float dw[2][8] = {};
-  // the loop's bounds are the block's, so that a warp's lanes stay together for the shuffles
+template <class T, int D, bool INTER, bool BACKWARD>
+__global__ void __launch_bounds__(kThreads, kResident<BACKWARD>)
+    qk_kernel(const __grid_constant__ QkParams p) {
+  using P = Place<D, INTER>;
+  constexpr int U = kRows<T>, kS = kStages<BACKWARD>, kTensors = BACKWARD ? 2 : 1;
+  constexpr int kTensor = kThreads * 8, kStage = U * kTensors * kTensor;  // elements
+  extern __shared__ __align__(16) uint8_t smem[];
+  T* const ring = reinterpret_cast<T*>(smem);  // [kS][U][kTensors][kGroups][D]
+  const P me(p.turned);
+  Ahead<T, D, INTER, BACKWARD> ahead;
+  ahead.begin(p, me);
+  for (int i = 0; i < kS - 1; ++i) ahead.issue(p, me, smem_u32(ring + i * kStage));
+  launch_dependents();
+  Eight dw[2];
+  if (BACKWARD)
+    for (int i = 0; i < 2; ++i) dw[i] = {splat<2>(0.f), splat<2>(0.f)};
+  int stage = 0, free = kS - 1;
   for (long long t0 = (long long)blockIdx.x * P::kGroups; t0 < p.tokens;
        t0 += (long long)gridDim.x * P::kGroups) {
-    const long long tk = t0 + me.group;
-    const bool mine = tk < p.tokens;
-    const long long b = mine ? tk / p.S : 0;
-    const int s = (int)(mine ? tk - b * p.S : 0);
-    const int pos = !mine ? -1 : (p.positions ? __ldg(p.positions + tk) : s);
-    const bool live = pos >= 0;
-    float cs[8], sn[8];
-    angles<INTER>(p, me.chunk, live ? pos : 0, cs, sn);
+    const Token t(p, t0 + me.group);
+    const bool live = t.pos >= 0;
+    const Angles turns = angles(p, me, live ? t.pos : 0);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const QkSide& a = p.side[side];
       int h, end;
       head_range(p, side, &h, &end);
-      float w[8];
-      if (h < end) load_weight<D>(a, me.chunk, w);
-      const T* xs = static_cast<const T*>(a.x.data) + b * a.x.stride_b + s * a.x.stride_s +
-                    me.chunk * 8;
-      const T* ys = static_cast<const T*>(a.dy.data) + b * a.dy.stride_b + s * a.dy.stride_s +
-                    me.chunk * 8;
-      T* dst = static_cast<T*>(a.out) + b * a.od.stride_b + s * a.od.stride_s + me.chunk * 8;
+      if (h >= end) continue;
+      const Eight w = load_weight(a, me);
+      T* to = static_cast<T*>(a.out) + t.b * a.od.stride_b + t.s * a.od.stride_s +
+              h * a.od.stride_n;
       for (; h < end; h += U) {
-        Vec8<T> rx[U], ry[U];
+        copies_arrived<kS - 2>();
+        ahead.issue(p, me, smem_u32(ring + free * kStage));
+        free = free + 1 == kS ? 0 : free + 1;
+        const T* row = ring + stage * kStage + me.group * D;
+        stage = stage + 1 == kS ? 0 : stage + 1;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          rx[u] = ry[u] = Vec8<T>{};
-          if (live && h + u < end) {
-            rx[u] = ld8(xs + (h + u) * a.x.stride_n);
-            ry[u] = ld8(ys + (h + u) * a.dy.stride_n);
+          Eight x = me.read(row);
+          const float norm = rsqrtf(group_sum<P::kLanes>(dot(x, x)) * (1.f / D) + p.eps);
+          if constexpr (!BACKWARD) {
+            x = turn<INTER, false>(x * norm * w, turns);
+          } else {
+            const float r = live && h + u < end ? norm : 0.f;  // eps may be 0
+            Eight dn = turn<INTER, true>(me.read(row + kTensor), turns);
+            x = x * r;
+            dw[side] = fma(dn, x, dw[side]);
+            dn = dn * w;
+            const float m = group_sum<P::kLanes>(dot(dn, x)) * (-1.f / D);
+            const F m2 = splat<2>(m);
+            x = Eight{fma(x.a, m2, dn.a), fma(x.b, m2, dn.b)} * r;
           }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (h + u >= end) break;
-          float x[8], dn[8];
-          widen8(rx[u], x);
-          widen8(ry[u], dn);
-          float ss = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-          const float norm = rsqrtf(group_sum<P::kLanes>(ss) * (1.f / D) + p.eps);
-          const float r = live ? norm : 0.f;  // eps may be 0
-          turn<INTER, -1>(dn, cs, sn, me.partner);
-          float dot = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[e] *= r;
-            dn[e] = live ? dn[e] : 0.f;
-            dw[side][e] = fmaf(dn[e], x[e], dw[side][e]);
-            dn[e] *= w[e];
-            dot = fmaf(dn[e], x[e], dot);
-          }
-          dot = group_sum<P::kLanes>(dot) * (1.f / D);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = live ? r * (dn[e] - x[e] * dot) : 0.f;
-          if (mine) st8(dst + (h + u) * a.od.stride_n, x);
+          if (!live) x = {splat<2>(0.f), splat<2>(0.f)};
+          if (t.mine && h + u < end) me.write(to, x);
+          to += a.od.stride_n;
+          row += kTensors * kTensor;
         }
       }
     }
   }
+  if constexpr (BACKWARD) {
+    float* const red = reinterpret_cast<float*>(smem);  // [kGroups][D]
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    __syncthreads();
+    for (int side = 0; side < 2; ++side) {
+      __syncthreads();
+      me.write(red + me.group * D, dw[side]);
+      __syncthreads();
+      if (threadIdx.x < D) {
+        float sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) red[me.group][me.chunk * 8 + e] = dw[side][e];
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float sum = 0.f;
-#pragma unroll
-      for (int g = 0; g < P::kGroups; ++g) sum += red[g][threadIdx.x];
-      const size_t block = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
-      p.part[(block * 2 + side) * D + threadIdx.x] = sum;
+        for (int g = 0; g < P::kGroups; ++g) sum += red[g * D + threadIdx.x];
+        const size_t block = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
+        p.part[(block * 2 + side) * D + threadIdx.x] = sum;
+      }
     }
   }
 }
 
-// The blocks' partial sums in a fixed order, in fp64: 8 threads for a channel, then those 8.
+// The blocks' partial sums in a fixed order, in fp64: 32 threads for a channel, then those 32.
 template <int D>
-__global__ void qk_weights_kernel(const float* part, int blocks, float* dwq, float* dwk) {
-  __shared__ double red[8][32];
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-  const int d = blockIdx.x * 32 + lane, side = blockIdx.y;
-  float* dw = side ? dwk : dwq;
+__global__ void __launch_bounds__(1024) qk_weights_kernel(const float* part, int blocks, float* dwq,
+                                                          float* dwk) {
+  __shared__ double red[32][33];
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, side = blockIdx.y;
+  float* const dw = side ? dwk : dwq;
   if (!dw) return;
+  wait_dependencies();
   double sum = 0;
-  for (int i = row; i < blocks; i += 8) sum += part[((size_t)i * 2 + side) * D + d];
+#pragma unroll 8
+  for (int i = row; i < blocks; i += 32)
+    sum += part[((size_t)i * 2 + side) * D + blockIdx.x * 32 + lane];
   red[row][lane] = sum;
   __syncthreads();
-  if (row == 0) {
-    for (int i = 1; i < 8; ++i) sum += red[i][lane];
-    dw[d] = (float)sum;
-  }
+  sum = warp_sum(red[lane][row]);
+  if (lane == 0) dw[blockIdx.x * 32 + row] = (float)sum;
 }
 
 kda_status_t validate(const kda_qk_shape_t* s) {
@@ -360,7 +405,7 @@ kda_status_t prepare(const kda_qk_shape_t* s, const kda_view_t* q, const kda_vie
   const int nb = batches(*s);
   p->tokens = (long long)nb * s->S;
   p->S = s->S;
-  p->turned8 = s->rotary_dim / 16;
+  p->turned = s->rotary_dim;
   p->eps = s->eps;
   p->positions = positions;
   p->inv_freq = inv_freq;
@@ -415,18 +460,37 @@ void dispatch(const kda_qk_shape_t& s, A&&... a) {
   else with_type((float*)nullptr);
 }
 
-template <class T, int D, bool INTER>
-struct Forward {
-  static void run(dim3 grid, const QkParams& p, cudaStream_t s) {
-    qk_forward_kernel<T, D, INTER><<<grid, kThreads, 0, s>>>(p);
+// Launches a pass; blocks that share a token's heads lie along y.
+template <class T, int D, bool INTER, bool BACKWARD>
+struct Pass {
+  static void run(dim3 grid, const QkParams& p, cudaStream_t s, cudaError_t* e) {
+    static PerDevice once;
+    constexpr int kSmem = kQkSmem<T, D, BACKWARD>;
+    const auto kernel = qk_kernel<T, D, INTER, BACKWARD>;
+    int dev = 0, unused;
+    *e = cudaGetDevice(&dev);
+    if (*e != cudaSuccess) return;
+    *e = once_per_device(once, dev, &unused, [&](int, int*) {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    });
+    if (*e != cudaSuccess) return;
+    kernel<<<grid, kThreads, kSmem, s>>>(p);
+    *e = cudaGetLastError();
   }
 };
 template <class T, int D, bool INTER>
-struct Backward {
-  static void run(dim3 grid, const QkParams& p, cudaStream_t s) {
-    qk_backward_kernel<T, D, INTER><<<grid, kThreads, 0, s>>>(p);
-  }
-};
+using Forward = Pass<T, D, INTER, false>;
+template <class T, int D, bool INTER>
+using Backward = Pass<T, D, INTER, true>;
+
+// The grid: blocks over tokens and, where those are few, over the heads of a token.
+dim3 grid_of(const kda_qk_shape_t& s, int most, QkParams* p) {
+  const int groups = kThreads / (s.D / 8), heads = s.Nq + s.Nk;
+  const long long want = std::min<long long>((p->tokens + groups - 1) / groups, most);
+  p->heads_per = heads_per_block(*p, want);
+  const int splits = (heads + p->heads_per - 1) / p->heads_per;
+  return dim3((unsigned)std::min<long long>(want, std::max(1, most / splits)), (unsigned)splits);
+}
 
 }  // namespace
 }  // namespace kda
@@ -453,14 +517,10 @@ extern "C" kda_status_t kda_qk_norm_rope(const kda_qk_shape_t* shape, const kda_
   }
   if (overlap(out[0], out[1])) return KDA_ERR_ALIAS;
   if ((st = check_device()) != KDA_OK) return st;
-  const int groups = kThreads / (shape->D / 8);
-  const long long blocks = (p.tokens + groups - 1) / groups;
-  if (blocks > INT_MAX) return KDA_ERR_SHAPE;
-  p.heads_per = heads_per_block(p, blocks);
-  const int heads = shape->Nq + shape->Nk;
-  const dim3 grid((unsigned)blocks, (unsigned)((heads + p.heads_per - 1) / p.heads_per));
-  dispatch<Forward>(*shape, grid, p, reinterpret_cast<cudaStream_t>(stream));
-  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  const dim3 grid = grid_of(*shape, kSpread * kResident<false>, &p);
+  cudaError_t e = cudaSuccess;
+  dispatch<Forward>(*shape, grid, p, reinterpret_cast<cudaStream_t>(stream), &e);
+  return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 extern "C" kda_status_t kda_qk_norm_rope_workspace_size(const kda_qk_shape_t* shape,
@@ -468,7 +528,7 @@ extern "C" kda_status_t kda_qk_norm_rope_workspace_size(const kda_qk_shape_t* sh
   if (!bytes) return KDA_ERR_NULL;
   const kda_status_t st = validate(shape);
   if (st != KDA_OK) return st;
-  *bytes = (size_t)kMaxBlocks * 2 * shape->D * 4;
+  *bytes = (size_t)kSpread * kResident<true> * 2 * shape->D * 4;
   return KDA_OK;
 }
 
@@ -512,20 +572,15 @@ extern "C" kda_status_t kda_qk_norm_rope_backward(
       if (overlap(outs[j], outs[i])) return KDA_ERR_ALIAS;
   }
   if ((st = check_device()) != KDA_OK) return st;
-  const int groups = kThreads / (shape->D / 8);
-  const int heads = shape->Nq + shape->Nk;
-  const long long want = std::min<long long>((p.tokens + groups - 1) / groups, kMaxBlocks);
-  p.heads_per = heads_per_block(p, want);
-  const int splits = (heads + p.heads_per - 1) / p.heads_per;
-  const int across = (int)std::min<long long>(want, std::max(1, kMaxBlocks / splits));
+  const dim3 grid = grid_of(*shape, kSpread * kResident<true>, &p);
   p.part = static_cast<float*>(workspace);
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  dispatch<Backward>(*shape, dim3((unsigned)across, (unsigned)splits), p, s);
-  if (cudaGetLastError() != cudaSuccess) return KDA_ERR_CUDA;
-  if (dq_weight || dk_weight) {
-    const dim3 grid(shape->D / 32, 2);
-    if (shape->D == 128) qk_weights_kernel<128><<<grid, 256, 0, s>>>(p.part, across * splits, dq_weight, dk_weight);
-    else qk_weights_kernel<64><<<grid, 256, 0, s>>>(p.part, across * splits, dq_weight, dk_weight);
-  }
-  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  const cudaStream_t stm = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t err = cudaSuccess;
+  dispatch<Backward>(*shape, grid, p, stm, &err);
+  if (err != cudaSuccess) return KDA_ERR_CUDA;
+  if (dq_weight || dk_weight)
+    err = launch_early(shape->D == 128 ? qk_weights_kernel<128> : qk_weights_kernel<64>,
+                       dim3(shape->D / 32, 2), 1024, 0, stm, p.part, (int)(grid.x * grid.y),
+                       dq_weight, dk_weight);
+  return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -109,27 +109,10 @@ __device__ __forceinline__ const int4* record(const RecParams& p, int i) {
   return reinterpret_cast<const int4*>(p.plan + kRecHeader) + 2 * i;
 }
 
-// Kernels of a call that follow one another start while the one before is still running
-// (programmatic dependent launch), and wait for its end before they read what it writes.
-__device__ __forceinline__ void launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_dependencies() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // 16 bytes from global to shared memory
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
-__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the warp's last PENDING groups of copies have arrived.
-template <int PENDING>
-__device__ __forceinline__ void copies_arrived() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
-  __syncwarp();
-}
-
 // A warp's way through the tiles of its block's units, and the copies of the next one.  The units
 // are dealt to the blocks in rounds, every other one in reverse, so that with the plan's order
 // (longest first) no block gets the longer unit of every round.
@@ -684,13 +667,6 @@ __global__ void __launch_bounds__(32 * kMapWarps, 1) rec_maps_kernel(const __gri
   }
 }
 
-// Sum over a warp, in every lane.
-__device__ __forceinline__ double warp_sum(double v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
 // ddt_bias and dA_log: the warps' parts in a fixed order, in fp64.  A block has 32 channels of a
 // head (the first one of a head its dA_log too); 32 threads a channel take the parts in turn.
 template <int D, int W>
@@ -822,23 +798,6 @@ struct Scratch {
     total = A + (backward ? plan[RH_PARTS] * N * 4 : 0);
   }
 };
-
-// A launch that may start before its stream's last kernel has ended.
-template <class... Params, class... Args>
-cudaError_t launch_early(void (*kernel)(Params...), int blocks, int threads, int smem,
-                         cudaStream_t s, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr;
-  cfg.gridDim = dim3((unsigned)blocks);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, (Params)args...);
-}
 
 // Launches a pass: the maps where sequences are cut, and the walk, a block on every multiprocessor
 // that has a unit.
