@@ -54,14 +54,14 @@ struct QkParams {
   float* part;     // backward: [blocks][2][D] partial weight gradients
 };
 
-// Rows of a step (so that their sums over lanes overlap), blocks that fit a multiprocessor by their
-// registers, and the steps whose copies a warp has under way or at work.
+// Rows of a step (so that their sums over lanes overlap), blocks on a multiprocessor, and the steps
+// whose copies a warp has under way or at work.  More of either is slower: 4x32x16384 forward takes
+// 345-353 us with 3 or 4 steps, 382 with 6 and 397 with 3 blocks, one block 488.
 template <class T>
 constexpr int kRows = sizeof(T) == 2 ? 2 : 1;
+constexpr int kResident = 2;
 template <bool BACKWARD>
-constexpr int kResident = BACKWARD ? 2 : 3;
-template <bool BACKWARD>
-constexpr int kStages = BACKWARD ? 6 : 4;
+constexpr int kStages = BACKWARD ? 3 : 4;
 
 template <class T, int D, bool BACKWARD>
 constexpr int kQkSmem = kStages<BACKWARD> * (BACKWARD ? 2 : 1) * kRows<T> * kThreads * 8 * (int)sizeof(T);
@@ -276,7 +276,7 @@ struct Ahead {
 };
 
 template <class T, int D, bool INTER, bool BACKWARD>
-__global__ void __launch_bounds__(kThreads, kResident<BACKWARD>)
+__global__ void __launch_bounds__(kThreads, kResident)
     qk_kernel(const __grid_constant__ QkParams p) {
   using P = Place<D, INTER>;
   constexpr int U = kRows<T>, kS = kStages<BACKWARD>, kTensors = BACKWARD ? 2 : 1;
@@ -517,7 +517,7 @@ extern "C" kda_status_t kda_qk_norm_rope(const kda_qk_shape_t* shape, const kda_
   }
   if (overlap(out[0], out[1])) return KDA_ERR_ALIAS;
   if ((st = check_device()) != KDA_OK) return st;
-  const dim3 grid = grid_of(*shape, kSpread * kResident<false>, &p);
+  const dim3 grid = grid_of(*shape, kSpread * kResident, &p);
   cudaError_t e = cudaSuccess;
   dispatch<Forward>(*shape, grid, p, reinterpret_cast<cudaStream_t>(stream), &e);
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
@@ -528,7 +528,7 @@ extern "C" kda_status_t kda_qk_norm_rope_workspace_size(const kda_qk_shape_t* sh
   if (!bytes) return KDA_ERR_NULL;
   const kda_status_t st = validate(shape);
   if (st != KDA_OK) return st;
-  *bytes = (size_t)kSpread * kResident<true> * 2 * shape->D * 4;
+  *bytes = (size_t)kSpread * kResident * 2 * shape->D * 4;
   return KDA_OK;
 }
 
@@ -572,7 +572,7 @@ extern "C" kda_status_t kda_qk_norm_rope_backward(
       if (overlap(outs[j], outs[i])) return KDA_ERR_ALIAS;
   }
   if ((st = check_device()) != KDA_OK) return st;
-  const dim3 grid = grid_of(*shape, kSpread * kResident<true>, &p);
+  const dim3 grid = grid_of(*shape, kSpread * kResident, &p);
   p.part = static_cast<float*>(workspace);
   const cudaStream_t stm = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t err = cudaSuccess;
