@@ -65,6 +65,14 @@ __device__ __forceinline__ Pairs<P> splat(float x) {
   for (int i = 0; i < P; ++i) r.v[i] = make_float2(x, x);
   return r;
 }
+// the same pair everywhere
+template <int P>
+__device__ __forceinline__ Pairs<P> both(float2 x) {
+  Pairs<P> r;
+#pragma unroll
+  for (int i = 0; i < P; ++i) r.v[i] = x;
+  return r;
+}
 template <int P>
 __device__ __forceinline__ Pairs<P> operator+(Pairs<P> a, Pairs<P> b) {
 #pragma unroll

@@ -83,19 +83,26 @@ template <class T, int D, bool BACKWARD>
 constexpr int kWalkSmem =
     Block<T, BACKWARD>::kWarps * Block<T, BACKWARD>::kStages * kStageBytes<T, D, BACKWARD>;
 
-// A tile as its copies' issuer describes it to the same warp later.
-struct __align__(16) Tile {
-  int valid, flags, slot, row;  // row: of its first token
-  int n, place, map, part;      // place: of its state
+// What a warp keeps of a tile from the start of its copies on: the lane's write logit, and the number
+// of tokens (0: no tile is left) with flags.
+struct Ahead {
+  float logit;
+  int info;
 };
 enum : int {
-  kFresh = 1,   // the warp's first tile in the unit
-  kFirst = 2,   // the segment's first tile of the walk
-  kLast = 4,    // the segment's last tile of the walk
-  kEnd = 8,     // of the segment that the walk of the sequence ends with
-  kCut = 16,    // of a cut sequence
-  kStop = 32,   // the ring's last tile
-  kOrder = 6    // flags >> kOrder: the segment's place in the walk of its sequence
+  kTokens = 31,
+  kFresh = 32,    // the warp's first tile in the unit
+  kFirst = 64,    // the segment's first tile of the walk
+  kLast = 128,    // the segment's last tile of the walk
+  kEnd = 256,     // of the segment that the walk of the sequence ends with
+  kCut = 512,     // of a cut sequence
+  kStop = 1024    // the ring's last tile
+};
+// The same of a unit, with its first tile: `row` of its first token, `place` of its state, `order` of
+// the segment in the walk of its sequence.
+struct __align__(16) Entry {
+  int slot, row, n, place;
+  int map, part, order, unused;
 };
 
 // Whether the plan on the device is the host's; block 0 leaves the status.
@@ -191,6 +198,7 @@ struct Walk {
     ++round;
     enter(p, zero);
   }
+  // (a branch for whole tiles, without the comparisons, was 10 % slower in both passes)
   __device__ static void copy_rows(uint32_t to, const char* from, long long step, int valid) {
     const int lane = threadIdx.x & 31;
     to += lane * 16;
@@ -200,28 +208,28 @@ struct Walk {
       from += step;
     }
   }
-  // Describes the next tile and starts its copies to `stage`; returns the lane's write logit.
+  // Starts the copies of the next tile to `stage`.
   template <class Zero>
-  __device__ float issue(const RecParams& p, uint32_t stage, Tile* tile, Zero&& zero) {
+  __device__ Ahead issue(const RecParams& p, uint32_t stage, Entry* entry, Zero&& zero) {
     const int lane = threadIdx.x & 31;
     __syncwarp();  // all lanes have read what the stage held
-    float logit = 0.f;
-    if (done) {
-      if (lane == 0) tile->valid = 0;
-    } else {
-      const int k = BACKWARD ? tiles - 1 - t : t;
-      const int valid = min(K, len - k * K);
-      if (lane == 0) {
+    Ahead ahead{0.f, 0};
+    if (!done) {
+      int valid = K;
+      ahead.info = K;
+      if (fresh || t == tiles - 1) {
+        const int k = BACKWARD ? tiles - 1 - t : t;
         const int order = BACKWARD ? segments - 1 - segment : segment;
         const bool last = t == tiles - 1;
-        int4* const to = reinterpret_cast<int4*>(tile);
-        to[0] = make_int4(valid,
-                          (fresh ? kFresh : 0) | (t == 0 ? kFirst : 0) | (last ? kLast : 0) |
-                              (order == segments - 1 ? kEnd : 0) | (segments > 1 ? kCut : 0) |
-                              (last && unit_of(round + 1) >= p.units ? kStop : 0) |
-                              order << kOrder,
-                          slot, start + k * K);
-        if (fresh) to[1] = make_int4(n, tile0 + k, map, part + t);
+        valid = min(K, len - k * K);
+        ahead.info = valid | (fresh ? kFresh : 0) | (t == 0 ? kFirst : 0) | (last ? kLast : 0) |
+                     (order == segments - 1 ? kEnd : 0) | (segments > 1 ? kCut : 0) |
+                     (last && unit_of(round + 1) >= p.units ? kStop : 0);
+        if (fresh && lane == 0) {
+          int4* const to = reinterpret_cast<int4*>(entry);
+          to[0] = make_int4(slot, start + k * K, n, tile0 + k);
+          to[1] = make_int4(map, part + t, order, 0);
+        }
       }
       copy_rows(stage, g, p.copy_step[0], valid);
       copy_rows(stage + K * kRow, x, p.copy_step[1], valid);
@@ -229,11 +237,11 @@ struct Walk {
         if (p.dout.data) copy_rows(stage + 2 * K * kRow, dout, p.copy_step[2], valid);
         if (lane < D / 4) copy16(stage + 3 * K * kRow + lane * 16, state);
       }
-      if (lane < valid) logit = to_f32(__ldg(reinterpret_cast<const T*>(beta)));
+      if (lane < valid) ahead.logit = to_f32(__ldg(reinterpret_cast<const T*>(beta)));
       next(p, zero);
     }
     copies_issued();
-    return logit;
+    return ahead;
   }
 };
 
@@ -303,6 +311,12 @@ __device__ __forceinline__ void store_rows(T* to, long long next, int valid, con
   }
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 template <class T, int D>
 __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     rec_forward_kernel(const __grid_constant__ RecParams p) {
@@ -312,7 +326,8 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
   constexpr int K = S::K, V = S::V, P = V / 2, kStages = B::kStages, W = B::kWarps;
   constexpr int kStage = kStageBytes<T, D, false>;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Tile tiles[W][kStages];
+  __shared__ Entry entries[W][kStages];
+  __shared__ float2 writes[W][K];  // b and b
   if (!same_plan(p)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
   const Ring<W, D> ring(warp);
@@ -326,11 +341,11 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
   Walk<T, D, false> walk;
   walk.begin(p, warp, zero);
   auto issue = [&](int s) {
-    return walk.issue(p, smem_u32(stages + s * kStage), &tiles[warp][s], zero);
+    return walk.issue(p, smem_u32(stages + s * kStage), &entries[warp][s], zero);
   };
-  float logits[kStages - 1];
+  Ahead ahead[kStages - 1];
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) logits[s] = issue(s);
+  for (int s = 0; s < kStages - 1; ++s) ahead[s] = issue(s);
 
   GateScale gc{};
   F bias = splat<P>(0.f);
@@ -338,28 +353,29 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
   float* state = nullptr;
   int slot = 0, n = 0, s = 0, fill = kStages - 1;
   for (bool begun = warp > 0;; begun = true) {  // the ring's first tile has none before it
-    const float b = sigmoid(logits[0]);
-#pragma unroll
-    for (int k = 0; k + 1 < kStages - 1; ++k) logits[k] = logits[k + 1];
-    logits[kStages - 2] = issue(fill);
-    fill = fill + 1 == kStages ? 0 : fill + 1;
-    __syncwarp();
-    const int4 t = *reinterpret_cast<const int4*>(&tiles[warp][s]);
-    const int valid = t.x, flags = t.y;
+    const int info = ahead[0].info, valid = info & kTokens;
     if (valid == 0) break;
-    if (flags & kFresh) {
-      const int4 u = reinterpret_cast<const int4*>(&tiles[warp][s])[1];
-      slot = t.z;
-      n = u.x;
+    const float b = sigmoid(ahead[0].logit);
+#pragma unroll
+    for (int k = 0; k + 1 < kStages - 1; ++k) ahead[k] = ahead[k + 1];
+    ahead[kStages - 2] = issue(fill);
+    fill = fill + 1 == kStages ? 0 : fill + 1;
+    if (lane < K) writes[warp][lane] = make_float2(b, b);
+    if (info & kFresh) {
+      const Entry& t = entries[warp][s];
+      slot = t.slot;
+      n = t.n;
       gc = gate_scale(__ldg(p.A_log + n), p.lower_bound);
       bias = load_const<P>(p.dt_bias + (size_t)n * D + chan);
-      o = out + slot * p.od.stride_b + n * p.od.stride_n + t.w * orow + chan;
-      state = p.states + ((size_t)u.y * p.N + n) * D + chan;
+      o = out + slot * p.od.stride_b + n * p.od.stride_n + t.row * orow + chan;
+      state = p.states + ((size_t)t.place * p.N + n) * D + chan;
     }
     F start = splat<P>(0.f);
-    if (flags & kFirst) {
-      if (flags & kCut) start = join<D>(p, tiles[warp][s].map, flags >> kOrder, n, chan);
-      else if (p.begin) start = load<P>(p.begin + ((size_t)slot * p.N + n) * D + chan);
+    if (info & kFirst) {
+      if (info & kCut)
+        start = join<D>(p, entries[warp][s].map, entries[warp][s].order, n, chan);
+      else if (p.begin)
+        start = load<P>(p.begin + ((size_t)slot * p.N + n) * D + chan);
     }
     T* const tg = reinterpret_cast<T*>(stages + s * kStage);
     copies_arrived<kStages - 1>();
@@ -372,7 +388,7 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     for (int k = 0; k < K; ++k) {
       const F e = each((load<P>(tg + k * D + chan) + bias) * gc.nz, ex2);
       a[k] = each(each(e + splat<P>(1.f), rcp) * gc.l2, ex2);
-      u[k] = load<P>(tg + kRecTileElems + k * D + chan) * __shfl_sync(0xffffffffu, b, k);
+      u[k] = load<P>(tg + kRecTileElems + k * D + chan) * both<P>(writes[warp][k]);
       if (k > 0) {
         u[k] = fma(a[k], u[k - 1], u[k]);
         a[k] = a[k] * a[k - 1];
@@ -382,12 +398,12 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     F h = start;
     if (begun) {
       ring.wait();
-      if (!(flags & kFirst)) h = load<P>(ring.inbox + chan);
+      if (!(info & kFirst)) h = load<P>(ring.inbox + chan);
     }
     const F before = h;
     h = fma(a[K - 1], h, u[K - 1]);
     store(ring.outbox + chan, h);
-    if (!(flags & kStop)) ring.pass();
+    if (!(info & kStop)) ring.pass();
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) u[k] = fma(a[k], before, u[k]);
     u[K - 1] = h;
@@ -397,7 +413,7 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     }
     store_rows<T, D>(o, orow, valid, u);
     o += W * K * orow;
-    if ((flags & (kLast | kEnd)) == (kLast | kEnd))
+    if ((info & (kLast | kEnd)) == (kLast | kEnd))
       store(p.end + ((size_t)slot * p.N + n) * D + chan, h);
     s = s + 1 == kStages ? 0 : s + 1;
   }
@@ -432,7 +448,8 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   constexpr int K = S::K, V = S::V, P = V / 2, kStages = B::kStages, W = B::kWarps;
   constexpr int kStage = kStageBytes<T, D, true>, kElems = kRecTileElems;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Tile tiles[W][kStages];
+  __shared__ Entry entries[W][kStages];
+  __shared__ float2 writes[W][K];  // b and b
   launch_dependents();
   if (!same_plan(p)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
@@ -458,11 +475,11 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   Walk<T, D, true> walk;
   walk.begin(p, warp, zero);
   auto issue = [&](int s) {
-    return walk.issue(p, smem_u32(stages + s * kStage), &tiles[warp][s], zero);
+    return walk.issue(p, smem_u32(stages + s * kStage), &entries[warp][s], zero);
   };
-  float logits[kStages - 1];
+  Ahead ahead[kStages - 1];
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) logits[s] = issue(s);
+  for (int s = 0; s < kStages - 1; ++s) ahead[s] = issue(s);
 
   // the warp's part of the parameters' gradients in the unit, and where it goes
   F sum_b = splat<P>(0.f), sum_raw = splat<P>(0.f);
@@ -484,31 +501,34 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   constexpr int kEach = 32 / K;  // lanes that end with the same token's sum
   int slot = 0, n = 0, s = 0, fill = kStages - 1;
   for (bool begun = warp > 0;; begun = true) {  // the ring's first tile has none before it
-    const float b_own = sigmoid(logits[0]), slope_own = b_own * sigmoid(-logits[0]);
-#pragma unroll
-    for (int k = 0; k + 1 < kStages - 1; ++k) logits[k] = logits[k + 1];
-    logits[kStages - 2] = issue(fill);
-    fill = fill + 1 == kStages ? 0 : fill + 1;
-    __syncwarp();
-    const int4 t = *reinterpret_cast<const int4*>(&tiles[warp][s]);
-    const int valid = t.x, flags = t.y;
+    const int info = ahead[0].info, valid = info & kTokens;
     if (valid == 0) break;
-    if (flags & kFresh) {
-      const int4 u = reinterpret_cast<const int4*>(&tiles[warp][s])[1];
+    // b, and its slope b (1 - b) without cancellation: 1 - b is e b
+    const float e_own = expf(-ahead[0].logit), b_own = 1.f / (1.f + e_own);
+    const float slope_own = e_own > 3e38f ? 0.f : b_own * (e_own * b_own);
+#pragma unroll
+    for (int k = 0; k + 1 < kStages - 1; ++k) ahead[k] = ahead[k + 1];
+    ahead[kStages - 2] = issue(fill);
+    fill = fill + 1 == kStages ? 0 : fill + 1;
+    if (lane < K) writes[warp][lane] = make_float2(b_own, b_own);
+    if (info & kFresh) {
+      const Entry& t = entries[warp][s];
       if (part != kNone) flush();
-      slot = t.z;
-      n = u.x;
-      part = (size_t)u.w * p.N + n;
+      slot = t.slot;
+      n = t.n;
+      part = (size_t)t.part * p.N + n;
       gc = gate_scale(__ldg(p.A_log + n), p.lower_bound);
       bias = load_const<P>(p.dt_bias + (size_t)n * D + chan);
-      o = slot * p.od.stride_b + n * p.od.stride_n + t.w * orow + chan;
+      o = slot * p.od.stride_b + n * p.od.stride_n + t.row * orow + chan;
       dbeta = static_cast<T*>(p.dbeta) + slot * p.bd.stride_b + n * p.bd.stride_n +
-              (t.w + lane / kEach) * p.bd.stride_s;
+              (t.row + lane / kEach) * p.bd.stride_s;
     }
     F start = splat<P>(0.f);
-    if (flags & kFirst) {
-      if (flags & kCut) start = join<D>(p, tiles[warp][s].map, flags >> kOrder, n, chan);
-      else if (p.begin) start = load<P>(p.begin + ((size_t)slot * p.N + n) * D + chan);
+    if (info & kFirst) {
+      if (info & kCut)
+        start = join<D>(p, entries[warp][s].map, entries[warp][s].order, n, chan);
+      else if (p.begin)
+        start = load<P>(p.begin + ((size_t)slot * p.N + n) * D + chan);
     }
     T* const tg = reinterpret_cast<T*>(stages + s * kStage);
     const T* const tx = tg + kElems + chan;
@@ -525,11 +545,11 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
       // e is kept finite: 1 - sigmoid is e sigmoid, without cancellation, and where the sigmoid
       // is zero so is their product
       const F e = each((load<P>(tg + k * D + chan) + bias) * gc.nz,
-                       [](float z) { return fminf(ex2(z), 3e38f); });
+                       [](float z) { return min_nan(ex2(z), 3e38f); });
       const F sig = each(e + splat<P>(1.f), rcp);
       a[k] = each(sig * gc.l2, ex2);
       w[k] = sig * (e * sig) * (a[k] * slope) * h;
-      h = fma(a[k], h, load<P>(tx + k * D) * __shfl_sync(0xffffffffu, b_own, k));
+      h = fma(a[k], h, load<P>(tx + k * D) * both<P>(writes[warp][k]));
     }
     // lam of a tile with nothing behind it, and the decays from its end
     F lam[K], c0 = splat<P>(0.f);
@@ -543,16 +563,16 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
     F c = start;
     if (begun) {
       ring.wait();
-      if (!(flags & kFirst)) c = load<P>(ring.inbox + chan);
+      if (!(info & kFirst)) c = load<P>(ring.inbox + chan);
     }
     const F behind = c;
     c = fma(a[0], c, c0);
     store(ring.outbox + chan, c);
-    if (!(flags & kStop)) ring.pass();
+    if (!(info & kStop)) ring.pass();
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) lam[k] = fma(a[k + 1], behind, lam[k]);
     lam[K - 1] = lam[K - 1] + behind;
-    if ((flags & (kLast | kEnd)) == (kLast | kEnd) && p.end)
+    if ((info & (kLast | kEnd)) == (kLast | kEnd) && p.end)
       store(p.end + ((size_t)slot * p.N + n) * D + chan, c);
     float dot[K];
     F here_b = splat<P>(0.f), here_raw = splat<P>(0.f);
@@ -563,7 +583,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
       here_b = here_b + w[k];
       if (k < valid) here_raw = fma(w[k], load<P>(tg + k * D + chan) + bias, here_raw);
       dot[k] = sum(lam[k] * load<P>(tx + k * D));
-      lam[k] = lam[k] * __shfl_sync(0xffffffffu, b_own, k);
+      lam[k] = lam[k] * both<P>(writes[warp][k]);
     }
     store_rows<T, D>(static_cast<T*>(p.out) + o, orow, valid, lam);
     store_rows<T, D>(static_cast<T*>(p.dg) + o, orow, valid, w);
