@@ -46,11 +46,6 @@ __device__ __forceinline__ GateScale gate_scale(float A_log, float lower_bound) 
   // never zero: a raw gate of -inf closes the gate whatever A_log is
   return {ea, fminf(-kLog2e * ea, -1.1754944e-38f), lower_bound * kLog2e};
 }
-// sigmoid(z) and, in *t, e^-z (which may be infinite: the sigmoid is then 0)
-__device__ __forceinline__ float gate_sigmoid(const GateScale& c, float raw, float* t) {
-  *t = ex2(c.nz * raw);
-  return rcp(1.0f + *t);
-}
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 // 2 P consecutive channels in pairs, for the packed fp32 instructions

@@ -272,3 +272,69 @@ def test_refusals(bad, cuda_ok):
     with pytest.raises((TypeError, ValueError, kda.KdaError)):
         kda.qk_norm_rope(*a, eps, layout, **kw)
     torch.cuda.synchronize()
+
+
+def test_offsets_past_32_bits(cuda_ok):
+    """Heads 2^31 elements apart, and outputs of more than 2^31 elements: equal heads give equal bits."""
+    D, S = 128, 40
+    d = make("BNSD", 1, 2, 2, S, D, BF, seed=15)
+    near, _ = run_both(d, "BNSD")
+    far = torch.empty((1 << 31) + S * D, dtype=BF, device="cuda")
+    wide = torch.as_strided(far, (1, 2, S, D), (0, 1 << 31, D, 1))
+    for n in ("q", "k", "dq", "dk"):
+        wide.copy_(d[n])
+        got, _ = run_both(dict(d, **{n: wide}), "BNSD")
+        assert all(torch.equal(got[m], near[m]) for m in got), n
+    del far, wide
+    d = make("BSND", 1, 1, 1, 131072, D, BF, seed=16)
+    q, dq = (d[n].expand(1, 131072, 130, D) for n in ("q", "dq"))
+    a = (q, d["k"], d["pos"], d["inv"], d["qw"], d["kw"], EPS, "BSND")
+    out, _ = kda.qk_norm_rope(*a)
+    assert out.numel() > 1 << 31
+    assert torch.equal(out[:, :, :1], out[:, :, -1:])
+    grad = kda.qk_norm_rope_backward(dq, d["dk"], *a)[0]
+    assert torch.equal(grad[:, :, :1], grad[:, :, -1:])
+    one = kda.qk_norm_rope(d["q"], *a[1:])[0]
+    assert torch.equal(one, out[:, :, :1])
+
+
+def test_nan_stays_in_its_row(cuda_ok):
+    """A NaN in a row spoils that row (and the weights' gradients of its side), nothing else."""
+    d = make("TND", 1, 3, 2, 21, 64, BF, seed=17)
+    clean, _ = run_both(d, "TND")
+    bad = dict(d, q=d["q"].clone())
+    bad["q"][7, 1, 3] = float("nan")
+    got, _ = run_both(bad, "TND")
+    row = torch.zeros(21, 3, 1, dtype=torch.bool, device="cuda")
+    row[7, 1] = True
+    for n in ("q", "dq"):
+        assert torch.isnan(torch.where(row, got[n], float("nan"))).all()
+        assert torch.equal(torch.where(row, 0, got[n]), torch.where(row, 0, clean[n]))
+    assert all(torch.equal(got[n], clean[n]) for n in ("k", "dk", "dkw"))
+
+
+def test_captured_training_step(cuda_ok):
+    d = make("TND", 1, 4, 2, 90, 128, FP, seed=18)
+    ts = [d[n].clone().requires_grad_() for n in ("q", "k", "qw", "kw")]
+
+    def step():
+        out = kda.qk_norm_rope(ts[0], ts[1], d["pos"], d["inv"], ts[2], ts[3], EPS, "TND")
+        return torch.autograd.grad(out, ts, [d["dq"], d["dk"]])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    new = make("TND", 1, 4, 2, 90, 128, FP, seed=19)
+    with torch.no_grad():
+        for t, n in zip(ts, ("q", "k", "qw", "kw")):
+            t.copy_(new[n])
+        for n in ("dq", "dk", "pos"):
+            d[n].copy_(new[n])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(captured, step()))

@@ -409,3 +409,144 @@ def test_refusals(bad, cuda_ok):
         else:
             kda.gated_recurrence(*a, **kw)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("layout", ["BNSD", "BSND", "TND"])
+@pytest.mark.parametrize("kind,D", [(BF, 128), (HF, 64), (FP, 128), (FP, 64)])
+def test_cut_sequences(layout, kind, D, cuda_ok):
+    """Long sequences of few heads, which the plan cuts: segments that start from joined maps, next
+    to a sequence that stays whole."""
+    lengths = [2500, 1, 700]
+    d = make(layout, lengths, 2, D, kind, S=None if layout == "TND" else 2600, seed=22)
+    d["A_log"].fill_(1.0)
+    d["dt_bias"].fill_(-1.5)  # slow decays: a segment's start matters far into it
+    assert d["plan"].host[12] > 0 and d["plan"].host[11] > len(lengths)
+    check_all(*run_both(d, -0.5, layout, lengths))
+    check_all(*run_both(d, -0.5, layout, lengths, h0=False, dout=False))
+    check_all(*run_both(d, -0.5, layout, lengths, dfinal=False))
+
+
+def test_cut_sequence_in_place(cuda_ok):
+    """The end of a cut sequence replaces its start while other segments are still at work."""
+    d = make("BNSD", [6000, 4000], 1, 128, BF, S=6000, seed=23)
+    assert d["plan"].host[12] > 0
+    a = list(args(d, -0.25, "BNSD"))
+    out, final = kda.gated_recurrence(*a)
+    for _ in range(3):
+        a[3] = d["h0"].clone()
+        out2, final2 = kda.gated_recurrence(*a, final_state=a[3])
+        assert final2.data_ptr() == a[3].data_ptr()
+        assert torch.equal(out, out2) and torch.equal(final, final2)
+
+
+def test_nan_stays_in_its_channel_and_after_its_token(cuda_ok):
+    """A NaN gate or value spoils its own channel from its token on (dbeta, a sum over channels, from
+    nowhere else), and a NaN gradient its channel up to its token; everything else keeps its bits."""
+    lengths, t, c = [150], 77, 5
+    d = make("TND", lengths, 2, 64, BF, seed=24)
+    clean, _ = run_both(d, -1.0, "TND", lengths)
+    for name in ("x", "g"):
+        bad = dict(d, **{name: d[name].clone()})
+        bad[name][t, 1, c] = float("nan")
+        got, _ = run_both(bad, -1.0, "TND", lengths)
+        spoilt = torch.zeros(150, 2, 64, dtype=torch.bool, device="cuda")
+        spoilt[t:, 1, c] = True
+        assert torch.isnan(got["out"][spoilt]).all()
+        assert torch.equal(got["out"][~spoilt], clean["out"][~spoilt])
+        assert torch.isnan(got["final"][0, 1, c]) and torch.isnan(got["final"]).sum() == 1
+    bad = dict(d, dout=d["dout"].clone())
+    bad["dout"][t, 1, c] = float("nan")
+    got, _ = run_both(bad, -1.0, "TND", lengths)
+    spoilt = torch.zeros(150, 2, 64, dtype=torch.bool, device="cuda")
+    spoilt[:t + 1, 1, c] = True
+    for name in ("dx", "dg"):
+        assert torch.isnan(got[name][spoilt]).all()
+        assert torch.equal(got[name][~spoilt], clean[name][~spoilt]), name
+    assert torch.isnan(got["dbeta"][:t + 1, 1]).all()
+    assert torch.equal(got["dbeta"][t + 1:], clean["dbeta"][t + 1:])
+    assert torch.equal(got["dbeta"][:, 0], clean["dbeta"][:, 0])
+    assert torch.equal(got["out"], clean["out"])
+
+
+def test_offsets_past_32_bits(cuda_ok):
+    """Inputs whose heads lie 2^31 elements apart, and outputs of more than 2^31 elements: every head
+    of equal inputs and parameters gives the same bits, the last as the first."""
+    D, S = 128, 96
+    far = torch.empty((1 << 31) + S * D, dtype=BF, device="cuda")
+    d = make("BNSD", [S], 2, D, BF, seed=25)
+    near, _ = run_both(d, -1.0, "BNSD", [S])
+    wide = torch.as_strided(far, (1, 2, S, D), (0, 1 << 31, D, 1))
+    for name in ("x", "g", "dout"):
+        wide.copy_(d[name])
+        got, _ = run_both(dict(d, **{name: wide}), -1.0, "BNSD", [S])
+        assert all(torch.equal(got[n], near[n]) for n in got), name
+    del far, wide
+    N, S = 130, 131072
+    one = make("BNSD", [S], 1, D, BF, seed=26)
+    every = {n: one[n].expand(1, N, *one[n].shape[2:]) for n in ("x", "g", "beta", "dout")}
+    every |= {n: one[n].expand(1, N, D).contiguous() for n in ("h0", "dfinal")}
+    every |= {"A_log": one["A_log"].expand(N).contiguous(),
+              "dt_bias": one["dt_bias"].expand(N, D).contiguous()}
+    every["plan"] = kda.recurrence_plan(every["x"], "BNSD")
+    a = args(every, -1.0, "BNSD")
+    out, final, states = kda.gated_recurrence(*a, return_states=True)
+    assert out.numel() > 1 << 31
+    grads = kda.gated_recurrence_backward(every["dout"], every["dfinal"], *a, states)
+    for t in (out, final) + grads[:4]:
+        assert torch.equal(t[:, :1], t[:, -1:]) and torch.equal(t[:, :1], t[:, 64:65])
+    assert torch.equal(grads[4][:1], grads[4][-1:]) and torch.equal(grads[5][:1], grads[5][-1:])
+    few = kda.gated_recurrence(*args(one, -1.0, "BNSD"))[0]  # cut, so not the same bits
+    diff = (few[0, 0].float() - out[0, -1].float()).abs()
+    # each is within half a step of bf16 of what its own fp32 error leaves, far below another half
+    assert (diff <= 2 * 2.0 ** -8 * few[0, 0].float().abs() + 1e-5).all()
+
+
+def test_captured_training_step(cuda_ok):
+    """Forward and backward through torch.autograd in one graph, replayed with new data."""
+    lengths = [300, 45]
+    d = make("TND", lengths, 2, 64, FP, seed=27)
+    ts = leaves(d)
+
+    def step():
+        out, final = kda.gated_recurrence(*ts, -1.0, "TND", d["plan"])
+        return torch.autograd.grad([out, final], ts, [d["dout"], d["dfinal"]])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    new = make("TND", lengths, 2, 64, FP, seed=28)
+    with torch.no_grad():
+        for t, name in zip(ts, ("x", "g", "beta", "h0", "A_log", "dt_bias")):
+            t.copy_(new[name])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(captured, step()))
+
+
+def test_calls_from_two_threads(cuda_ok):
+    """One plan, a thread and a stream each, first calls of a kernel included."""
+    from concurrent.futures import ThreadPoolExecutor
+    lengths = [900, 70]
+    d = make("TND", lengths, 3, 64, HF, seed=29)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+
+    def work(s):
+        with torch.cuda.stream(s):
+            a = args(d, -1.0, "TND")
+            res = None
+            for _ in range(5):
+                out, final, states = kda.gated_recurrence(*a, return_states=True)
+                res = (out, final) + kda.gated_recurrence_backward(d["dout"], d["dfinal"], *a, states)
+            s.synchronize()
+            return res
+
+    with ThreadPoolExecutor(2) as pool:
+        got = list(pool.map(work, streams))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    check_all(*run_both(d, -1.0, "TND", lengths))
