@@ -66,9 +66,10 @@ _here = contextlib.nullcontext()
 def launch_on(device: torch.device, stream):
     """(context, cuda stream handle): inside the context the call's device is the current one, and
     what is allocated belongs to the stream that the kernels run on."""
-    if stream is None and device.index == torch.cuda.current_device():
+    index = device.index
+    if stream is None and index == torch._C._cuda_getDevice():
         # the handle alone: a Stream object would cost a call 2 us
-        return _here, torch._C._cuda_getCurrentRawStream(device.index)
+        return _here, torch._C._cuda_getCurrentRawStream(index)
     s = stream if stream is not None else torch.cuda.current_stream(device)
     if s.device != device:
         raise ValueError(f"stream is on {s.device}, the tensors on {device}")

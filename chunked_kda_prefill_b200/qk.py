@@ -23,6 +23,10 @@ from ._views import (dense_like, dtype_code, expect, expect_dense, launch_on, ne
 from .api import LAYOUTS, _ptr
 
 
+_LIMIT = 1 << 31
+_workspace_bytes = {}
+
+
 def _check(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved) -> KdaQkShape:
     dev = q.device
     if dev.type != "cuda":
@@ -41,7 +45,7 @@ def _check(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleav
     else:
         (B, Nq, S, D), Nk = q.shape, k.shape[1]
         k_shape, tokens = (B, Nk, S, D), (B, S)
-    if max(B, S, Nq, Nk, D) >= 1 << 31:
+    if B >= _LIMIT or S >= _LIMIT or Nq >= _LIMIT or Nk >= _LIMIT or D >= _LIMIT:
         raise KdaError(3, "a size of q or k does not fit 32 bits")
     expect(k, "k", q.dtype, dev, k_shape)
     if positions is not None:
@@ -52,9 +56,10 @@ def _check(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleav
             raise KdaError(3, "inv_freq must be a vector")
         turned = 2 * inv_freq.shape[0]
         expect_dense(inv_freq, "inv_freq", torch.float32, dev, inv_freq.shape)
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            expect_dense(w, name, torch.float32, dev, (D,))
+    if q_weight is not None:
+        expect_dense(q_weight, "q_weight", torch.float32, dev, (D,))
+    if k_weight is not None:
+        expect_dense(k_weight, "k_weight", torch.float32, dev, (D,))
     return KdaQkShape(LAYOUTS[layout], B, Nq, Nk, S, D, code, turned, int(bool(interleaved)), eps)
 
 
@@ -62,9 +67,10 @@ def _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interle
              stream):
     shape = _check(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved)
     dev = q.device
-    for t, name, like in ((q_out, "q_out", q), (k_out, "k_out", k)):
-        if t is not None:
-            expect_dense(t, name, q.dtype, dev, like.shape)
+    if q_out is not None:
+        expect_dense(q_out, "q_out", q.dtype, dev, q.shape)
+    if k_out is not None:
+        expect_dense(k_out, "k_out", q.dtype, dev, k.shape)
     ctx, handle = launch_on(dev, stream)
     with ctx:
         if q_out is None:
@@ -96,9 +102,12 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k
         if t is not None:
             expect_dense(t, name, q.dtype, dev, like.shape)
     L = _lib.load()
-    ws_bytes = ctypes.c_size_t(0)
-    check(L.kda_qk_norm_rope_workspace_size(ctypes.byref(shape), ctypes.byref(ws_bytes)),
-          "kda_qk_norm_rope_workspace_size")
+    ws_bytes = _workspace_bytes.get(shape.D)  # it goes by the head dim alone
+    if ws_bytes is None:
+        size = ctypes.c_size_t(0)
+        check(L.kda_qk_norm_rope_workspace_size(ctypes.byref(shape), ctypes.byref(size)),
+              "kda_qk_norm_rope_workspace_size")
+        ws_bytes = _workspace_bytes[shape.D] = size.value
     ctx, handle = launch_on(dev, stream)
     with ctx:
         if dq is None:
@@ -107,12 +116,12 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k
             dk = dense_like(k)
         dqw = torch.empty_like(q_weight) if q_weight is not None else None
         dkw = torch.empty_like(k_weight) if k_weight is not None else None
-        ws = torch.empty(ws_bytes.value, dtype=torch.uint8, device=dev)
+        ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         check(L.kda_qk_norm_rope_backward(
             ctypes.byref(shape), ctypes.byref(view(dq_out, "dq_out", layout)),
             ctypes.byref(view(dk_out, "dk_out", layout)), ctypes.byref(view(q, "q", layout)),
             ctypes.byref(view(k, "k", layout)), _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
-            _ptr(k_weight), ws.data_ptr(), ws_bytes.value, dq.data_ptr(), dk.data_ptr(),
+            _ptr(k_weight), ws.data_ptr(), ws_bytes, dq.data_ptr(), dk.data_ptr(),
             _ptr(dqw), _ptr(dkw), handle), "kda_qk_norm_rope_backward")
     return dq, dk, dqw, dkw
 

@@ -23,10 +23,11 @@ import torch
 
 from . import _lib
 from ._lib import KdaError, KdaRecurrenceShape, check
-from ._views import (dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, view,
+from ._views import (DTYPES, dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, view,
                      viewable)
 from .api import LAYOUTS, _ptr
 
+_F32 = torch.float32
 _STATUS_BYTES = 256  # a workspace that holds the device status alone
 _P_I32 = ctypes.POINTER(ctypes.c_int32)
 
@@ -46,10 +47,13 @@ class KdaRecurrencePlan:
     def __post_init__(self):
         sh = self.shape
         self._host_ptr = self.host.ctypes.data_as(_P_I32)
-        self._rows = {"BNSD": (sh.B, sh.N, sh.S), "BSND": (sh.B, sh.S, sh.N),
-                      "TND": (sh.S, sh.N)}[self.layout]
-        self._x = torch.Size(self._rows + (sh.D,))
+        self._rows = torch.Size({"BNSD": (sh.B, sh.N, sh.S), "BSND": (sh.B, sh.S, sh.N),
+                                 "TND": (sh.S, sh.N)}[self.layout])
+        self._x = self._rows + torch.Size((sh.D,))
         self._state = torch.Size((sh.B, sh.N, sh.D))
+        self._heads = torch.Size((sh.N,))
+        self._params = torch.Size((sh.N, sh.D))
+        self._index = self.dev.get_device()
         self._shapes = {}
 
     def _shape_for(self, dtype: int) -> KdaRecurrenceShape:
@@ -122,6 +126,19 @@ def recurrence_plan(x: torch.Tensor, layout: str, cu_seqlens=None) -> KdaRecurre
 
 def _check(plan, layout, dev, x, g, beta, initial_state, A_log, dt_bias):
     """Types, devices and shapes of the inputs against the plan; the element type's code."""
+    kind, index, shape = x.dtype, plan._index, plan._x
+    code = DTYPES.get(kind)
+    # all of it at once (half the time of the checks below, which name what is wrong)
+    if (index >= 0 and x.get_device() == g.get_device() == beta.get_device() == A_log.get_device()
+            == dt_bias.get_device() == index and plan.layout == layout and code is not None
+            and g.dtype is kind and beta.dtype is kind and A_log.dtype is dt_bias.dtype is _F32
+            and x.shape == g.shape == shape and beta.shape == plan._rows
+            and A_log.shape == plan._heads and dt_bias.shape == plan._params
+            and A_log.is_contiguous() and dt_bias.is_contiguous()
+            and (initial_state is None
+                 or (initial_state.get_device() == index and initial_state.dtype is _F32
+                     and initial_state.shape == plan._state and initial_state.is_contiguous()))):
+        return code
     if dev.type != "cuda":
         raise ValueError("the gated recurrence runs on a CUDA device only")
     if plan.layout != layout:
@@ -162,7 +179,7 @@ def _forward(x, g, beta, initial_state, A_log, dt_bias, lower_bound, layout, pla
         if out is None:
             out = dense_like(x)
         if final_state is None:
-            final_state = (dense_like(initial_state) if initial_state is not None else
+            final_state = (torch.empty_like(initial_state) if initial_state is not None else
                            torch.empty(plan._state, dtype=torch.float32, device=dev))
         states = A_log.new_empty(plan.states_shape) if want_states else None
         if workspace is None and plan.workspace_bytes == _STATUS_BYTES:
@@ -288,15 +305,21 @@ def gated_recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound: float,
     code = dtype_code(x, "x")
     if x.dim() != 3:
         raise KdaError(3, "gated_recurrence_step expects x [B, N, D]")
-    shape = x.shape
+    shape, kind, index = x.shape, x.dtype, dev.index
     B, N, D = shape
-    expect_dense(x, "x", x.dtype, dev, shape)
-    expect_dense(g, "g", x.dtype, dev, shape)
-    expect_dense(beta, "beta", x.dtype, dev, shape[:2])
-    expect_dense(A_log, "A_log", torch.float32, dev, shape[1:2])
-    expect_dense(dt_bias, "dt_bias", torch.float32, dev, shape[1:])
+    # all of it at once, then what is wrong
+    if not (g.get_device() == beta.get_device() == A_log.get_device() == dt_bias.get_device() == index
+            and g.dtype is kind and beta.dtype is kind and A_log.dtype is dt_bias.dtype is _F32
+            and g.shape == shape and beta.shape == (B, N) and A_log.shape == (N,)
+            and dt_bias.shape == (N, D) and x.is_contiguous() and g.is_contiguous()
+            and beta.is_contiguous() and A_log.is_contiguous() and dt_bias.is_contiguous()):
+        expect_dense(x, "x", kind, dev, shape)
+        expect_dense(g, "g", kind, dev, shape)
+        expect_dense(beta, "beta", kind, dev, shape[:2])
+        expect_dense(A_log, "A_log", _F32, dev, shape[1:2])
+        expect_dense(dt_bias, "dt_bias", _F32, dev, shape[1:])
     if state is not None:
-        expect_dense(state, "state", torch.float32, dev, shape)
+        expect_dense(state, "state", _F32, dev, shape)
     if out is not None:
         expect_dense(out, "out", x.dtype, dev, shape)
     if state_out is not None:
@@ -304,9 +327,9 @@ def gated_recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound: float,
     ctx, handle = launch_on(dev, stream)
     with ctx:
         if out is None:
-            out = dense_like(x)
+            out = torch.empty_like(x)
         if state_out is None:
-            state_out = (dense_like(state) if state is not None else
+            state_out = (torch.empty_like(state) if state is not None else
                          torch.empty(shape, dtype=torch.float32, device=dev))
         check(_lib.load().kda_recurrence_step(
             B, N, D, code, x.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state),
