@@ -446,7 +446,7 @@ __device__ __forceinline__ float warp_sums(float (&v)[K], int lane) {
 }
 
 // 4x32x16384 bf16: 490 us, 5.75 TB/s (6.4 TB/s where 148 units keep every multiprocessor busy).  From
-// inputs in L2 it takes 466 us: 43 instructions a value, 57 % of the issue slots.  13 or 14 warps spill
+// inputs in L2 it takes 466 us: 35 instructions a value, 57 % of the issue slots.  13 or 14 warps spill
 // registers (840-910 us); 11 warps with a stage more take 520 us.
 template <class T, int D>
 __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
