@@ -36,7 +36,8 @@ struct RecParams {
   const int32_t* plan;
   int32_t checksum;
   int32_t N, units;   // units: segments times heads
-  int32_t slot_rows;  // rows that a slot's outputs have, padding included; 0 for packed rows
+  int32_t slot_rows;  // rows that a slot's outputs have; 0 where none lies behind a sequence's tokens
+  bool spread;        // all blocks write the zeros behind every sequence, not just their units'
   const float* begin;  // [B][N][D] the walk's start (forward h0, backward dfinal), or null for zeros
   const float* A_log;
   const float* dt_bias;
@@ -103,7 +104,8 @@ enum : int {
 // the segment in the walk of its sequence.
 struct __align__(16) Entry {
   int slot, row, n, place;
-  int map, part, order, unused;
+  int map, part, order;
+  int parts;  // rows of partial gradients that the unit has behind the warp's own
 };
 
 // Whether the plan on the device is the host's; block 0 leaves the status.
@@ -145,10 +147,10 @@ struct Walk {
     return reinterpret_cast<const char*>(at<T>(v, slot, n, row + lane / kLanes)) +
            lane % kLanes * 16;
   }
-  // zero(slot, n, row, rows): called for the rows behind a sequence's last token
+  // zero(slot, n, row, end, warps, warp): writes the rows behind a sequence's last token, a share of them
   template <class Zero>
   __device__ void enter(const RecParams& p, Zero&& zero) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (;; ++round) {
       const long long unit = unit_of(round);
       done = unit >= p.units;
@@ -159,8 +161,8 @@ struct Walk {
       slot = r0.x; start = r0.y; len = r0.z; tile0 = r0.w;
       part = r1.x; segment = r1.y; segments = r1.z; map = r1.w;
       tiles = (len + K - 1) / K;
-      if (p.slot_rows && segment + 1 == segments)
-        zero(slot, n, start + len, p.slot_rows - start - len);
+      if (p.slot_rows && !p.spread && segment + 1 == segments)
+        zero(slot, n, start + len, p.slot_rows, W, warp);
       if (t < tiles) break;
       t -= tiles;
     }
@@ -174,9 +176,30 @@ struct Walk {
       state = reinterpret_cast<const char*>(p.states + ((size_t)(tile0 + k) * p.N + n) * D) + lane * 16;
     }
   }
+  // The rows behind all sequences, over all warps of the grid (there are fewer units than
+  // multiprocessors); the records are read 32 at a time.
+  template <class Zero>
+  __device__ void zero_all(const RecParams& p, Zero&& zero) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, records = p.units / p.N;
+    for (int base = 0; base < records; base += 32) {
+      int at = 0, row = p.slot_rows;
+      if (base + lane < records) {
+        const int4 r0 = __ldg(record(p, base + lane)), r1 = __ldg(record(p, base + lane) + 1);
+        at = r0.x;
+        if (r1.y + 1 == r1.z) row = r0.y + r0.z;
+      }
+      for (unsigned left = __ballot_sync(0xffffffffu, row < p.slot_rows); left; left &= left - 1) {
+        const int from = __ffs(left) - 1;
+        const int s = __shfl_sync(0xffffffffu, at, from), r = __shfl_sync(0xffffffffu, row, from);
+        for (int h = 0; h < p.N; ++h)
+          zero(s, h, r, p.slot_rows, W * gridDim.x, warp * gridDim.x + blockIdx.x);
+      }
+    }
+  }
   template <class Zero>
   __device__ void begin(const RecParams& p, int warp, Zero&& zero) {
     dout = state = nullptr;
+    if (p.spread) zero_all(p, zero);
     round = 0;
     t = warp;
     enter(p, zero);
@@ -229,7 +252,7 @@ struct Walk {
         if (fresh && lane == 0) {
           int4* const to = reinterpret_cast<int4*>(entry);
           to[0] = make_int4(slot, start + k * K, n, tile0 + k);
-          to[1] = make_int4(map, part + t, order, 0);
+          to[1] = make_int4(map, part + t, order, min(kRecRing, tiles) - t);
         }
       }
       copy_rows(stage, g, p.copy_step[0], valid);
@@ -340,9 +363,9 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
   uint8_t* const stages = smem + warp * kStages * kStage;
   T* const out = static_cast<T*>(p.out);
   const long long orow = p.od.stride_s;
-  auto zero = [&](int slot, int n, int row, int rows) {
-    T* const o = out + slot * p.od.stride_b + n * p.od.stride_n + row * orow + chan;
-    for (int k = warp; k < rows; k += W) store(o + k * orow, splat<P>(0.f));
+  auto zero = [&](int slot, int n, int row, int end, int warps, int mine) {
+    T* const o = out + slot * p.od.stride_b + n * p.od.stride_n + chan;
+    for (long long k = row + mine; k < end; k += warps) store(o + k * orow, splat<P>(0.f));
   };
   Walk<T, D, false> walk;
   walk.begin(p, warp, zero);
@@ -471,11 +494,10 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
         store(reinterpret_cast<T*>(stages + s * kStage) + 2 * kElems + k * D + chan,
               splat<P>(0.f));
   }
-  auto zero = [&](int slot, int n, int row, int rows) {
-    const long long o = slot * p.od.stride_b + n * p.od.stride_n + row * orow + chan;
-    T* const ob = static_cast<T*>(p.dbeta) + slot * p.bd.stride_b + n * p.bd.stride_n +
-                  row * p.bd.stride_s;
-    for (int k = warp; k < rows; k += W) {
+  auto zero = [&](int slot, int n, int row, int end, int warps, int mine) {
+    const long long o = slot * p.od.stride_b + n * p.od.stride_n + chan;
+    T* const ob = static_cast<T*>(p.dbeta) + slot * p.bd.stride_b + n * p.bd.stride_n;
+    for (long long k = row + mine; k < end; k += warps) {
       store(static_cast<T*>(p.out) + o + k * orow, splat<P>(0.f));
       store(static_cast<T*>(p.dg) + o + k * orow, splat<P>(0.f));
       if (lane == 0) ob[k * p.bd.stride_s] = from_f32<T>(0.f);
@@ -494,13 +516,19 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   F sum_b = splat<P>(0.f), sum_raw = splat<P>(0.f);
   constexpr size_t kNone = ~(size_t)0;
   size_t part = kNone;
+  int parts = 0;
   auto flush = [&]() {
     float raw = sum(sum_raw);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) raw += __shfl_xor_sync(0xffffffffu, raw, o);
-    store(p.part_bias + part * D + chan, sum_b);
-    if (lane == 0) p.part_A[part] = raw;
-    sum_b = sum_raw = splat<P>(0.f);
+    // a unit has up to kRecRing rows, more than the ring has warps: zeros in those left over
+    for (int i = 0; i < parts; i += W) {
+      store(p.part_bias + part * D + chan, sum_b);
+      if (lane == 0) p.part_A[part] = raw;
+      sum_b = sum_raw = splat<P>(0.f);
+      raw = 0.f;
+      part += (size_t)W * p.N;
+    }
   };
 
   GateScale gc{};
@@ -526,6 +554,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
       slot = t.slot;
       n = t.n;
       part = (size_t)t.part * p.N + n;
+      parts = t.parts;
       gc = gate_scale(__ldg(p.A_log + n), p.lower_bound);
       bias = load_const<P>(p.dt_bias + (size_t)n * D + chan);
       o = slot * p.od.stride_b + n * p.od.stride_n + t.row * orow + chan;
@@ -675,7 +704,9 @@ __global__ void __launch_bounds__(32 * kMapWarps, 1) rec_maps_kernel(const __gri
       now = next;
     }
   }
-  store(&sa[warp][chan], pa);
+  // a product that is too small for fp32 stays above zero, so that an infinite state stays infinite
+  auto above_zero = [](float v) { return v == 0.f ? 1.4e-45f : v; };
+  store(&sa[warp][chan], each(pa, above_zero));
   store(&sh[warp][chan], ph);
   __syncthreads();
   if (warp > 0) return;
@@ -689,7 +720,7 @@ __global__ void __launch_bounds__(32 * kMapWarps, 1) rec_maps_kernel(const __gri
     ph = fma(ka, ph, load<P>(&sh[w][chan]));
   }
   float* m = p.maps + ((size_t)(r1.w + order + 1) * p.N + n) * 2 * D + chan;
-  store(m, pa);
+  store(m, each(pa, above_zero));
   store(m + D, ph);
   if (order == 0) {
     m -= (size_t)p.N * 2 * D;
@@ -701,25 +732,22 @@ __global__ void __launch_bounds__(32 * kMapWarps, 1) rec_maps_kernel(const __gri
 // ddt_bias and dA_log: the warps' parts in a fixed order, in fp64.  A block has 32 channels of a
 // head (the first one of a head its dA_log too); 32 threads a channel take the parts in turn.  About 4
 // us behind the walk, most of it the launch.
-template <int D, int W>
+template <int D>
 __global__ void __launch_bounds__(1024) rec_params_kernel(const __grid_constant__ RecParams p,
-                                                          float* dA_log, float* ddt_bias) {
+                                                          int parts, float* dA_log,
+                                                          float* ddt_bias) {
   __shared__ double red[32][33];
-  constexpr int kBlocks = D / 32, K = Shape<D>::K;
+  constexpr int kBlocks = D / 32;
   const int n = blockIdx.x / kBlocks, d0 = blockIdx.x % kBlocks * 32;
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, parts = p.units / p.N * W;
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
   wait_dependencies();
   if (p.plan[RH_CHECKSUM] != p.checksum) return;
   double sum = 0, raw = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = row; i < parts; i += 32) {
-    const int r = i / W, j = i - r * W;
-    const int4 r0 = __ldg(record(p, r));
-    if (j < (r0.z + K - 1) / K) {
-      const size_t part = (size_t)(__ldg(&record(p, r)[1].x) + j) * p.N + n;
-      sum += p.part_bias[part * D + d0 + lane];
-      if (lane == 0) raw += p.part_A[part];
-    }
+    const size_t part = (size_t)i * p.N + n;
+    sum += p.part_bias[part * D + d0 + lane];
+    if (lane == 0) raw += p.part_A[part];
   }
   red[row][lane] = sum;
   __syncthreads();
@@ -811,7 +839,7 @@ kda_status_t prepare(const kda_recurrence_shape_t* shape, const int32_t* plan_ho
   p->checksum = plan_host[RH_CHECKSUM];
   p->N = shape->N;
   p->units = plan_host[RH_RECORDS] * shape->N;
-  p->slot_rows = shape->layout == KDA_LAYOUT_TND ? 0 : shape->S;
+  p->slot_rows = plan_host[RH_PADDED] ? shape->S : 0;
   p->A_log = A_log;
   p->dt_bias = dt_bias;
   p->lower_bound = lower_bound;
@@ -840,7 +868,7 @@ struct Scratch {
 };
 
 // Launches a pass: the maps where sequences are cut, and the walk, a block on every multiprocessor
-// that has a unit.
+// that has a unit or rows to write zeros to.
 template <class T, int D, bool BACKWARD, class Kernel>
 cudaError_t launch(Kernel kernel, PerDevice& once, RecParams& p, const int32_t* plan,
                    cudaStream_t s) {
@@ -855,7 +883,8 @@ cudaError_t launch(Kernel kernel, PerDevice& once, RecParams& p, const int32_t* 
     return err == cudaSuccess ? cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, d) : err;
   });
   if (e != cudaSuccess) return e;
-  const int blocks = std::min(sms, p.units);
+  p.spread = p.slot_rows && p.units < sms;
+  const int blocks = p.spread ? sms : std::min(sms, p.units);
   constexpr int K = Shape<D>::K, kCopy = 512 / (D * (int)sizeof(T));
   const kda_view_t* const views[] = {&p.g, &p.x, &p.dout, &p.beta};
   for (int i = 0; i < 4; ++i) {
@@ -1011,8 +1040,8 @@ extern "C" kda_status_t kda_recurrence_backward(
     using T = std::remove_pointer_t<decltype(tag)>;
     const cudaError_t err = launch_backward<T, D>(p, plan_host, s);
     if (err != cudaSuccess) return err;
-    return launch_early(rec_params_kernel<D, Block<T, true>::kWarps>, shape->N * (D / 32), 1024, 0,
-                        s, p, dA_log, ddt_bias);
+    return launch_early(rec_params_kernel<D>, shape->N * (D / 32), 1024, 0,
+                        s, p, plan_host[RH_PARTS], dA_log, ddt_bias);
   });
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -19,10 +19,10 @@ constexpr int kRecSpread = 148;  // multiprocessors that a plan spreads long seq
 
 // RH_TILES is the number of tiles in one head, RH_MAPS the rows of maps that the segments of cut
 // sequences need (0: none is cut), RH_PARTS the rows of the parameters' partial gradients,
-// RH_LONGEST the tiles of the longest segment.
+// RH_LONGEST the tiles of the longest segment, RH_PADDED whether rows lie behind a sequence's tokens.
 enum RecHeader : int {
   RH_MAGIC = 0, RH_VERSION, RH_HEADER_WORDS, RH_RECORD_WORDS, RH_LAYOUT, RH_B, RH_N, RH_S, RH_D,
-  RH_TILE_ROWS, RH_TILES, RH_RECORDS, RH_MAPS, RH_PARTS, RH_LONGEST, RH_TABLE_HASH = 16,
+  RH_TILE_ROWS, RH_TILES, RH_RECORDS, RH_MAPS, RH_PARTS, RH_LONGEST, RH_PADDED, RH_TABLE_HASH,
   RH_CHECKSUM = kRecHeader - 1
 };
 // RR_SLOT is the sequence, RR_START the segment's first token within its slot (or in the packed

@@ -114,6 +114,7 @@ kda_status_t build(const kda_recurrence_shape_t& s, const int32_t* cu, int32_t* 
   std::vector<Segment> segs;
   segs.reserve(cut.segments);
   long long maps = 0;
+  bool padded = false;
   each_length(s, cu, [&](int b, int32_t len) {
     const long long tiles = tiles_of(len, R), count = segments_of(tiles, cut.most);
     for (long long k = 0; k < count; ++k) {
@@ -122,6 +123,7 @@ kda_status_t build(const kda_recurrence_shape_t& s, const int32_t* cu, int32_t* 
                       (int32_t)count, (int32_t)maps});
     }
     if (count > 1) maps += count;
+    padded |= !tnd && len < s.S;
   });
   std::stable_sort(segs.begin(), segs.end(),
                    [](const Segment& a, const Segment& d) { return a.len > d.len; });
@@ -157,6 +159,7 @@ kda_status_t build(const kda_recurrence_shape_t& s, const int32_t* cu, int32_t* 
   plan[RH_MAPS] = (int32_t)maps;
   plan[RH_PARTS] = (int32_t)part;
   plan[RH_LONGEST] = (int32_t)tiles_of(segs[0].len, R);
+  plan[RH_PADDED] = padded;
   plan[RH_TABLE_HASH] = (int32_t)(fnv(plan + kRecHeader, segs.size() * kRecRecord) & 0x7fffffff);
   plan[RH_CHECKSUM] = (int32_t)(fnv(plan, RH_CHECKSUM) & 0x7fffffff);
   return KDA_OK;

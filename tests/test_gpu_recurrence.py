@@ -550,3 +550,39 @@ def test_calls_from_two_threads(cuda_ok):
         got = list(pool.map(work, streams))
     assert all(torch.equal(a, b) for a, b in zip(*got))
     check_all(*run_both(d, -1.0, "TND", lengths))
+
+
+@pytest.mark.parametrize("lengths,cut", [([150], False), ([4000], True)])
+def test_infinite_values_stay_infinite(lengths, cut, cuda_ok):
+    """An infinite value makes its channel's state infinite for good, however small the decays that
+    follow multiply to, and touches nothing else."""
+    d = make("TND", lengths, 2, 64, BF, seed=30)
+    if not cut:
+        lengths = [150] + [1] * 100  # enough units to leave every sequence whole
+        d = make("TND", lengths, 2, 64, BF, seed=30)
+    assert (d["plan"].host[12] > 0) == cut
+    clean, _ = kda.gated_recurrence(*args(d, -5.0, "TND"))
+    d["x"] = d["x"].clone()
+    d["x"][77, 1, 5] = float("inf")
+    out, final = kda.gated_recurrence(*args(d, -5.0, "TND"))
+    spoilt = torch.zeros(clean.shape, dtype=torch.bool, device="cuda")
+    spoilt[77:lengths[0], 1, 5] = True
+    assert (out[spoilt] == float("inf")).all() and final[0, 1, 5] == float("inf")
+    assert torch.equal(out[~spoilt], clean[~spoilt])
+
+
+def test_long_padding_behind_few_sequences(cuda_ok):
+    """Two heads, slots of 20000 rows: the zeros come from every block, in all layouts' strides."""
+    lengths = [3, 20000, 900]
+    for layout in ("BNSD", "BSND"):
+        d = make(layout, lengths, 2, 64, HF, S=20000, seed=31)
+        for name in ("out", "dx", "dg"):
+            torch.full(d["x"].shape, 7.0, dtype=HF, device="cuda")  # what the results' memory may hold
+        a = args(d, -5.0, layout)
+        out, final, states = kda.gated_recurrence(*a, return_states=True)
+        grads = kda.gated_recurrence_backward(d["dout"], d["dfinal"], *a, states)
+        for t in (out,) + grads[:3]:
+            for b, n in enumerate(lengths):
+                slot = t[b] if layout == "BSND" else t[b].transpose(0, 1)
+                assert torch.count_nonzero(slot[n:]) == 0
+                assert torch.isfinite(slot[:n]).all() and torch.count_nonzero(slot[:n]) > 0

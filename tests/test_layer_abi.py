@@ -90,6 +90,7 @@ def test_plan_records(L, D, N, layout, S, lengths):
         assert max(lens) - min(lens) <= 1
         maps += len(mine) if len(mine) > 1 else 0
     assert int(p[12]) == maps
+    assert int(p[15]) == (layout != 2 and min(lengths) < S)
     if maps:  # a cut pays only where it fills the machine
         assert len(rec) * N <= 8 * 148
     floats = ctypes.c_size_t(0)
@@ -113,7 +114,7 @@ def test_recurrence_plan_capacity_and_corruption(L):
         a.ctypes.data_as(P_I32), a.size if k is None else k, 0, ctypes.byref(n))
     assert ok(p) == 0 and n.value >= 256
     assert ok(p, p.size - 1) == PLAN and ok(p, 3) == PLAN
-    for word in (0, 4, 5, 10, 11, 12, 13, 14, 16, 23):
+    for word in (0, 4, 5, 10, 11, 12, 13, 14, 15, 16, 23):
         bad = p.copy()
         bad[word] += 1
         assert ok(bad) == PLAN, word
