@@ -1,7 +1,7 @@
 // kda_recurrence.cu -- the gated recurrence, the vector form of the KDA state:
 //     a_t = exp(lb sigmoid(e^A (g_t + bias))),  h_t = a_t h_{t-1} + sigmoid(beta_t) x_t.
 //
-// A ring of warps, a block's, walks one segment (a sequence, or a part of a long one) of one head, a
+// A ring of warps, a block's (a single warp where segments are many and short), walks one segment (a sequence, or a part of a long one) of one head, a
 // tile of 1024 values a warp at a time: the warp's own copies bring its next tiles to shared memory, it
 // forms all decays and writes of its tile and what the tile makes of a state of zero, waits for the
 // state that the warp before it leaves, passes on the state after the tile (one multiply-add) and only
@@ -123,23 +123,25 @@ __device__ __forceinline__ const int4* record(const RecParams& p, int i) {
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
-// A warp's way through the tiles of its block's units, and the copies of the next one.  The units
-// are dealt to the blocks in rounds, every other one in reverse, so that with the plan's order
-// (longest first) no block gets the longer unit of every round.
-template <class T, int D, bool BACKWARD>
+// A warp's way through the tiles of its block's (or its own) units, and the copies of the next one.
+// The units are dealt to the blocks in rounds, every other one in reverse, so that with the plan's
+// order (longest first) no block gets the longer unit of every round.
+template <class T, int D, bool BACKWARD, bool SOLO>
 struct Walk {
   using B = Block<T, BACKWARD>;
   static constexpr int K = Shape<D>::K, W = B::kWarps, kRow = D * (int)sizeof(T);
+  static constexpr int kRing = SOLO ? 1 : W;  // warps that walk a unit
   static constexpr int kLanes = kRow / 16;    // lanes of a row's copy
   static constexpr int kRows = 32 / kLanes;   // rows of a copy
   int slot, start, len, tile0;        // the record
   int part, segment, segments, map;
   int n, t, tiles, round;
+  int place, places;                  // the warp's, or its block's, among those that units go to
   bool fresh, done;
   const char *g, *x, *dout, *beta, *state;  // the lane's, of the next tile
 
-  __device__ static long long unit_of(int round) {
-    return (long long)round * gridDim.x + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+  __device__ long long unit_of(int round) const {
+    return (long long)round * places + (round & 1 ? places - 1 - place : place);
   }
   // the lane's part of a tile's first copy
   __device__ const char* lane_rows(const kda_view_t& v, int row) const {
@@ -162,7 +164,7 @@ struct Walk {
       part = r1.x; segment = r1.y; segments = r1.z; map = r1.w;
       tiles = (len + K - 1) / K;
       if (p.slot_rows && !p.spread && segment + 1 == segments)
-        zero(slot, n, start + len, p.slot_rows, W, warp);
+        zero(slot, n, start + len, p.slot_rows, kRing, SOLO ? 0 : warp);
       if (t < tiles) break;
       t -= tiles;
     }
@@ -200,21 +202,23 @@ struct Walk {
   __device__ void begin(const RecParams& p, int warp, Zero&& zero) {
     dout = state = nullptr;
     if (p.spread) zero_all(p, zero);
+    places = SOLO ? gridDim.x * W : gridDim.x;
+    place = SOLO ? blockIdx.x + warp * gridDim.x : blockIdx.x;
     round = 0;
-    t = warp;
+    t = SOLO ? 0 : warp;
     enter(p, zero);
   }
   template <class Zero>
   __device__ void next(const RecParams& p, Zero&& zero) {
     fresh = false;
-    t += W;
+    t += kRing;
     if (t < tiles) {
       g += p.tile_step[0];
       x += p.tile_step[1];
       beta += p.tile_step[3];
       if (BACKWARD) {
         dout += p.tile_step[2];
-        state -= (size_t)W * p.N * D * 4;
+        state -= (size_t)kRing * p.N * D * 4;
       }
       return;
     }
@@ -252,7 +256,7 @@ struct Walk {
         if (fresh && lane == 0) {
           int4* const to = reinterpret_cast<int4*>(entry);
           to[0] = make_int4(slot, start + k * K, n, tile0 + k);
-          to[1] = make_int4(map, part + t, order, min(kRecRing, tiles) - t);
+          to[1] = make_int4(map, part + t, order, min(SOLO ? 1 : kRecRing, tiles) - t);
         }
       }
       copy_rows(stage, g, p.copy_step[0], valid);
@@ -298,17 +302,23 @@ __device__ __noinline__ Pairs<D / 64> join(const RecParams& p, int map, int orde
 // A warp's place in its block's ring: the state is handed on through shared memory, with a barrier of
 // the two warps that only the later one waits at.  (One warp more that runs through maps which the
 // others post took 220 ns a tile, a wait at an mbarrier and two accesses to shared memory.)
-template <int W, int D>
+template <int W, int D, bool SOLO>
 struct Ring {
-  float *inbox, *outbox;  // the state handed to this warp, and to the next one
+  float *inbox, *outbox;  // the state handed to this warp, and to the next one (its own, of one warp)
   int warp;
   __device__ explicit Ring(int w) : warp(w) {
     __shared__ __align__(16) float box[W][D];
     inbox = box[warp];
-    outbox = box[(warp + 1) % W];
+    outbox = box[SOLO ? warp : (warp + 1) % W];
   }
-  __device__ void wait() const { named_bar_sync(warp, 64); }
-  __device__ void pass() const { named_bar_arrive((warp + 1) % W, 64); }
+  __device__ void wait() const {
+    if (SOLO) __syncwarp();  // keeps what is before and after apart; without it registers spill
+    else named_bar_sync(warp, 64);
+  }
+  __device__ void pass() const {
+    if (SOLO) __syncwarp();
+    else named_bar_arrive((warp + 1) % W, 64);
+  }
 };
 
 // Rows of a partial tile that hold no token: closed gates (decay one) and zero writes.
@@ -346,20 +356,21 @@ __device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
 // every multiprocessor busy).  What else is busy: 65 % of the special-function unit, three results a
 // value.  Sharing one reciprocal between two values (289 us) is not worth its second path for
 // products that overflow; 12 warps take 305 us, a stage fewer 325 us.
-template <class T, int D>
+template <class T, int D, bool SOLO>
 __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     rec_forward_kernel(const __grid_constant__ RecParams p) {
   using B = Block<T, false>;
   using S = Shape<D>;
   using F = typename S::F;
   constexpr int K = S::K, V = S::V, P = V / 2, kStages = B::kStages, W = B::kWarps;
+  constexpr int kRing = SOLO ? 1 : W;
   constexpr int kStage = kStageBytes<T, D, false>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Entry entries[W][kStages];
   __shared__ float2 writes[W][K];  // b and b
   if (!same_plan(p)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
-  const Ring<W, D> ring(warp);
+  const Ring<W, D, SOLO> ring(warp);
   uint8_t* const stages = smem + warp * kStages * kStage;
   T* const out = static_cast<T*>(p.out);
   const long long orow = p.od.stride_s;
@@ -367,7 +378,7 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     T* const o = out + slot * p.od.stride_b + n * p.od.stride_n + chan;
     for (long long k = row + mine; k < end; k += warps) store(o + k * orow, splat<P>(0.f));
   };
-  Walk<T, D, false> walk;
+  Walk<T, D, false, SOLO> walk;
   walk.begin(p, warp, zero);
   auto issue = [&](int s) {
     return walk.issue(p, smem_u32(stages + s * kStage), &entries[warp][s], zero);
@@ -381,7 +392,7 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
   T* o = nullptr;
   float* state = nullptr;
   int slot = 0, n = 0, s = 0, fill = kStages - 1;
-  for (bool begun = warp > 0;; begun = true) {  // the ring's first tile has none before it
+  for (bool begun = SOLO || warp > 0;; begun = true) {  // a ring's first tile has none before it
     const int info = ahead[0].info, valid = info & kTokens;
     if (valid == 0) break;
     const float b = sigmoid(ahead[0].logit);
@@ -432,16 +443,16 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     const F before = h;
     h = fma(a[K - 1], h, u[K - 1]);
     store(ring.outbox + chan, h);
-    if (!(info & kStop)) ring.pass();
+    if (SOLO || !(info & kStop)) ring.pass();
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) u[k] = fma(a[k], before, u[k]);
     u[K - 1] = h;
     if (p.states) {
       store(state, before);
-      state += (size_t)W * p.N * D;
+      state += (size_t)kRing * p.N * D;
     }
     store_rows<T, D>(o, orow, valid, u);
-    o += W * K * orow;
+    o += kRing * K * orow;
     if ((info & (kLast | kEnd)) == (kLast | kEnd))
       store(p.end + ((size_t)slot * p.N + n) * D + chan, h);
     s = s + 1 == kStages ? 0 : s + 1;
@@ -471,13 +482,14 @@ __device__ __forceinline__ float warp_sums(float (&v)[K], int lane) {
 // 4x32x16384 bf16: 490 us, 5.75 TB/s (6.4 TB/s where 148 units keep every multiprocessor busy).  From
 // inputs in L2 it takes 466 us: 35 instructions a value, 57 % of the issue slots.  13 or 14 warps spill
 // registers (840-910 us); 11 warps with a stage more take 520 us.
-template <class T, int D>
+template <class T, int D, bool SOLO>
 __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
     rec_backward_kernel(const __grid_constant__ RecParams p) {
   using B = Block<T, true>;
   using S = Shape<D>;
   using F = typename S::F;
   constexpr int K = S::K, V = S::V, P = V / 2, kStages = B::kStages, W = B::kWarps;
+  constexpr int kRing = SOLO ? 1 : W;
   constexpr int kStage = kStageBytes<T, D, true>, kElems = kRecTileElems;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Entry entries[W][kStages];
@@ -485,7 +497,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   launch_dependents();
   if (!same_plan(p)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
-  const Ring<W, D> ring(warp);
+  const Ring<W, D, SOLO> ring(warp);
   uint8_t* const stages = smem + warp * kStages * kStage;  // a stage: g, x, dout, state
   const long long orow = p.od.stride_s;
   if (!p.dout.data) {
@@ -503,7 +515,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
       if (lane == 0) ob[k * p.bd.stride_s] = from_f32<T>(0.f);
     }
   };
-  Walk<T, D, true> walk;
+  Walk<T, D, true, SOLO> walk;
   walk.begin(p, warp, zero);
   auto issue = [&](int s) {
     return walk.issue(p, smem_u32(stages + s * kStage), &entries[warp][s], zero);
@@ -522,12 +534,12 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) raw += __shfl_xor_sync(0xffffffffu, raw, o);
     // a unit has up to kRecRing rows, more than the ring has warps: zeros in those left over
-    for (int i = 0; i < parts; i += W) {
+    for (int i = 0; i < parts; i += kRing) {
       store(p.part_bias + part * D + chan, sum_b);
       if (lane == 0) p.part_A[part] = raw;
       sum_b = sum_raw = splat<P>(0.f);
       raw = 0.f;
-      part += (size_t)W * p.N;
+      part += (size_t)kRing * p.N;
     }
   };
 
@@ -537,7 +549,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   T* dbeta = nullptr;     // of the lane's token
   constexpr int kEach = 32 / K;  // lanes that end with the same token's sum
   int slot = 0, n = 0, s = 0, fill = kStages - 1;
-  for (bool begun = warp > 0;; begun = true) {  // the ring's first tile has none before it
+  for (bool begun = SOLO || warp > 0;; begun = true) {  // a ring's first tile has none before it
     const int info = ahead[0].info, valid = info & kTokens;
     if (valid == 0) break;
     // b, and its slope b (1 - b) without cancellation: 1 - b is e b
@@ -606,7 +618,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
     const F behind = c;
     c = fma(a[0], c, c0);
     store(ring.outbox + chan, c);
-    if (!(info & kStop)) ring.pass();
+    if (SOLO || !(info & kStop)) ring.pass();
 #pragma unroll
     for (int k = 0; k < K - 1; ++k) lam[k] = fma(a[k + 1], behind, lam[k]);
     lam[K - 1] = lam[K - 1] + behind;
@@ -630,8 +642,8 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
     const int k = lane / kEach;
     const float total = warp_sums<K>(dot, lane) * __shfl_sync(0xffffffffu, slope_own, k);
     if (lane % kEach == 0 && k < valid) *dbeta = from_f32<T>(total);
-    o -= W * K * orow;
-    dbeta -= W * K * p.bd.stride_s;
+    o -= kRing * K * orow;
+    dbeta -= kRing * K * p.bd.stride_s;
     s = s + 1 == kStages ? 0 : s + 1;
   }
   if (part != kNone) flush();
@@ -869,7 +881,7 @@ struct Scratch {
 
 // Launches a pass: the maps where sequences are cut, and the walk, a block on every multiprocessor
 // that has a unit or rows to write zeros to.
-template <class T, int D, bool BACKWARD, class Kernel>
+template <class T, int D, bool BACKWARD, bool SOLO, class Kernel>
 cudaError_t launch(Kernel kernel, PerDevice& once, RecParams& p, const int32_t* plan,
                    cudaStream_t s) {
   using B = Block<T, BACKWARD>;
@@ -883,6 +895,7 @@ cudaError_t launch(Kernel kernel, PerDevice& once, RecParams& p, const int32_t* 
     return err == cudaSuccess ? cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, d) : err;
   });
   if (e != cudaSuccess) return e;
+  constexpr int kRing = SOLO ? 1 : B::kWarps;
   p.spread = p.slot_rows && p.units < sms;
   const int blocks = p.spread ? sms : std::min(sms, p.units);
   constexpr int K = Shape<D>::K, kCopy = 512 / (D * (int)sizeof(T));
@@ -890,7 +903,7 @@ cudaError_t launch(Kernel kernel, PerDevice& once, RecParams& p, const int32_t* 
   for (int i = 0; i < 4; ++i) {
     const long long row = views[i]->stride_s * (long long)sizeof(T);
     if (i < 3) p.copy_step[i] = kCopy * row;
-    p.tile_step[i] = (BACKWARD ? -B::kWarps : B::kWarps) * K * row;
+    p.tile_step[i] = (BACKWARD ? -kRing : kRing) * K * row;
   }
   if (plan[RH_MAPS]) {
     rec_maps_kernel<T, D, BACKWARD><<<(unsigned)p.units, 32 * kMapWarps, 0, s>>>(p);
@@ -903,14 +916,16 @@ cudaError_t launch(Kernel kernel, PerDevice& once, RecParams& p, const int32_t* 
 
 template <class T, int D>
 cudaError_t launch_forward(RecParams& p, const int32_t* plan, cudaStream_t s) {
-  static PerDevice once;
-  return launch<T, D, false>(rec_forward_kernel<T, D>, once, p, plan, s);
+  static PerDevice once[2];
+  return plan[RH_SOLO] ? launch<T, D, false, true>(rec_forward_kernel<T, D, true>, once[1], p, plan, s)
+                       : launch<T, D, false, false>(rec_forward_kernel<T, D, false>, once[0], p, plan, s);
 }
 
 template <class T, int D>
 cudaError_t launch_backward(RecParams& p, const int32_t* plan, cudaStream_t s) {
-  static PerDevice once;
-  return launch<T, D, true>(rec_backward_kernel<T, D>, once, p, plan, s);
+  static PerDevice once[2];
+  return plan[RH_SOLO] ? launch<T, D, true, true>(rec_backward_kernel<T, D, true>, once[1], p, plan, s)
+                       : launch<T, D, true, false>(rec_backward_kernel<T, D, false>, once[0], p, plan, s);
 }
 
 template <class F>

@@ -19,15 +19,16 @@ constexpr int kRecSpread = 148;  // multiprocessors that a plan spreads long seq
 
 // RH_TILES is the number of tiles in one head, RH_MAPS the rows of maps that the segments of cut
 // sequences need (0: none is cut), RH_PARTS the rows of the parameters' partial gradients,
-// RH_LONGEST the tiles of the longest segment, RH_PADDED whether rows lie behind a sequence's tokens.
+// RH_LONGEST the tiles of the longest segment, RH_PADDED whether rows lie behind a sequence's tokens,
+// RH_SOLO whether a segment is a single warp's.
 enum RecHeader : int {
   RH_MAGIC = 0, RH_VERSION, RH_HEADER_WORDS, RH_RECORD_WORDS, RH_LAYOUT, RH_B, RH_N, RH_S, RH_D,
-  RH_TILE_ROWS, RH_TILES, RH_RECORDS, RH_MAPS, RH_PARTS, RH_LONGEST, RH_PADDED, RH_TABLE_HASH,
+  RH_TILE_ROWS, RH_TILES, RH_RECORDS, RH_MAPS, RH_PARTS, RH_LONGEST, RH_PADDED, RH_TABLE_HASH, RH_SOLO,
   RH_CHECKSUM = kRecHeader - 1
 };
 // RR_SLOT is the sequence, RR_START the segment's first token within its slot (or in the packed
 // rows), RR_LEN its tokens, RR_TILE its first tile, RR_PART its first row of partial gradients (it
-// has one for each of its tiles, kRecRing at the most), RR_SEGMENT its place among the RR_SEGMENTS
+// has one for each of its tiles, kRecRing at the most, or a single one for a single warp), RR_SEGMENT its place among the RR_SEGMENTS
 // of its sequence and RR_MAP the sequence's first row of maps.
 enum RecRecord : int {
   RR_SLOT = 0, RR_START, RR_LEN, RR_TILE, RR_PART, RR_SEGMENT, RR_SEGMENTS, RR_MAP

@@ -127,6 +127,11 @@ kda_status_t build(const kda_recurrence_shape_t& s, const int32_t* cu, int32_t* 
   });
   std::stable_sort(segs.begin(), segs.end(),
                    [](const Segment& a, const Segment& d) { return a.len > d.len; });
+  // Many short segments: a warp each, if the longest one is no more than a warp's share of all tiles.
+  // Else a ring would pass by the units of kRecRing warps for each of its tiles.
+  long long all = 0;
+  for (const Segment& q : segs) all += tiles_of(q.len, R);
+  const bool solo = tiles_of(segs[0].len, R) * kRecSpread * kRecRing <= all * s.N;
   std::memset(plan, 0, kRecHeader * sizeof(int32_t));
   int32_t* rec = plan + kRecHeader;
   long long tile = 0, part = 0;
@@ -142,7 +147,7 @@ kda_status_t build(const kda_recurrence_shape_t& s, const int32_t* cu, int32_t* 
     rec[RR_MAP] = q.map;
     rec += kRecRecord;
     tile += tiles;
-    part += std::min<long long>(tiles, kRecRing);
+    part += std::min<long long>(tiles, solo ? 1 : kRecRing);
   }
   plan[RH_MAGIC] = kRecMagic;
   plan[RH_VERSION] = kRecVersion;
@@ -160,6 +165,7 @@ kda_status_t build(const kda_recurrence_shape_t& s, const int32_t* cu, int32_t* 
   plan[RH_PARTS] = (int32_t)part;
   plan[RH_LONGEST] = (int32_t)tiles_of(segs[0].len, R);
   plan[RH_PADDED] = padded;
+  plan[RH_SOLO] = solo;
   plan[RH_TABLE_HASH] = (int32_t)(fnv(plan + kRecHeader, segs.size() * kRecRecord) & 0x7fffffff);
   plan[RH_CHECKSUM] = (int32_t)(fnv(plan, RH_CHECKSUM) & 0x7fffffff);
   return KDA_OK;

@@ -586,3 +586,13 @@ def test_long_padding_behind_few_sequences(cuda_ok):
                 slot = t[b] if layout == "BSND" else t[b].transpose(0, 1)
                 assert torch.count_nonzero(slot[n:]) == 0
                 assert torch.isfinite(slot[:n]).all() and torch.count_nonzero(slot[:n]) > 0
+
+
+@pytest.mark.parametrize("layout,kind,D", [("TND", BF, 128), ("BNSD", HF, 64), ("BSND", FP, 128)])
+def test_more_sequences_than_warps(layout, kind, D, cuda_ok):
+    """So many short sequences that every warp walks its own, several one after another."""
+    lengths = [1 + (7 * i) % 40 for i in range(1300)]
+    d = make(layout, lengths, 4, D, kind, seed=32)
+    assert d["plan"].host[17] == 1
+    check_all(*run_both(d, -1.0, layout, lengths))
+    check_all(*run_both(d, -1.0, layout, lengths, h0=False, dout=False))

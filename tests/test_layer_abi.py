@@ -60,7 +60,7 @@ def test_recurrence_lengths(L, layout, B, S, cu, code):
 @pytest.mark.parametrize("N", [1, 3, 32])
 @pytest.mark.parametrize("layout,S,lengths", [
     (2, None, [1]), (2, None, [130, 1, 700, 64, 65, 63]), (1, 300, [300, 1, 128]), (0, 129, [129, 64]),
-    (0, 8192, [8192]), (2, None, [65536]), (1, 4000, [4000, 2777]), (2, None, [9000] + [3] * 400)])
+    (0, 8192, [8192]), (2, None, [65536]), (1, 4000, [4000, 2777]), (2, None, [9000] + [3] * 400), (2, None, [2, 3, 1] * 100), (1, 40, [39, 40] * 1300)])
 def test_plan_records(L, D, N, layout, S, lengths):
     """The segments, longest first, cover every sequence in order, in whole tiles but the last; their
     tiles, parts and maps lie side by side."""
@@ -72,10 +72,12 @@ def test_plan_records(L, D, N, layout, S, lengths):
     tiles = lambda n: -(-n // R)  # noqa: E731
     assert int(p[11]) == len(rec) and int(p[9]) == R
     assert [r[2] for r in rec] == sorted((r[2] for r in rec), reverse=True)
+    solo = tiles(max(lengths)) * 148 * 16 <= sum(map(tiles, lengths)) * N
+    assert int(p[17]) == solo
     tile = part = 0
     for r in rec:
         assert r[3:5] == [tile, part]
-        tile, part = tile + tiles(r[2]), part + min(16, tiles(r[2]))
+        tile, part = tile + tiles(r[2]), part + min(1 if solo else 16, tiles(r[2]))
     assert (int(p[10]), int(p[13]), int(p[14])) == (tile, part, tiles(rec[0][2]))
     maps = 0
     for b, n in enumerate(lengths):
@@ -114,7 +116,7 @@ def test_recurrence_plan_capacity_and_corruption(L):
         a.ctypes.data_as(P_I32), a.size if k is None else k, 0, ctypes.byref(n))
     assert ok(p) == 0 and n.value >= 256
     assert ok(p, p.size - 1) == PLAN and ok(p, 3) == PLAN
-    for word in (0, 4, 5, 10, 11, 12, 13, 14, 15, 16, 23):
+    for word in (0, 4, 5, 10, 11, 12, 13, 14, 15, 16, 17, 23):
         bad = p.copy()
         bad[word] += 1
         assert ok(bad) == PLAN, word
