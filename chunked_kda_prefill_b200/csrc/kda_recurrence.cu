@@ -741,37 +741,39 @@ __global__ void __launch_bounds__(32 * kMapWarps, 1) rec_maps_kernel(const __gri
   }
 }
 
-// ddt_bias and dA_log: the warps' parts in a fixed order, in fp64.  A block has 32 channels of a
-// head (the first one of a head its dA_log too); 32 threads a channel take the parts in turn.  About 4
-// us behind the walk, most of it the launch.
+// ddt_bias and dA_log: the warps' parts in a fixed order, in fp64.  A block has 8 channels of a head
+// (the first one of a head its dA_log too); 128 threads a channel take the parts in turn.  About 4 us
+// behind the walk, most of it the launch.
+constexpr int kParamChannels = 8;
 template <int D>
 __global__ void __launch_bounds__(1024) rec_params_kernel(const __grid_constant__ RecParams p,
                                                           int parts, float* dA_log,
                                                           float* ddt_bias) {
-  __shared__ double red[32][33];
-  constexpr int kBlocks = D / 32;
-  const int n = blockIdx.x / kBlocks, d0 = blockIdx.x % kBlocks * 32;
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  constexpr int kBlocks = D / kParamChannels, kRows = 1024 / kParamChannels;
+  __shared__ double red[kParamChannels + 1][kRows];
+  const int n = blockIdx.x / kBlocks, d0 = blockIdx.x % kBlocks * kParamChannels;
+  const int c = threadIdx.x % kParamChannels, row = threadIdx.x / kParamChannels;
   wait_dependencies();
   if (p.plan[RH_CHECKSUM] != p.checksum) return;
   double sum = 0, raw = 0;
 #pragma unroll 8
-  for (int i = row; i < parts; i += 32) {
+  for (int i = row; i < parts; i += kRows) {
     const size_t part = (size_t)i * p.N + n;
-    sum += p.part_bias[part * D + d0 + lane];
-    if (lane == 0) raw += p.part_A[part];
+    sum += p.part_bias[part * D + d0 + c];
+    if (d0 == 0 && c == 0) raw += p.part_A[part];
   }
-  red[row][lane] = sum;
+  red[c][row] = sum;
+  if (c == 0) red[kParamChannels][row] = raw;
   __syncthreads();
-  sum = warp_sum(red[lane][row]);
-  if (lane == 0) ddt_bias[(size_t)n * D + d0 + row] = (float)sum;
-  if (d0 != 0) return;
-  __syncthreads();
-  if (lane == 0) red[0][row] = raw;
-  __syncthreads();
-  if (row > 0) return;
-  raw = warp_sum(red[0][lane]);
-  if (lane == 0) dA_log[n] = (float)raw;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp > kParamChannels) return;
+  sum = 0;
+#pragma unroll
+  for (int i = lane; i < kRows; i += 32) sum += red[warp][i];
+  sum = warp_sum(sum);
+  if (lane > 0) return;
+  if (warp < kParamChannels) ddt_bias[(size_t)n * D + d0 + warp] = (float)sum;
+  else if (d0 == 0) dA_log[n] = (float)sum;
 }
 
 // One token of every sequence, 4 channels a thread.  Bound by HBM, 14 bytes a value (16-bit), and by
@@ -1055,7 +1057,7 @@ extern "C" kda_status_t kda_recurrence_backward(
     using T = std::remove_pointer_t<decltype(tag)>;
     const cudaError_t err = launch_backward<T, D>(p, plan_host, s);
     if (err != cudaSuccess) return err;
-    return launch_early(rec_params_kernel<D>, shape->N * (D / 32), 1024, 0,
+    return launch_early(rec_params_kernel<D>, shape->N * (D / kParamChannels), 1024, 0,
                         s, p, plan_host[RH_PARTS], dA_log, ddt_bias);
   });
   return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;

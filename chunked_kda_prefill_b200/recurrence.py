@@ -12,6 +12,10 @@ Per sequence, head n and channel d, with flash_kda's activations of the gate and
 ``gated_recurrence`` is differentiable with respect to x, g, beta, initial_state, A_log and
 dt_bias.  ``gated_recurrence_backward`` is its backward pass as a call of its own, and
 ``gated_recurrence_step`` one token for each sequence, from the state that a prefill returned.
+
+Every call can be captured in a CUDA graph; the plan is made before.  When a training step is
+captured, torch's rule holds: no eager autograd graph of the same leaves may be alive then, since
+their gradients would be accumulated on that graph's stream (``torch.autograd.grad`` does not).
 """
 from __future__ import annotations
 

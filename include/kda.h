@@ -322,7 +322,7 @@ KDA_API kda_status_t kda_recurrence_workspace_size(const int32_t* plan_host, siz
                                                    int32_t backward, size_t* bytes);
 
 /* fp32 values of the `states` buffer: the [N, D] states before every 1024 / D tokens of each
- * sequence, from its first one. */
+ * sequence, from its first one, in the plan's own order. */
 KDA_API kda_status_t kda_recurrence_states_size(const int32_t* plan_host, size_t n_int32,
                                                 size_t* n_floats);
 
