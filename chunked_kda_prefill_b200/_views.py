@@ -76,6 +76,14 @@ def launch_on(device: torch.device, stream):
     return _on(device, s), s.cuda_stream
 
 
+def used_on(stream, *tensors) -> None:
+    """Memory of tensors that a call on a stream of the caller's choice uses is not handed out again
+    before that stream has come past the call."""
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
 def needs_grad(*tensors) -> bool:
     for t in tensors:
         if t is not None and t.requires_grad:

@@ -18,8 +18,8 @@ import torch
 
 from . import _lib
 from ._lib import KdaError, KdaQkShape, check
-from ._views import (dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, view,
-                     viewable)
+from ._views import (dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, used_on,
+                     view, viewable)
 from .api import LAYOUTS, _ptr
 
 
@@ -72,6 +72,8 @@ def _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interle
     if k_out is not None:
         expect_dense(k_out, "k_out", q.dtype, dev, k.shape)
     ctx, handle = launch_on(dev, stream)
+    if stream is not None:
+        used_on(stream, q, k, positions, inv_freq, q_weight, k_weight, q_out, k_out)
     with ctx:
         if q_out is None:
             q_out = dense_like(q)
@@ -109,6 +111,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k
               "kda_qk_norm_rope_workspace_size")
         ws_bytes = _workspace_bytes[shape.D] = size.value
     ctx, handle = launch_on(dev, stream)
+    if stream is not None:
+        used_on(stream, dq_out, dk_out, q, k, positions, inv_freq, q_weight, k_weight, dq, dk)
     with ctx:
         if dq is None:
             dq = dense_like(q)
@@ -158,7 +162,8 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps: float, layo
     may be q and k themselves where those are dense.
 
     Differentiable when q, k or a weight requires a gradient; then q_out, k_out and stream cannot
-    be given (choose the stream with torch.cuda.stream).
+    be given (choose the stream with torch.cuda.stream).  A call on a given stream does not wait for
+    the streams that made its inputs.
     """
     if inv_freq is not None and needs_grad(inv_freq):
         raise ValueError("inv_freq has no gradient here")

@@ -27,8 +27,8 @@ import torch
 
 from . import _lib
 from ._lib import KdaError, KdaRecurrenceShape, check
-from ._views import (DTYPES, dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, view,
-                     viewable)
+from ._views import (DTYPES, dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, used_on,
+                     view, viewable)
 from .api import LAYOUTS, _ptr
 
 _F32 = torch.float32
@@ -179,6 +179,9 @@ def _forward(x, g, beta, initial_state, A_log, dt_bias, lower_bound, layout, pla
     if final_state is not None:
         expect_dense(final_state, "final_state", torch.float32, dev, plan._state)
     ctx, handle = launch_on(dev, stream)
+    if stream is not None:
+        used_on(stream, x, g, beta, initial_state, A_log, dt_bias, plan.dev, out, final_state,
+                workspace)
     with ctx:
         if out is None:
             out = dense_like(x)
@@ -218,6 +221,8 @@ def gated_recurrence_backward(dout, dfinal_state, x, g, beta, initial_state, A_l
         expect_dense(dfinal_state, "dfinal_state", torch.float32, dev, plan._state)
     expect_dense(states, "states", torch.float32, dev, plan.states_shape)
     ctx, handle = launch_on(dev, stream)
+    if stream is not None:
+        used_on(stream, dout, dfinal_state, x, g, beta, A_log, dt_bias, states, plan.dev, workspace)
     with ctx:
         dx, dg, dbeta = dense_like(x), dense_like(x), dense_like(beta)
         dh0 = torch.empty_like(initial_state) if initial_state is not None else None
@@ -275,7 +280,8 @@ def gated_recurrence(x, g, beta, initial_state, A_log, dt_bias, lower_bound: flo
     type; rows past a valid length are zeros.  final_state: fp32 [B, N, D].
 
     Differentiable when an input requires a gradient; then out, final_state, return_states,
-    workspace and stream cannot be given (choose the stream with torch.cuda.stream).
+    workspace and stream cannot be given (choose the stream with torch.cuda.stream).  A call on a
+    given stream does not wait for the streams that made its inputs.
     ``return_states=True`` adds the states that gated_recurrence_backward needs.  ``workspace``
     (plan.workspace_bytes) keeps the call's device status for device_status; by default every call
     has a scratch of its own.
@@ -329,6 +335,8 @@ def gated_recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound: float,
     if state_out is not None:
         expect_dense(state_out, "state_out", torch.float32, dev, shape)
     ctx, handle = launch_on(dev, stream)
+    if stream is not None:
+        used_on(stream, x, g, beta, state, A_log, dt_bias, out, state_out)
     with ctx:
         if out is None:
             out = torch.empty_like(x)

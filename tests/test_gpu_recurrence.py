@@ -596,3 +596,29 @@ def test_more_sequences_than_warps(layout, kind, D, cuda_ok):
     assert d["plan"].host[17] == 1
     check_all(*run_both(d, -1.0, layout, lengths))
     check_all(*run_both(d, -1.0, layout, lengths, h0=False, dout=False))
+
+
+def test_inputs_may_go_while_another_stream_uses_them(cuda_ok):
+    """Inputs and the plan are dropped right after a call on another stream, and their memory is asked
+    for again; a long wait on that stream comes first."""
+    lengths = [600, 30]
+    d = make("TND", lengths, 2, 64, BF, seed=33)
+    want = kda.gated_recurrence(*args(d, -1.0, "TND"))
+    q = d["x"].contiguous()
+    inv = torch.ones(32, device="cuda")
+    turned = kda.qk_norm_rope(q, q.clone(), None, inv, None, None, 1e-6, "TND")
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        torch.cuda._sleep(50_000_000)
+    mine = {n: t.clone() for n, t in d.items() if n != "plan"}
+    mine["plan"] = kda.recurrence_plan(mine["x"], "TND", cu_seqlens=[0, 600, 630])
+    k, f = q.clone(), inv.clone()
+    torch.cuda.current_stream().synchronize()
+    got = kda.gated_recurrence(*args(mine, -1.0, "TND"), stream=other)
+    rot = kda.qk_norm_rope(mine["x"], k, None, f, None, None, 1e-6, "TND", stream=other)
+    sizes = [t.numel() for t in mine.values() if isinstance(t, torch.Tensor)] + [k.numel()]
+    del mine, k, f
+    junk = [torch.full((n,), float("nan"), dtype=t, device="cuda") for n in sizes for t in (BF, FP)]
+    torch.cuda.synchronize()
+    assert junk and all(torch.equal(a, b) for a, b in zip(got + rot, want + turned))
