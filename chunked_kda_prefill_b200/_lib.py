@@ -119,3 +119,28 @@ def load():
 def check(code: int, where: str) -> None:
     if code != 0:
         raise KdaError(code, where)
+
+
+_calls = False  # not looked for yet
+
+
+def calls():
+    """The compiled calls (binding/calls.cpp) on the loaded library, or None where they were not built
+    for this torch."""
+    global _calls
+    if _calls is False:
+        L = load()
+        try:
+            import torch
+
+            from . import _calls as m
+            if m.torch_version != torch.__version__:
+                raise ImportError("compiled against another torch")
+            m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                L.kda_recurrence_forward, L.kda_recurrence_backward, L.kda_recurrence_step,
+                L.kda_qk_norm_rope, L.kda_qk_norm_rope_workspace_size,
+                L.kda_qk_norm_rope_backward)))
+            _calls = m
+        except ImportError:
+            _calls = None
+    return _calls

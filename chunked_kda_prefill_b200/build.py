@@ -4,7 +4,10 @@
 
 Compiles every ``csrc/*.cu`` and ``csrc/*.cpp`` to objects under ``_build/`` (in parallel)
 and links ``chunked_kda_prefill_b200/libkda.so`` with the CUDA runtime linked statically, so
-the library loads on a machine without a GPU (its host entry points work there).
+the library loads on a machine without a GPU (its host entry points work there).  With g++ it also
+compiles ``binding/calls.cpp`` against this interpreter and its torch into ``_calls.so``, the calls of
+the operators around the prefill in their common form; without that file (or under another torch)
+they take the same way through ctypes, at two to three times the host time.
 
 ``--define`` builds a variant instead (for example ``KDA_STATE_LO=0``, the state operand without
 its bf16 remainder, or ``KDA_PHASE_TIMING=1``, per-phase clock stamps for
@@ -23,6 +26,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
+CALLS = os.path.join(PKG, "_calls.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -63,6 +67,38 @@ def _compile(src, verbose, build_dir=BUILD, defines=()):
     return obj
 
 
+def build_calls(force: bool = False) -> str:
+    """``_calls.so``, or a RuntimeError that says why it could not be compiled."""
+    import sysconfig
+
+    import torch
+
+    src = os.path.join(PKG, "binding", "calls.cpp")
+    stamp = os.path.join(BUILD, "calls.torch")  # the torch that _calls.so was compiled against
+    header = os.path.join(PKG, "..", "include", "kda.h")
+    fresh = (os.path.exists(stamp) and open(stamp).read() == torch.__version__
+             and not _stale(CALLS, [src, header]))
+    if fresh and not force:
+        return CALLS
+    home = os.path.dirname(torch.__file__)
+    lib, include = os.path.join(home, "lib"), os.path.join(home, "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = ([os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared",
+            "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DKDA_TORCH_VERSION="{torch.__version__}"', "-I", sysconfig.get_paths()["include"]]
+           + ["-I", include, "-I", os.path.join(include, "torch", "csrc", "api", "include"), "-I",
+              cuda, src, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-o", tmp])
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
+    return CALLS
+
+
 def variant_tag(defines) -> str:
     return "_".join(d.replace("=", "").lower() for d in sorted(defines))
 
@@ -87,6 +123,11 @@ def build(force: bool = False, verbose: bool = False, defines=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
+    if not defines:
+        try:
+            build_calls(force)
+        except (RuntimeError, OSError, ImportError) as e:
+            print(f"without {os.path.basename(CALLS)}: {e}", file=sys.stderr)
     return lib
 
 

@@ -96,6 +96,12 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k
     (dq_out and dk_out themselves where those are dense).  A weight's gradient is None when the
     weight is.
     """
+    calls = _lib.calls()
+    if dq is None and dk is None and stream is None and calls is not None:
+        res = calls.qk_backward(q, k, positions, inv_freq, q_weight, k_weight, eps, layout,
+                                interleaved, dq_out, dk_out)
+        if res is not None:
+            return res if res.__class__ is tuple else check(res, "kda_qk_norm_rope_backward")
     shape = _check(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved)
     dev = q.device
     expect(dq_out, "dq_out", q.dtype, dev, q.shape)
@@ -135,8 +141,8 @@ class _QkNormRope(torch.autograd.Function):
     def forward(ctx, q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved):
         ctx.save_for_backward(q, k, positions, inv_freq, q_weight, k_weight)
         ctx.call = eps, layout, interleaved
-        return _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved,
-                        None, None, None)
+        # no gradient is wanted in here, so this takes the short way
+        return qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -165,6 +171,11 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps: float, layo
     be given (choose the stream with torch.cuda.stream).  A call on a given stream does not wait for
     the streams that made its inputs.
     """
+    calls = _lib.calls()
+    if q_out is None and k_out is None and stream is None and calls is not None:
+        res = calls.qk_forward(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved)
+        if res is not None:
+            return res if res.__class__ is tuple else check(res, "kda_qk_norm_rope")
     if inv_freq is not None and needs_grad(inv_freq):
         raise ValueError("inv_freq has no gradient here")
     if needs_grad(q, k, q_weight, k_weight):

@@ -58,6 +58,10 @@ class KdaRecurrencePlan:
         self._heads = torch.Size((sh.N,))
         self._params = torch.Size((sh.N, sh.D))
         self._index = self.dev.get_device()
+        calls = _lib.calls()
+        self._handle = calls and calls.plan(
+            sh.layout, sh.B, sh.N, sh.S, sh.D, self.host.ctypes.data, self.host.size, self.host,
+            self.dev, self.workspace_bytes, self.backward_workspace_bytes, self.states_shape[0])
         self._shapes = {}
 
     def _shape_for(self, dtype: int) -> KdaRecurrenceShape:
@@ -213,6 +217,11 @@ def gated_recurrence_backward(dout, dfinal_state, x, g, beta, initial_state, A_l
     ``gated_recurrence(..., return_states=True)`` returned for the same inputs and plan.
     dinitial_state is None when initial_state is.
     """
+    if workspace is None and stream is None and plan._handle is not None:
+        res = _lib.calls().recurrence_backward(plan._handle, layout, x, g, beta, initial_state, A_log,
+                                               dt_bias, lower_bound, states, dout, dfinal_state)
+        if res is not None:
+            return res if res.__class__ is tuple else check(res, "kda_recurrence_backward")
     dev = x.device
     code = _check(plan, layout, dev, x, g, beta, initial_state, A_log, dt_bias)
     if dout is not None:
@@ -245,8 +254,9 @@ def gated_recurrence_backward(dout, dfinal_state, x, g, beta, initial_state, A_l
 class _GatedRecurrence(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, g, beta, initial_state, A_log, dt_bias, lower_bound, layout, plan):
-        out, final_state, states = _forward(x, g, beta, initial_state, A_log, dt_bias, lower_bound,
-                                            layout, plan, None, None, True, None, None)
+        # no gradient is wanted in here, so this takes the short way
+        out, final_state, states = gated_recurrence(x, g, beta, initial_state, A_log, dt_bias,
+                                                    lower_bound, layout, plan, return_states=True)
         ctx.save_for_backward(x, g, beta, initial_state, A_log, dt_bias, states)
         ctx.call = lower_bound, layout, plan
         ctx.set_materialize_grads(False)
@@ -286,6 +296,12 @@ def gated_recurrence(x, g, beta, initial_state, A_log, dt_bias, lower_bound: flo
     (plan.workspace_bytes) keeps the call's device status for device_status; by default every call
     has a scratch of its own.
     """
+    if (out is None and final_state is None and workspace is None and stream is None
+            and plan._handle is not None):
+        res = _lib.calls().recurrence_forward(plan._handle, layout, x, g, beta, initial_state, A_log,
+                                              dt_bias, lower_bound, return_states)
+        if res is not None:
+            return res if res.__class__ is tuple else check(res, "kda_recurrence_forward")
     if needs_grad(x, g, beta, initial_state, A_log, dt_bias):
         if (out is not None or final_state is not None or return_states or workspace is not None
                 or stream is not None):
@@ -306,6 +322,11 @@ def gated_recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound: float,
     x, g: [B, N, D] in bf16, fp16 or fp32, beta: [B, N], all dense; state: fp32 [B, N, D] or None
     (zeros); pass ``state_out=state`` to update it in place.  Not differentiable.
     """
+    calls = _lib.calls()
+    if stream is None and calls is not None:
+        res = calls.recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound, out, state_out)
+        if res is not None:
+            return res if res.__class__ is tuple else check(res, "kda_recurrence_step")
     dev = x.device
     if dev.type != "cuda":
         raise ValueError("gated_recurrence_step runs on a CUDA device only")
