@@ -33,8 +33,6 @@ constexpr int kThreads = 256;
 // Multiprocessors that the grids are made for.  In the backward pass each block leaves one partial sum
 // of the weights' gradients.
 constexpr int kSpread = 148;
-// Blocks wanted before heads stop being split over blocks (about two for each SM).
-constexpr int kWantBlocks = 296;
 
 struct QkSide {
   kda_view_t x, dy;  // dy: backward only
@@ -356,23 +354,30 @@ __global__ void __launch_bounds__(kThreads, kResident)
   }
 }
 
-// The blocks' partial sums in a fixed order, in fp64: 32 threads for a channel, then those 32.
+// The blocks' partial sums in a fixed order, in fp64: 128 threads for a channel, then a warp.
+constexpr int kSumChannels = 8;
 template <int D>
 __global__ void __launch_bounds__(1024) qk_weights_kernel(const float* part, int blocks, float* dwq,
                                                           float* dwk) {
-  __shared__ double red[32][33];
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, side = blockIdx.y;
+  constexpr int kRows = 1024 / kSumChannels;
+  __shared__ double red[kSumChannels][kRows];
+  const int c = threadIdx.x % kSumChannels, row = threadIdx.x / kSumChannels, side = blockIdx.y;
   float* const dw = side ? dwk : dwq;
   if (!dw) return;
   wait_dependencies();
   double sum = 0;
-#pragma unroll 8
-  for (int i = row; i < blocks; i += 32)
-    sum += part[((size_t)i * 2 + side) * D + blockIdx.x * 32 + lane];
-  red[row][lane] = sum;
+#pragma unroll 4
+  for (int i = row; i < blocks; i += kRows)
+    sum += part[((size_t)i * 2 + side) * D + blockIdx.x * kSumChannels + c];
+  red[c][row] = sum;
   __syncthreads();
-  sum = warp_sum(red[lane][row]);
-  if (lane == 0) dw[blockIdx.x * 32 + row] = (float)sum;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp >= kSumChannels) return;
+  sum = 0;
+#pragma unroll
+  for (int i = lane; i < kRows; i += 32) sum += red[warp][i];
+  sum = warp_sum(sum);
+  if (lane == 0) dw[blockIdx.x * kSumChannels + warp] = (float)sum;
 }
 
 kda_status_t validate(const kda_qk_shape_t* s) {
@@ -443,13 +448,6 @@ bool same_tensor(const kda_view_t& v, const QkSide& a, int nb, int S) {
          (a.heads <= 1 || v.stride_n == a.od.stride_n) && (S <= 1 || v.stride_s == a.od.stride_s);
 }
 
-// Heads of one block: all of a token's, unless that leaves SMs without a block.
-int heads_per_block(const QkParams& p, long long token_blocks) {
-  const int heads = p.side[0].heads + p.side[1].heads;
-  const long long split = std::min<long long>(heads, (kWantBlocks + token_blocks - 1) / token_blocks);
-  return (int)((heads + split - 1) / split);
-}
-
 template <template <class, int, bool> class K, class... A>
 void dispatch(const kda_qk_shape_t& s, A&&... a) {
   auto with_type = [&](auto* tag) {
@@ -485,13 +483,25 @@ using Forward = Pass<T, D, INTER, false>;
 template <class T, int D, bool INTER>
 using Backward = Pass<T, D, INTER, true>;
 
-// The grid: blocks over tokens and, where those are few, over the heads of a token.
+// The grid: blocks over tokens and, where that takes less time, over the heads of a token.  A block's
+// turn over its groups' tokens costs its steps over the heads and about four more to begin with
+// (positions, angles, the first copies).
 dim3 grid_of(const kda_qk_shape_t& s, int most, QkParams* p) {
-  const int groups = kThreads / (s.D / 8), heads = s.Nq + s.Nk;
-  const long long want = std::min<long long>((p->tokens + groups - 1) / groups, most);
-  p->heads_per = heads_per_block(*p, want);
-  const int splits = (heads + p->heads_per - 1) / p->heads_per;
-  return dim3((unsigned)std::min<long long>(want, std::max(1, most / splits)), (unsigned)splits);
+  const int groups = kThreads / (s.D / 8), heads = s.Nq + s.Nk, rows = s.dtype == KDA_FP32 ? 1 : 2;
+  const long long blocks = (p->tokens + groups - 1) / groups;
+  long long least = LLONG_MAX;
+  dim3 grid;
+  for (int want = 1; want <= std::min(heads, most); ++want) {
+    const int per = (heads + want - 1) / want, splits = (heads + per - 1) / per;
+    const long long across = std::min<long long>(blocks, most / splits);
+    const long long cost = (blocks + across - 1) / across * (4 + (per + rows - 1) / rows);
+    if (cost < least) {
+      least = cost;
+      grid = dim3((unsigned)across, (unsigned)splits);
+      p->heads_per = per;
+    }
+  }
+  return grid;
 }
 
 }  // namespace
@@ -582,7 +592,7 @@ extern "C" kda_status_t kda_qk_norm_rope_backward(
   if (err != cudaSuccess) return KDA_ERR_CUDA;
   if (dq_weight || dk_weight)
     err = launch_early(shape->D == 128 ? qk_weights_kernel<128> : qk_weights_kernel<64>,
-                       dim3(shape->D / 32, 2), 1024, 0, stm, p.part, (int)(grid.x * grid.y),
+                       dim3(shape->D / kSumChannels, 2), 1024, 0, stm, p.part, (int)(grid.x * grid.y),
                        dq_weight, dk_weight);
   return err == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
