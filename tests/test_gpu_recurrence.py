@@ -622,3 +622,91 @@ def test_inputs_may_go_while_another_stream_uses_them(cuda_ok):
     junk = [torch.full((n,), float("nan"), dtype=t, device="cuda") for n in sizes for t in (BF, FP)]
     torch.cuda.synchronize()
     assert junk and all(torch.equal(a, b) for a, b in zip(got + rot, want + turned))
+
+
+def test_compiled_and_python_calls_agree(cuda_ok, monkeypatch):
+    """The compiled calls are there, and give what the Python functions give by way of ctypes: results,
+    their shapes and types, statuses and refusals."""
+    from chunked_kda_prefill_b200 import _lib
+    assert _lib.calls() is not None
+    for layout, lengths, kind, lb in (("BNSD", [200, 3], BF, -5), ("BSND", [70, 90], HF, -1.0),
+                                      ("TND", [3000, 5], FP, -0.5)):
+        d = make(layout, lengths, 2, 64, kind, S=None if layout == "TND" else 210, seed=34)
+        one = [d[n].movedim(2, 1)[:, 0] if layout == "BNSD" else d[n][:, 0] if layout == "BSND" else
+               d[n][:2] for n in ("x", "g", "beta")]
+        one = [t.contiguous() for t in one]
+        inv = torch.rand(16, device="cuda")
+        w = torch.rand(64, device="cuda")
+
+        def everything():
+            res = []
+            for h0 in (True, False):
+                a = args(d, lb, layout, h0)
+                out, final, states = kda.gated_recurrence(*a, return_states=True)
+                res += [*kda.gated_recurrence(*a), out, final]
+                for dout in (d["dout"], None):
+                    for dfinal in (d["dfinal"], None):
+                        res += kda.gated_recurrence_backward(dout, dfinal, *a, states)
+                state = d["h0"].clone()
+                res += kda.gated_recurrence_step(*one, state if h0 else None, d["A_log"],
+                                                 d["dt_bias"], lb)
+                res += kda.gated_recurrence_step(*one, state, d["A_log"], d["dt_bias"], lb,
+                                                 state_out=state)
+                assert res[-1] is state
+            for pos, f, qw in ((None, inv, None), (None, None, w)):
+                c = (d["x"], d["g"], pos, f, qw, w, 1e-6, layout)
+                res += kda.qk_norm_rope(*c, interleaved=True)
+                res += kda.qk_norm_rope_backward(d["dout"], d["x"], *c, interleaved=True)
+            bad = list(args(d, lb, layout))
+            for i, v in ((6, -7.0), (2, d["beta"][:1]), (4, d["A_log"].double()), (7, "NBD")):
+                with pytest.raises((TypeError, ValueError, kda.KdaError)) as e:
+                    kda.gated_recurrence(*bad[:i], v, *bad[i + 1:])
+                res.append(str(e.value))
+            with pytest.raises(kda.KdaError) as e:
+                kda.qk_norm_rope(d["x"], d["x"], None, None, None, None, -1.0, layout)
+            return res + [str(e.value)]
+
+        fast = everything()
+        with monkeypatch.context() as m:
+            m.setattr(_lib, "_calls", None)
+            m.setattr(d["plan"], "_handle", None)
+            slow = everything()
+        assert len(fast) == len(slow)
+        for a, b in zip(fast, slow):
+            if isinstance(a, torch.Tensor):
+                assert a.dtype == b.dtype and a.is_contiguous() and a.shape == b.shape
+                assert torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0))
+            else:
+                assert a == b
+
+
+def test_compiled_calls_follow_stream_grad_mode_and_capture(cuda_ok):
+    """The current stream is the one that results are made on; inputs that want a gradient, and results
+    under no_grad and inference mode, are told apart."""
+    lengths = [500]
+    d = make("TND", lengths, 2, 64, BF, seed=35)
+    want, _ = kda.gated_recurrence(*args(d, -1.0, "TND"))
+    out = None
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        # the stream's own memory first: asking the device for some may wait for all of its work
+        for _ in range(2):
+            del out
+            out, _ = kda.gated_recurrence(*args(d, -1.0, "TND"))
+        s.synchronize()
+        torch.cuda._sleep(20_000_000)
+        del out
+        out, _ = kda.gated_recurrence(*args(d, -1.0, "TND"))
+        done = torch.cuda.Event()
+        done.record()
+    assert not done.query()
+    s.synchronize()
+    assert torch.equal(out, want)
+    ts = leaves(d)
+    assert kda.gated_recurrence(*ts, -1.0, "TND", d["plan"])[0].grad_fn is not None
+    with torch.no_grad():
+        assert not kda.gated_recurrence(*ts, -1.0, "TND", d["plan"])[0].requires_grad
+    with torch.inference_mode():
+        out, _ = kda.gated_recurrence(*ts, -1.0, "TND", d["plan"])
+        assert torch.equal(out, want) and out.is_inference()

@@ -306,3 +306,31 @@ def test_views_of_tensors():
     assert not _views.viewable(torch.ones((), dtype=torch.bfloat16).expand(2, 64))
     odd = torch.zeros(4, 68, dtype=torch.bfloat16)
     assert not _views.viewable(odd[:, :64]) and _views.viewable(odd[:1, :64])
+
+
+def test_compiled_calls_leave_to_python_what_does_not_fit():
+    """The compiled calls are built here, answer None to what is not theirs to take, and never raise
+    or run for it."""
+    import torch
+
+    import chunked_kda_prefill_b200 as kda
+    from chunked_kda_prefill_b200 import _lib
+    m = _lib.calls()
+    assert m is not None and m.torch_version == torch.__version__
+    x = torch.zeros(4, 2, 64)
+    beta, A, bias, state = x[..., 0].contiguous(), torch.zeros(2), torch.zeros(2, 64), x[:1]
+    plan = kda.recurrence_plan(x, "TND", cu_seqlens=[0, 4])
+    rec = [plan._handle, "TND", x, x, beta, state, A, bias, -1.0]
+    assert m.recurrence_forward(*rec, False) is None                    # not on a CUDA device
+    assert m.recurrence_backward(*rec, x, None, None) is None
+    assert m.recurrence_step(x, x, beta, None, A, bias, -1.0, None, None) is None
+    assert m.qk_forward(x, x, None, None, None, None, 1e-6, "TND", False) is None
+    assert m.qk_backward(x, x, None, None, None, None, 1e-6, "TND", False, x, x) is None
+    for call, n in ((m.recurrence_forward, 10), (m.recurrence_backward, 12), (m.recurrence_step, 9),
+                    (m.qk_forward, 9), (m.qk_backward, 11)):
+        assert call(*[None] * n) is None and call(*["TND"] * n) is None and call() is None
+    for bad in ((), (1, 2), (0,) * 6, ("a",) * 6):
+        with pytest.raises((TypeError, ValueError)):
+            m.bind(*bad)
+    with pytest.raises(TypeError):
+        m.plan(*range(12))
