@@ -283,7 +283,7 @@ __device__ __noinline__ Pairs<D / 64> join(const RecParams& p, int map, int orde
   wait_dependencies();
   const float* m = p.maps + ((size_t)map * p.N + n) * 2 * D + chan;
   const size_t row = (size_t)p.N * 2 * D;
-  constexpr int kAhead = 8;  // loads under way at a time
+  constexpr int kAhead = 16;  // loads under way at a time
   for (int k = 0; k <= order; k += kAhead) {
     F a[kAhead], h[kAhead];
 #pragma unroll
@@ -660,7 +660,7 @@ template <class T, int D, bool BACKWARD>
 __global__ void __launch_bounds__(32 * kMapWarps, 1) rec_maps_kernel(const __grid_constant__ RecParams p) {
   using S = Shape<D>;
   using F = typename S::F;
-  constexpr int V = S::V, P = V / 2, kBatch = 16 / (int)sizeof(T);
+  constexpr int V = S::V, P = V / 2, kBatch = 8 / (int)sizeof(T);
   __shared__ __align__(16) float sa[kMapWarps][D], sh[kMapWarps][D];
   launch_dependents();
   if (p.plan[RH_CHECKSUM] != p.checksum) return;
