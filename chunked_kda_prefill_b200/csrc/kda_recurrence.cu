@@ -139,6 +139,16 @@ struct Walk {
   int place, places;                  // the warp's, or its block's, among those that units go to
   bool fresh, done;
   const char *g, *x, *dout, *beta, *state;  // the lane's, of the next tile
+  int4 r0, r1;
+
+  // The first record is on its way while the plan is checked.
+  __device__ Walk(const RecParams& p) {
+    const int warp = threadIdx.x >> 5;
+    places = SOLO ? gridDim.x * W : gridDim.x;
+    place = SOLO ? blockIdx.x + warp * gridDim.x : blockIdx.x;
+    round = 0;
+    fetch(p);
+  }
 
   __device__ long long unit_of(int round) const {
     return (long long)round * places + (round & 1 ? places - 1 - place : place);
@@ -149,17 +159,24 @@ struct Walk {
     return reinterpret_cast<const char*>(at<T>(v, slot, n, row + lane / kLanes)) +
            lane % kLanes * 16;
   }
+  // The record of the round's unit.
+  __device__ void fetch(const RecParams& p) {
+    const long long unit = unit_of(round);
+    done = unit >= p.units;
+    if (done) return;
+    const int i = (int)unit / p.N;
+    n = (int)unit - i * p.N;
+    r0 = __ldg(record(p, i));
+    r1 = __ldg(record(p, i) + 1);
+  }
   // zero(slot, n, row, end, warps, warp): writes the rows behind a sequence's last token, a share of them
-  template <class Zero>
+  template <bool FIRST = false, class Zero>
   __device__ void enter(const RecParams& p, Zero&& zero) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (;; ++round) {
-      const long long unit = unit_of(round);
-      done = unit >= p.units;
+    for (bool fetched = FIRST;; ++round) {
+      if (!fetched) fetch(p);
+      fetched = false;
       if (done) return;
-      const int i = (int)unit / p.N;
-      n = (int)unit - i * p.N;
-      const int4 r0 = __ldg(record(p, i)), r1 = __ldg(record(p, i) + 1);
       slot = r0.x; start = r0.y; len = r0.z; tile0 = r0.w;
       part = r1.x; segment = r1.y; segments = r1.z; map = r1.w;
       tiles = (len + K - 1) / K;
@@ -202,11 +219,8 @@ struct Walk {
   __device__ void begin(const RecParams& p, int warp, Zero&& zero) {
     dout = state = nullptr;
     if (p.spread) zero_all(p, zero);
-    places = SOLO ? gridDim.x * W : gridDim.x;
-    place = SOLO ? blockIdx.x + warp * gridDim.x : blockIdx.x;
-    round = 0;
     t = SOLO ? 0 : warp;
-    enter(p, zero);
+    enter<true>(p, zero);
   }
   template <class Zero>
   __device__ void next(const RecParams& p, Zero&& zero) {
@@ -368,6 +382,7 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Entry entries[W][kStages];
   __shared__ float2 writes[W][K];  // b and b
+  Walk<T, D, false, SOLO> walk(p);
   if (!same_plan(p)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
   const Ring<W, D, SOLO> ring(warp);
@@ -378,7 +393,6 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     T* const o = out + slot * p.od.stride_b + n * p.od.stride_n + chan;
     for (long long k = row + mine; k < end; k += warps) store(o + k * orow, splat<P>(0.f));
   };
-  Walk<T, D, false, SOLO> walk;
   walk.begin(p, warp, zero);
   auto issue = [&](int s) {
     return walk.issue(p, smem_u32(stages + s * kStage), &entries[warp][s], zero);
@@ -495,6 +509,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   __shared__ Entry entries[W][kStages];
   __shared__ float2 writes[W][K];  // b and b
   launch_dependents();
+  Walk<T, D, true, SOLO> walk(p);
   if (!same_plan(p)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
   const Ring<W, D, SOLO> ring(warp);
@@ -515,7 +530,6 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
       if (lane == 0) ob[k * p.bd.stride_s] = from_f32<T>(0.f);
     }
   };
-  Walk<T, D, true, SOLO> walk;
   walk.begin(p, warp, zero);
   auto issue = [&](int s) {
     return walk.issue(p, smem_u32(stages + s * kStage), &entries[warp][s], zero);
@@ -663,9 +677,9 @@ __global__ void __launch_bounds__(32 * kMapWarps, 1) rec_maps_kernel(const __gri
   constexpr int V = S::V, P = V / 2, kBatch = 8 / (int)sizeof(T);
   __shared__ __align__(16) float sa[kMapWarps][D], sh[kMapWarps][D];
   launch_dependents();
-  if (p.plan[RH_CHECKSUM] != p.checksum) return;
   const int i = blockIdx.x / p.N, n = blockIdx.x - i * p.N;
   const int4 r0 = __ldg(record(p, i)), r1 = __ldg(record(p, i) + 1);
+  if (p.plan[RH_CHECKSUM] != p.checksum) return;
   const int order = BACKWARD ? r1.z - 1 - r1.y : r1.y;
   if (order + 1 == r1.z) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, chan = lane * V;
