@@ -260,7 +260,8 @@ PyObject* recurrence_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       wants_grad({in.x, in.g, in.beta, in.h0, in.A, in.bias}))
     Py_RETURN_NONE;
   const Plan& p = *in.p;
-  const bool keep = a[9] == Py_True;
+  const int keep = PyObject_IsTrue(a[9]);
+  if (keep < 0) return nullptr;
   const Tensor out = like(*in.x), final = fresh(p.state, *in.x, ScalarType::Float);
   Tensor states, work;
   if (keep) states = fresh(p.states, *in.x, ScalarType::Float);

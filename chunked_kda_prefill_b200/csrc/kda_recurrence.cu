@@ -210,15 +210,31 @@ struct Walk {
       for (unsigned left = __ballot_sync(0xffffffffu, row < p.slot_rows); left; left &= left - 1) {
         const int from = __ffs(left) - 1;
         const int s = __shfl_sync(0xffffffffu, at, from), r = __shfl_sync(0xffffffffu, row, from);
-        for (int h = 0; h < p.N; ++h)
-          zero(s, h, r, p.slot_rows, W * gridDim.x, warp * gridDim.x + blockIdx.x);
+        const unsigned rows = p.slot_rows - r, step = W * gridDim.x;
+        if (rows >= step) {
+          for (int h = 0; h < p.N; ++h)
+            zero(s, h, r, p.slot_rows, step, warp * gridDim.x + blockIdx.x);
+          continue;
+        }
+        // fewer rows than warps: all heads' rows one after another
+        const unsigned step_heads = step / rows, step_rows = step - step_heads * rows;
+        unsigned k = warp * gridDim.x + blockIdx.x, h = k / rows;
+        k -= h * rows;
+        while (h < (unsigned)p.N) {
+          zero(s, (int)h, r + (int)k, r + (int)k + 1, 1, 0);
+          h += step_heads;
+          k += step_rows;
+          if (k >= rows) {
+            k -= rows;
+            ++h;
+          }
+        }
       }
     }
   }
   template <class Zero>
   __device__ void begin(const RecParams& p, int warp, Zero&& zero) {
     dout = state = nullptr;
-    if (p.spread) zero_all(p, zero);
     t = SOLO ? 0 : warp;
     enter<true>(p, zero);
   }
@@ -400,6 +416,7 @@ __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
   Ahead ahead[kStages - 1];
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) ahead[s] = issue(s);
+  if (p.spread) walk.zero_all(p, zero);
 
   GateScale gc{};
   F bias = splat<P>(0.f);
@@ -537,6 +554,7 @@ __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
   Ahead ahead[kStages - 1];
 #pragma unroll
   for (int s = 0; s < kStages - 1; ++s) ahead[s] = issue(s);
+  if (p.spread) walk.zero_all(p, zero);
 
   // the warp's part of the parameters' gradients in the unit, and where it goes
   F sum_b = splat<P>(0.f), sum_raw = splat<P>(0.f);

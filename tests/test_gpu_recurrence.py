@@ -644,6 +644,7 @@ def test_compiled_and_python_calls_agree(cuda_ok, monkeypatch):
                 a = args(d, lb, layout, h0)
                 out, final, states = kda.gated_recurrence(*a, return_states=True)
                 res += [*kda.gated_recurrence(*a), out, final]
+                res += kda.gated_recurrence(*a, return_states=1)
                 for dout in (d["dout"], None):
                     for dfinal in (d["dfinal"], None):
                         res += kda.gated_recurrence_backward(dout, dfinal, *a, states)
@@ -695,7 +696,7 @@ def test_compiled_calls_follow_stream_grad_mode_and_capture(cuda_ok):
             del out
             out, _ = kda.gated_recurrence(*args(d, -1.0, "TND"))
         s.synchronize()
-        torch.cuda._sleep(20_000_000)
+        torch.cuda._sleep(400_000_000)
         del out
         out, _ = kda.gated_recurrence(*args(d, -1.0, "TND"))
         done = torch.cuda.Event()
