@@ -338,3 +338,25 @@ def test_captured_training_step(cuda_ok):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(captured, step()))
+
+
+def test_frequencies_of_every_size(cuda_ok):
+    """Very slow and very fast rotations, negative ones and none; a frequency that is not a number
+    spoils its own pair alone.  Positions below 2^20 and frequencies below 7: the reference's angle, a
+    product in fp64, is off by at most 2^-53 of 7e6, 1e-9, far below the bound."""
+    d = make("TND", 1, 2, 1, 48, 64, FP, seed=20)
+    d["pos"][:8] = torch.arange(8, dtype=torch.int32)
+    d["inv"] = torch.tensor([1e-12, 1e-7, 3.0, 6.2831855, 0.7, -2.5, 0.0, 1.5707964] * 4, device="cuda")
+    for interleaved in (False, True):
+        check_all(*run_both(d, "TND", interleaved))
+    # a turn of 1e-7 keeps its own relative accuracy: x alone, one position
+    one = dict(d, q=torch.zeros(1, 1, 64, device="cuda"), pos=torch.ones(1, dtype=torch.int32).cuda())
+    one["q"][0, 0, 2] = 8.0
+    q, _ = kda.qk_norm_rope(one["q"], one["q"], one["pos"], d["inv"], None, None, 0.0, "TND",
+                            interleaved=True)
+    assert abs(q[0, 0, 3].item() / (8.0 * 1e-7) - 1) < 1e-6
+    d["inv"][5] = float("nan")
+    q, _ = kda.qk_norm_rope(*inputs(d), EPS, "TND")
+    bad = torch.zeros(64, dtype=torch.bool, device="cuda")
+    bad[5] = bad[37] = True
+    assert torch.isnan(q[..., bad]).all() and torch.isfinite(q[..., ~bad]).all()
