@@ -181,19 +181,22 @@ __device__ __forceinline__ void head_range(const QkParams& p, int side, int* lo,
   *hi = min(n, ((int)blockIdx.y + 1) * p.heads_per - before);
 }
 
-// A token of a group: its slot, its place there and its position (negative: padding, or none left).
+// A token of a group: its slot and its place there.
 struct Token {
   long long b;
-  int s, pos;
+  int s;
   bool mine;
   __device__ Token(const QkParams& p, long long t) {
     mine = t < p.tokens;
     if (!mine) t = 0;
     b = p.tokens <= UINT32_MAX ? (uint32_t)t / (uint32_t)p.S : t / p.S;
     s = (int)(t - b * p.S);
-    pos = !mine ? -1 : p.positions ? __ldg(p.positions + t) : s;
   }
 };
+// Its position where positions are given; it is asked for a token ahead, so that nothing waits for it.
+__device__ __forceinline__ int given_position(const QkParams& p, long long t) {
+  return p.positions && t < p.tokens ? __ldg(p.positions + t) : 0;
+}
 
 // The copies that run ahead: a warp's way through its groups' tokens, sides and heads, kRows heads of
 // one side a step.  The bounds are the block's, so that a warp's lanes stay together.
@@ -203,11 +206,12 @@ struct Ahead {
   static constexpr int U = kRows<T>, kTensors = BACKWARD ? 2 : 1;
   static constexpr int kRowBytes = D * (int)sizeof(T), kCopies = (int)sizeof(T) / 2;
   long long t0;
-  int side, h, end;
+  int side, h, end, next_pos;
   bool done, live;
   const char *x, *y;
 
-  __device__ void enter(const QkParams& p, const P& me, const Token& t) {
+  __device__ void enter(const QkParams& p, const P& me) {
+    const Token t(p, t0 + me.group);
     const QkSide& a = p.side[side];
     head_range(p, side, &h, &end);
     x = static_cast<const char*>(a.x.data) +
@@ -218,26 +222,24 @@ struct Ahead {
           (t.b * a.dy.stride_b + t.s * a.dy.stride_s + h * a.dy.stride_n) * (long long)sizeof(T) +
           me.lane * 16;
   }
-  // to the first side with heads of the next token that has one
-  __device__ void settle(const QkParams& p, const P& me) {
-    for (;;) {
-      done = t0 >= p.tokens;
-      if (done) return;
-      const Token t(p, t0 + me.group);
-      live = t.pos >= 0;
-      for (; side < 2; ++side) {
-        enter(p, me, t);
-        if (h < end) return;
-      }
-      side = 0;
-      t0 += (long long)gridDim.x * P::kGroups;
+  // at a token: its first side with heads
+  __device__ void arrive(const QkParams& p, const P& me) {
+    done = t0 >= p.tokens;
+    if (done) return;
+    live = t0 + me.group < p.tokens && next_pos >= 0;
+    next_pos = given_position(p, t0 + me.group + (long long)gridDim.x * P::kGroups);
+    side = 0;
+    enter(p, me);
+    if (h >= end) {
+      side = 1;
+      enter(p, me);
     }
   }
   __device__ void begin(const QkParams& p, const P& me) {
     x = y = nullptr;
     t0 = (long long)blockIdx.x * P::kGroups;
-    side = 0;
-    settle(p, me);
+    next_pos = given_position(p, t0 + me.group);
+    arrive(p, me);
   }
   // Starts the copies of a step; rows of padding become zeros.
   __device__ void issue(const QkParams& p, const P& me, uint32_t stage) {
@@ -258,12 +260,13 @@ struct Ahead {
         if (BACKWARD) y += a.dy.stride_n * (long long)sizeof(T);
       }
       h += U;
+      if (h >= end && side == 0) {
+        side = 1;
+        enter(p, me);
+      }
       if (h >= end) {
-        if (++side == 2) {
-          side = 0;
-          t0 += (long long)gridDim.x * P::kGroups;
-        }
-        settle(p, me);
+        t0 += (long long)gridDim.x * P::kGroups;
+        arrive(p, me);
       }
     }
     copies_issued();
@@ -291,12 +294,14 @@ __global__ void __launch_bounds__(kThreads, kResident)
   Eight dw[2];
   if (BACKWARD)
     for (int i = 0; i < 2; ++i) dw[i] = {splat<2>(0.f), splat<2>(0.f)};
-  int stage = 0, free = kS - 1;
+  int stage = 0, free = kS - 1, next_pos = given_position(p, (long long)blockIdx.x * P::kGroups + me.group);
   for (long long t0 = (long long)blockIdx.x * P::kGroups; t0 < p.tokens;
        t0 += (long long)gridDim.x * P::kGroups) {
     const Token t(p, t0 + me.group);
-    const bool live = t.pos >= 0;
-    const Angles turns = angles(p, me, live ? t.pos : 0);
+    const int pos = p.positions ? next_pos : t.s;
+    next_pos = given_position(p, t0 + me.group + (long long)gridDim.x * P::kGroups);
+    const bool live = t.mine && pos >= 0;
+    const Angles turns = angles(p, me, live ? pos : 0);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const QkSide& a = p.side[side];
