@@ -360,3 +360,19 @@ def test_frequencies_of_every_size(cuda_ok):
     bad = torch.zeros(64, dtype=torch.bool, device="cuda")
     bad[5] = bad[37] = True
     assert torch.isnan(q[..., bad]).all() and torch.isfinite(q[..., ~bad]).all()
+
+
+@pytest.mark.parametrize("layout,B,S", [("TND", 1, 20011), ("BNSD", 3, 6007), ("BSND", 2, 9001)])
+def test_in_place_over_many_turns(layout, B, S, cuda_ok):
+    """Every block takes several tokens, with the next ones' rows under way while it writes."""
+    d = make(layout, B, 3, 2, S, 64, BF, seed=21)
+    a = (d["pos"], d["inv"], d["qw"], d["kw"], EPS, layout)
+    want = kda.qk_norm_rope(d["q"], d["k"], *a)
+    back = kda.qk_norm_rope_backward(d["dq"], d["dk"], d["q"], d["k"], *a)
+    dq, dk = d["dq"].clone(), d["dk"].clone()
+    mine = kda.qk_norm_rope_backward(dq, dk, d["q"], d["k"], *a, dq=dq, dk=dk)
+    assert mine[0].data_ptr() == dq.data_ptr() and mine[1].data_ptr() == dk.data_ptr()
+    assert all(torch.equal(p, q) for p, q in zip(mine, back))
+    q, k = d["q"].clone(), d["k"].clone()
+    kda.qk_norm_rope(q, k, *a, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1])

@@ -711,3 +711,45 @@ def test_compiled_calls_follow_stream_grad_mode_and_capture(cuda_ok):
     with torch.inference_mode():
         out, _ = kda.gated_recurrence(*ts, -1.0, "TND", d["plan"])
         assert torch.equal(out, want) and out.is_inference()
+
+
+@pytest.mark.parametrize("lengths,N,S", [([4000, 9], 2, 4100), ([1 + i % 30 for i in range(900)], 8, 31),
+                                         ([70, 500, 3], 3, 500)])
+def test_workspace_and_results_between_guards(lengths, N, S, cuda_ok):
+    """Cut sequences, a warp for each of many short ones, and a ring: the workspaces of both passes and
+    the forward's results end where they say, and the status is left in them."""
+    d = make("BSND", lengths, N, 64, HF, S=S, seed=36)
+    plan, a = d["plan"], args(d, -1.0, "BSND")
+
+    def guarded(n, dtype, fill):
+        buf = torch.full((n + 8192,), fill, dtype=dtype, device="cuda")
+        return buf, buf[4096:4096 + n]
+
+    want = kda.gated_recurrence(*a, return_states=True)
+    want_grads = kda.gated_recurrence_backward(d["dout"], d["dfinal"], *a, want[2])
+    ob, out = guarded(d["x"].numel(), HF, 3.0)
+    fb, final = guarded(d["h0"].numel(), FP, 3.0)
+    wb, ws = guarded(plan.workspace_bytes, torch.uint8, 7)
+    got = kda.gated_recurrence(*a, out=out.view(d["x"].shape), final_state=final.view(d["h0"].shape),
+                               workspace=ws, return_states=True)
+    kda.device_status(ws)
+    bb, bws = guarded(plan.backward_workspace_bytes, torch.uint8, 7)
+    grads = kda.gated_recurrence_backward(d["dout"], d["dfinal"], *a, got[2], workspace=bws)
+    kda.device_status(bws)
+    assert all(torch.equal(p, q) for p, q in zip(got + grads, want + want_grads))
+    for buf, fill in ((ob, 3), (fb, 3), (wb, 7), (bb, 7)):
+        assert (buf[:4096] == fill).all() and (buf[-4096:] == fill).all()
+    short = torch.empty(plan.backward_workspace_bytes - 1, dtype=torch.uint8, device="cuda")
+    with pytest.raises(kda.KdaError):
+        kda.gated_recurrence_backward(d["dout"], d["dfinal"], *a, got[2], workspace=short)
+
+
+def test_broadcast_writes_and_gates(cuda_ok):
+    """One write logit for all heads and tokens, one gate for all tokens, one gradient for all: strides
+    of zero in every place, the gradients of every copy apart."""
+    lengths, layout = [700, 41], "BSND"
+    d = make(layout, lengths, 3, 64, FP, S=700, seed=37, pad=0.0)
+    d["beta"] = d["beta"][:1, :1, :1].expand(2, 700, 3)
+    d["g"] = d["g"][:, :1].expand(2, 700, 3, 64)
+    d["dout"] = d["dout"][:1, :1, :1].expand(2, 700, 3, 64)
+    check_all(*run_both(d, -2.0, layout, lengths))
