@@ -5,7 +5,7 @@
 Compiles every ``csrc/*.cu`` and ``csrc/*.cpp`` to objects under ``_build/`` (in parallel)
 and links ``chunked_kda_prefill_b200/libkda.so`` with the CUDA runtime linked statically, so
 the library loads on a machine without a GPU (its host entry points work there).  With g++ it also
-compiles ``binding/calls.cpp`` against this interpreter and its torch into ``_calls.so``, the calls of
+compiles ``binding/calls.cpp`` against this interpreter and its torch into ``_calls``, the calls of
 the operators around the prefill in their common form; without that file (or under another torch)
 they take the same way through ctypes, at two to three times the host time.
 
@@ -20,13 +20,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libkda.so")
-CALLS = os.path.join(PKG, "_calls.so")
+CALLS = os.path.join(PKG, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
@@ -68,13 +69,11 @@ def _compile(src, verbose, build_dir=BUILD, defines=()):
 
 
 def build_calls(force: bool = False) -> str:
-    """``_calls.so``, or a RuntimeError that says why it could not be compiled."""
-    import sysconfig
-
+    """The compiled calls' file, or a RuntimeError that says why it could not be compiled."""
     import torch
 
     src = os.path.join(PKG, "binding", "calls.cpp")
-    stamp = os.path.join(BUILD, "calls.torch")  # the torch that _calls.so was compiled against
+    stamp = os.path.join(BUILD, "calls.torch")  # the torch that it was compiled against
     header = os.path.join(PKG, "..", "include", "kda.h")
     fresh = (os.path.exists(stamp) and open(stamp).read() == torch.__version__
              and not _stale(CALLS, [src, header]))
