@@ -206,27 +206,30 @@ struct Ahead {
   static constexpr int U = kRows<T>, kTensors = BACKWARD ? 2 : 1;
   static constexpr int kRowBytes = D * (int)sizeof(T), kCopies = (int)sizeof(T) / 2;
   long long t0;
-  int side, h, end, next_pos;
+  int side, h, end, next_pos, s;
+  long long b;  // the token's slot, s its place there
   bool done, live;
   const char *x, *y;
 
   __device__ void enter(const QkParams& p, const P& me) {
-    const Token t(p, t0 + me.group);
     const QkSide& a = p.side[side];
     head_range(p, side, &h, &end);
     x = static_cast<const char*>(a.x.data) +
-        (t.b * a.x.stride_b + t.s * a.x.stride_s + h * a.x.stride_n) * (long long)sizeof(T) +
+        (b * a.x.stride_b + s * a.x.stride_s + h * a.x.stride_n) * (long long)sizeof(T) +
         me.lane * 16;
     if (BACKWARD)
       y = static_cast<const char*>(a.dy.data) +
-          (t.b * a.dy.stride_b + t.s * a.dy.stride_s + h * a.dy.stride_n) * (long long)sizeof(T) +
+          (b * a.dy.stride_b + s * a.dy.stride_s + h * a.dy.stride_n) * (long long)sizeof(T) +
           me.lane * 16;
   }
   // at a token: its first side with heads
   __device__ void arrive(const QkParams& p, const P& me) {
     done = t0 >= p.tokens;
     if (done) return;
-    live = t0 + me.group < p.tokens && next_pos >= 0;
+    const Token t(p, t0 + me.group);
+    b = t.b;
+    s = t.s;
+    live = t.mine && next_pos >= 0;
     next_pos = given_position(p, t0 + me.group + (long long)gridDim.x * P::kGroups);
     side = 0;
     enter(p, me);
