@@ -12,7 +12,7 @@
 // rows of the next steps are on their way to shared memory meanwhile (without them in registers more
 // blocks fit a multiprocessor), and only the sums over a row cross lanes.
 // Both passes are bound by HBM: 4 bytes a value forward (16-bit), 6 backward.  Forward 4x32x16384
-// bf16, 64 heads a token, 341 us: 6.3 TB/s of the 6.47 that a copy reaches; backward of 65536 tokens
+// bf16, 64 heads a token, 343 us: 6.26 TB/s of the 6.47 that a copy reaches; backward of 65536 tokens
 // with 40 heads 333 us, 6.05 TB/s.
 #include <cuda_runtime.h>
 
@@ -55,16 +55,15 @@ struct QkParams {
 };
 
 // Rows of a step (so that their sums over lanes overlap), blocks on a multiprocessor, and the steps
-// whose copies a warp has under way or at work.  More of either is slower: 4x32x16384 forward takes
-// 345-353 us with 3 or 4 steps, 382 with 6 and 397 with 3 blocks, one block 488.
+// whose copies a warp has under way or at work.  More of either is slower, and fewer: 4x32x16384
+// forward takes 344 us with 3 steps, 371 with 4 and 428 with 2; three blocks took 397, one block 488.
 template <class T>
 constexpr int kRows = sizeof(T) == 2 ? 2 : 1;
 constexpr int kResident = 2;
-template <bool BACKWARD>
-constexpr int kStages = BACKWARD ? 3 : 4;
+constexpr int kStages = 3;
 
 template <class T, int D, bool BACKWARD>
-constexpr int kQkSmem = kStages<BACKWARD> * (BACKWARD ? 2 : 1) * kRows<T> * kThreads * 8 * (int)sizeof(T);
+constexpr int kQkSmem = kStages * (BACKWARD ? 2 : 1) * kRows<T> * kThreads * 8 * (int)sizeof(T);
 
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v) {
@@ -120,15 +119,19 @@ struct Angles {
   F c, s;
 };
 template <class P>
-__device__ __forceinline__ Angles angles(const QkParams& p, const P& me, int pos) {
+__device__ __forceinline__ double turn_rate(const QkParams& p, const P& me, int i) {
   constexpr double kInv2Pi = 0.15915494309189533577;
+  return me.turns ? (double)__ldg(p.inv_freq + me.lane * 4 + i) * kInv2Pi : 0.0;
+}
+template <class P>
+__device__ __forceinline__ Angles angles(const P& me, const double (&rate)[4], int pos) {
   Angles r{splat<2>(1.f), splat<2>(0.f)};
   if (!me.turns) return r;
   float c[4], s[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     // whole turns drop out in fp64: the product is off by at most 2^-53 of up to 2^31 radians
-    double turns = (double)pos * ((double)__ldg(p.inv_freq + me.lane * 4 + i) * kInv2Pi);
+    double turns = (double)pos * rate[i];
     turns -= rint(turns);
     sincospif(2.f * (float)turns, &s[i], &c[i]);
   }
@@ -285,41 +288,50 @@ template <class T, int D, bool INTER, bool BACKWARD>
 __global__ void __launch_bounds__(kThreads, kResident)
     qk_kernel(const __grid_constant__ QkParams p) {
   using P = Place<D, INTER>;
-  constexpr int U = kRows<T>, kS = kStages<BACKWARD>, kTensors = BACKWARD ? 2 : 1;
+  constexpr int U = kRows<T>, kTensors = BACKWARD ? 2 : 1;
   constexpr int kTensor = kThreads * 8, kStage = U * kTensors * kTensor;  // elements
   extern __shared__ __align__(16) uint8_t smem[];
-  T* const ring = reinterpret_cast<T*>(smem);  // [kS][U][kTensors][kGroups][D]
+  T* const ring = reinterpret_cast<T*>(smem);  // [kStages][U][kTensors][kGroups][D]
   const P me(p.turned);
   Ahead<T, D, INTER, BACKWARD> ahead;
   ahead.begin(p, me);
-  for (int i = 0; i < kS - 1; ++i) ahead.issue(p, me, smem_u32(ring + i * kStage));
+  for (int i = 0; i < kStages - 1; ++i) ahead.issue(p, me, smem_u32(ring + i * kStage));
   launch_dependents();
-  Eight dw[2];
+  // The forward pass keeps both sides' weights and the frequencies in registers; the backward pass has
+  // none left, and reads them again for every token.
+  Eight dw[2], weights[2];
+  double rate[4];  // turns for a position
+  if (!BACKWARD) {
+    for (int i = 0; i < 2; ++i) weights[i] = load_weight(p.side[i], me);
+    for (int i = 0; i < 4; ++i) rate[i] = turn_rate(p, me, i);
+  }
   if (BACKWARD)
     for (int i = 0; i < 2; ++i) dw[i] = {splat<2>(0.f), splat<2>(0.f)};
-  int stage = 0, free = kS - 1, next_pos = given_position(p, (long long)blockIdx.x * P::kGroups + me.group);
+  int stage = 0, free = kStages - 1, next_pos = given_position(p, (long long)blockIdx.x * P::kGroups + me.group);
   for (long long t0 = (long long)blockIdx.x * P::kGroups; t0 < p.tokens;
        t0 += (long long)gridDim.x * P::kGroups) {
     const Token t(p, t0 + me.group);
     const int pos = p.positions ? next_pos : t.s;
     next_pos = given_position(p, t0 + me.group + (long long)gridDim.x * P::kGroups);
     const bool live = t.mine && pos >= 0;
-    const Angles turns = angles(p, me, live ? pos : 0);
+    if (BACKWARD)
+      for (int i = 0; i < 4; ++i) rate[i] = turn_rate(p, me, i);
+    const Angles turns = angles(me, rate, live ? pos : 0);
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
       const QkSide& a = p.side[side];
       int h, end;
       head_range(p, side, &h, &end);
       if (h >= end) continue;
-      const Eight w = load_weight(a, me);
+      const Eight w = BACKWARD ? load_weight(a, me) : weights[side];
       T* to = static_cast<T*>(a.out) + t.b * a.od.stride_b + t.s * a.od.stride_s +
               h * a.od.stride_n;
       for (; h < end; h += U) {
-        copies_arrived<kS - 2>();
+        copies_arrived<kStages - 2>();
         ahead.issue(p, me, smem_u32(ring + free * kStage));
-        free = free + 1 == kS ? 0 : free + 1;
+        free = free + 1 == kStages ? 0 : free + 1;
         const T* row = ring + stage * kStage + me.group * D;
-        stage = stage + 1 == kS ? 0 : stage + 1;
+        stage = stage + 1 == kStages ? 0 : stage + 1;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           Eight x = me.read(row);
