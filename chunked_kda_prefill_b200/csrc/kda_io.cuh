@@ -33,6 +33,12 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // The head's constants of the gate a = exp(lb sigmoid(e^A raw)): both exponentials are powers of
 // two, so log2(e) is folded into the factors once.
 struct GateScale {
@@ -43,8 +49,8 @@ struct GateScale {
 __device__ __forceinline__ GateScale gate_scale(float A_log, float lower_bound) {
   constexpr float kLog2e = 1.4426950408889634f;
   const float ea = expf(A_log);
-  // never zero: a raw gate of -inf closes the gate whatever A_log is
-  return {ea, fminf(-kLog2e * ea, -1.1754944e-38f), lower_bound * kLog2e};
+  // never zero: a raw gate of -inf closes the gate whatever number A_log is (NaN stays NaN)
+  return {ea, min_nan(-kLog2e * ea, -1.1754944e-38f), lower_bound * kLog2e};
 }
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 

@@ -376,12 +376,6 @@ __device__ __forceinline__ void store_rows(T* to, long long next, int valid, con
   }
 }
 
-__device__ __forceinline__ float min_nan(float a, float b) {  // NaN if one is
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
 // 4x32x16384 bf16: 292 us, 5.5 TB/s of the 6.47 that a copy reaches (6.05 TB/s where 148 units keep
 // every multiprocessor busy).  What else is busy: 65 % of the special-function unit, three results a
 // value.  Sharing one reciprocal between two values (289 us) is not worth its second path for
