@@ -63,3 +63,60 @@ def test_nan_in_a_log_spoils_its_head_alone(name, cuda_ok):
     for n in ("dA_log", "ddt_bias"):
         assert torch.equal(got[n][keep], clean[n][keep]), n
     assert all(torch.equal(p[:, keep], q[:, keep]) for p, q in zip(bad, step))
+
+
+def last_tokens(lengths):
+    return torch.tensor(lengths).cumsum(0).sub(1).cuda()
+
+
+@pytest.mark.parametrize("D", [128, 64])
+@pytest.mark.parametrize("name", list(FORMS))
+def test_infinite_bias_is_a_gate_held_open(name, D, cuda_ok):
+    """dt_bias = inf makes the sigmoid one, as a bias of 1e30 does, and so does every result that has a
+    value: dA_log is 0 * inf by its formula and left out."""
+    d, lengths = form(name, D, seed=2)
+    d["dt_bias"] = d["dt_bias"].clone()
+    d["dt_bias"][1, 5] = 1e30
+    want, step = both(d), single(d)
+    d["dt_bias"][1, 5] = float("inf")
+    got, open_step = both(d), single(d)
+    for n in got:
+        if n == "dA_log":
+            assert torch.equal(got[n][:1], want[n][:1])
+        else:
+            assert torch.isfinite(got[n]).all() and torch.equal(got[n], want[n]), n
+    assert all(torch.equal(p, q) for p, q in zip(open_step, step))
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("name", list(FORMS))
+def test_last_token_does_not_reach_the_parameters(name, bad, cuda_ok):
+    """No gradient but dbeta contains the last token's value: an infinite or broken one leaves the
+    bits of all others, wherever in a tile the sequence ends."""
+    d, lengths = form(name, seed=3)
+    clean = both(d)
+    d["x"] = d["x"].clone()
+    last = last_tokens(lengths)
+    d["x"][last, 1, 5] = bad
+    got = both(d)
+    assert not torch.isfinite(got["final"][:, 1, 5]).any()
+    for n in ("dx", "dg", "dh0", "dA_log", "ddt_bias"):
+        assert torch.equal(got[n], clean[n]), n
+    others = torch.ones_like(clean["dbeta"], dtype=torch.bool)
+    others[last, 1] = False
+    assert torch.equal(got["dbeta"][others], clean["dbeta"][others])
+
+
+@pytest.mark.parametrize("param", ["A_log", "dt_bias"])
+@pytest.mark.parametrize("name", list(FORMS))
+def test_broken_parameter_leaves_the_last_gradient(name, param, cuda_ok):
+    """No decay lies behind a sequence's last token: its dx and dbeta are those of whole parameters."""
+    d, lengths = form(name, seed=4)
+    clean = both(d)
+    d[param] = d[param].clone()
+    d[param][1] = float("nan")
+    got, last = both(d), last_tokens(lengths)
+    for n in ("dx", "dbeta"):
+        assert torch.equal(got[n][last], clean[n][last]), n
+        assert torch.equal(got[n][:, 0], clean[n][:, 0]), n
+    assert torch.isnan(got["dg"][:, 1]).all() and torch.isnan(got["out"][:, 1]).all()
