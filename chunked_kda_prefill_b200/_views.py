@@ -5,6 +5,7 @@ from __future__ import annotations
 import contextlib
 
 import torch
+from torch.autograd import forward_ad
 
 from ._lib import KdaError, KdaView
 
@@ -84,11 +85,19 @@ def used_on(stream, *tensors) -> None:
             t.record_stream(stream)
 
 
+def has_tangent(*tensors) -> bool:
+    """Whether one carries a forward-mode derivative (which requires_grad does not say)."""
+    return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def needs_grad(*tensors) -> bool:
-    for t in tensors:
-        if t is not None and t.requires_grad:
-            return torch.is_grad_enabled()
-    return False
+    return has_tangent(*tensors) or (torch.is_grad_enabled()
+                                     and any(t is not None and t.requires_grad for t in tensors))
+
+
+def no_tangents(what: str, *tensors) -> None:
+    if has_tangent(*tensors):
+        raise ValueError(f"{what} has no forward-mode derivative")
 
 
 def dense_like(t: torch.Tensor) -> torch.Tensor:

@@ -8,6 +8,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
@@ -125,7 +126,15 @@ Tensor fresh(const Shape& s, const Tensor& on, ScalarType type) {
 kda_stream_t stream_of(int dev) {
   return reinterpret_cast<kda_stream_t>(c10::cuda::getCurrentCUDAStream(dev).stream());
 }
+// Whether one carries a forward-mode derivative.
+bool has_tangent(std::initializer_list<const Tensor*> ts) {
+  if (!c10::AutogradState::get_tls_state().get_fw_grad_mode()) return false;
+  for (const Tensor* t : ts)
+    if (t && t->_fw_grad(0).defined()) return true;  // there is one level
+  return false;
+}
 bool wants_grad(std::initializer_list<const Tensor*> ts) {
+  if (has_tangent(ts)) return true;
   if (!c10::GradMode::is_enabled()) return false;
   for (const Tensor* t : ts)
     if (t && t->requires_grad()) return true;
@@ -293,6 +302,7 @@ PyObject* recurrence_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!fits(dout, in.x->scalar_type(), p.x) || !view(*dout, p.shape.layout, true, &vd))
       Py_RETURN_NONE;
   }
+  if (has_tangent({in.x, in.g, in.beta, in.h0, in.A, in.bias, states, dout, dfinal})) Py_RETURN_NONE;
   const Tensor dx = like(*in.x), dg = like(*in.x), dbeta = like(*in.beta), dA = like(*in.A),
                dbias = like(*in.bias),
                work = fresh({(int64_t)p.backward_workspace}, *in.x, ScalarType::Byte);
@@ -416,7 +426,8 @@ PyObject* qk_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   kda_view_t vdq, vdk;
   const ScalarType type = in.q->scalar_type();
   if (!fits(dqo, type, in.q->sizes()) || !fits(dko, type, in.k->sizes()) ||
-      !view(*dqo, in.shape.layout, true, &vdq) || !view(*dko, in.shape.layout, true, &vdk))
+      !view(*dqo, in.shape.layout, true, &vdq) || !view(*dko, in.shape.layout, true, &vdk) ||
+      has_tangent({in.q, in.k, in.inv, in.qw, in.kw, dqo, dko}))
     Py_RETURN_NONE;
   size_t bytes = 0;
   const kda_status_t st = lib.qk_workspace(&in.shape, &bytes);

@@ -5,7 +5,7 @@
 Per token and head, r = 1 / sqrt(mean(x^2) + eps) and n = x r weight; the pair i of the first
 2 * len(inv_freq) channels then turns by position * inv_freq[i].  The outputs are dense in the
 layout, as flash_kda and decode take them.  ``qk_norm_rope`` is differentiable with respect to q, k
-and the weights; ``qk_norm_rope_backward`` is its backward pass as a call of its own.
+and the weights (once, in reverse mode: inputs with a forward-mode tangent are refused); ``qk_norm_rope_backward`` is its backward pass as a call of its own.
 
 Single tokens (a decode batch) are the TND layout with one token per sequence: q [B, Nq, D],
 positions [B].
@@ -18,8 +18,8 @@ import torch
 
 from . import _lib
 from ._lib import KdaError, KdaQkShape, check
-from ._views import (dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, used_on,
-                     view, viewable)
+from ._views import (dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, no_tangents,
+                     used_on, view, viewable)
 from .api import LAYOUTS, _ptr
 
 
@@ -102,6 +102,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k
                                 interleaved, dq_out, dk_out)
         if res is not None:
             return res if res.__class__ is tuple else check(res, "kda_qk_norm_rope_backward")
+    no_tangents("qk_norm_rope_backward", dq_out, dk_out, q, k, inv_freq, q_weight, k_weight)
     shape = _check(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved)
     dev = q.device
     expect(dq_out, "dq_out", q.dtype, dev, q.shape)

@@ -10,7 +10,7 @@ Per sequence, head n and channel d, with flash_kda's activations of the gate and
     h_t = a_t h_{t-1} + sigmoid(beta_t[n]) x_t,        out_t = h_t
 
 ``gated_recurrence`` is differentiable with respect to x, g, beta, initial_state, A_log and
-dt_bias.  ``gated_recurrence_backward`` is its backward pass as a call of its own, and
+dt_bias (once, in reverse mode: inputs with a forward-mode tangent are refused).  ``gated_recurrence_backward`` is its backward pass as a call of its own, and
 ``gated_recurrence_step`` one token for each sequence, from the state that a prefill returned.
 
 Every call can be captured in a CUDA graph; the plan is made before.  When a training step is
@@ -27,8 +27,8 @@ import torch
 
 from . import _lib
 from ._lib import KdaError, KdaRecurrenceShape, check
-from ._views import (DTYPES, dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, used_on,
-                     view, viewable)
+from ._views import (DTYPES, dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, no_tangents,
+                     used_on, view, viewable)
 from .api import LAYOUTS, _ptr
 
 _F32 = torch.float32
@@ -222,6 +222,8 @@ def gated_recurrence_backward(dout, dfinal_state, x, g, beta, initial_state, A_l
                                                dt_bias, lower_bound, states, dout, dfinal_state)
         if res is not None:
             return res if res.__class__ is tuple else check(res, "kda_recurrence_backward")
+    no_tangents("gated_recurrence_backward", dout, dfinal_state, x, g, beta, initial_state, A_log,
+                dt_bias, states)
     dev = x.device
     code = _check(plan, layout, dev, x, g, beta, initial_state, A_log, dt_bias)
     if dout is not None:

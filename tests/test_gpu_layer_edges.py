@@ -120,3 +120,58 @@ def test_broken_parameter_leaves_the_last_gradient(name, param, cuda_ok):
         assert torch.equal(got[n][last], clean[n][last]), n
         assert torch.equal(got[n][:, 0], clean[n][:, 0]), n
     assert torch.isnan(got["dg"][:, 1]).all() and torch.isnan(got["out"][:, 1]).all()
+
+
+def qk_inputs(kind=FP, S=40):
+    gen = torch.Generator().manual_seed(7)
+    rnd = lambda *s: torch.randn(*s, generator=gen).cuda()  # noqa: E731
+    return {"q": rnd(S, 3, 64).to(kind), "k": rnd(S, 2, 64).to(kind), "positions": None,
+            "inv_freq": rnd(16).abs(), "q_weight": rnd(64), "k_weight": rnd(64), "eps": 1e-6,
+            "layout": "TND"}
+
+
+def test_forward_mode_derivatives_are_refused(way):
+    """An input with a tangent: there is no forward-mode formula, and no call drops the tangent."""
+    from torch.autograd import forward_ad as fa
+    d = make("TND", [30, 9], 2, 64, FP, seed=5)
+    if way == "python":
+        d["plan"]._handle = None
+    plain = args(d, -1.0, "TND")
+    states = kda.gated_recurrence(*plain, return_states=True)[2]
+    qk = qk_inputs()
+    calls = 0
+    for grad in (torch.enable_grad, torch.no_grad):
+        with grad(), fa.dual_level():
+            dual = lambda t: fa.make_dual(t, torch.ones_like(t))  # noqa: E731
+            refused = (NotImplementedError, ValueError, RuntimeError)
+            for i in range(6):
+                a = list(plain)
+                a[i] = dual(a[i])
+                with pytest.raises(refused):
+                    kda.gated_recurrence(*a)
+                with pytest.raises(refused):
+                    kda.gated_recurrence_backward(d["dout"], None, *a, states)
+                calls += 1
+            for name in ("dout", "dfinal"):
+                g = {"dout": d["dout"], "dfinal": d["dfinal"]}
+                g[name] = dual(g[name])
+                with pytest.raises(refused):
+                    kda.gated_recurrence_backward(g["dout"], g["dfinal"], *plain, states)
+            for name in ("x", "g", "beta", "h0", "A_log", "dt_bias"):
+                with pytest.raises(refused):
+                    single(dict(d, **{name: dual(d[name])}))
+            for name in ("q", "k", "inv_freq", "q_weight", "k_weight"):
+                c = dict(qk, **{name: dual(qk[name])})
+                with pytest.raises(refused):
+                    kda.qk_norm_rope(**c)
+                with pytest.raises(refused):
+                    kda.qk_norm_rope_backward(qk["q"], qk["k"], **c)
+            for i in range(2):
+                g = [qk["q"], qk["k"]]
+                g[i] = dual(g[i])
+                with pytest.raises(refused):
+                    kda.qk_norm_rope_backward(*g, **qk)
+            # inputs without a tangent are taken at a dual level as anywhere
+            assert kda.gated_recurrence(*plain)[0].isfinite().all()
+            assert kda.qk_norm_rope(**qk)[0].isfinite().all() and single(d)[0].isfinite().all()
+    assert calls == 12
