@@ -3,6 +3,7 @@ arguments, the launch stream and the device of a call."""
 from __future__ import annotations
 
 import contextlib
+import sys
 
 import torch
 from torch.autograd import forward_ad
@@ -93,6 +94,15 @@ def has_tangent(*tensors) -> bool:
 def needs_grad(*tensors) -> bool:
     return has_tangent(*tensors) or (torch.is_grad_enabled()
                                      and any(t is not None and t.requires_grad for t in tensors))
+
+
+def not_recorded(what: str) -> None:
+    """Refuses a call while torch.jit.trace or make_fx records: they see no operation of torch here and
+    would keep the results as constants."""
+    proxies = sys.modules.get("torch.fx.experimental.proxy_tensor")  # not loaded: nobody uses make_fx
+    if torch.jit.is_tracing() or (proxies is not None and proxies.get_proxy_mode() is not None):
+        raise RuntimeError(f"{what} cannot be recorded by torch.jit.trace or make_fx: its results "
+                           "would be constants of the recording")
 
 
 def no_tangents(what: str, *tensors) -> None:

@@ -10,6 +10,8 @@
 #include <ATen/ops/empty.h>
 #include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -80,6 +82,14 @@ bool maybe(PyObject* o, int dev, ScalarType type, at::IntArrayRef shape, const T
   if (o == Py_None) return true;
   *t = plain(o, dev);
   return dense(*t, type, shape);
+}
+
+// Whether a recording of torch's operations, or another mode that sees them, is on.
+bool watched() {
+  using c10::DispatchKey;
+  return c10::impl::TorchDispatchModeTLS::any_modes_set() ||
+         c10::impl::tls_is_dispatch_key_included(DispatchKey::Tracer) ||
+         c10::impl::tls_is_dispatch_key_included(DispatchKey::PreDispatch);
 }
 
 int type_code(ScalarType t) {
@@ -265,7 +275,7 @@ struct Inputs {
 PyObject* recurrence_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Inputs in;
-  if (n != 10 || !in.read(a[0], a[1], a + 2) ||
+  if (n != 10 || watched() || !in.read(a[0], a[1], a + 2) ||
       wants_grad({in.x, in.g, in.beta, in.h0, in.A, in.bias}))
     Py_RETURN_NONE;
   const Plan& p = *in.p;
@@ -290,7 +300,7 @@ PyObject* recurrence_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* recurrence_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Inputs in;
-  if (n != 12 || !in.read(a[0], a[1], a + 2)) Py_RETURN_NONE;
+  if (n != 12 || watched() || !in.read(a[0], a[1], a + 2)) Py_RETURN_NONE;
   const Plan& p = *in.p;
   const Tensor *dout = nullptr, *dfinal, *states = plain(a[9], in.dev);
   kda_view_t vd;
@@ -328,7 +338,7 @@ int device_of(PyObject* o) {  // of a CUDA tensor on the current device, else -1
 // recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound, out, state_out)
 PyObject* recurrence_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  const int dev = n == 9 ? device_of(a[0]) : -1;
+  const int dev = n == 9 && !watched() ? device_of(a[0]) : -1;
   if (dev < 0) Py_RETURN_NONE;
   const Tensor *x = plain(a[0], dev), *g = plain(a[1], dev), *beta = plain(a[2], dev),
                *A = plain(a[4], dev), *bias = plain(a[5], dev), *state, *out_arg, *state_arg;
@@ -409,7 +419,7 @@ struct Heads {
 PyObject* qk_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Heads in;
-  if (n != 9 || !in.read(a) || wants_grad({in.q, in.k, in.inv, in.qw, in.kw})) Py_RETURN_NONE;
+  if (n != 9 || watched() || !in.read(a) || wants_grad({in.q, in.k, in.inv, in.qw, in.kw})) Py_RETURN_NONE;
   const Tensor q = like(*in.q), k = like(*in.k);
   CALL(lib.qk_forward(&in.shape, &in.vq, &in.vk, data<int32_t>(in.pos), data(in.inv), data(in.qw),
                       data(in.kw), q.data_ptr(), k.data_ptr(), stream_of(in.dev)));
@@ -421,7 +431,7 @@ PyObject* qk_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* qk_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   Heads in;
-  if (n != 11 || !in.read(a)) Py_RETURN_NONE;
+  if (n != 11 || watched() || !in.read(a)) Py_RETURN_NONE;
   const Tensor *dqo = plain(a[9], in.dev), *dko = plain(a[10], in.dev);
   kda_view_t vdq, vdk;
   const ScalarType type = in.q->scalar_type();

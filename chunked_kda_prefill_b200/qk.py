@@ -19,7 +19,7 @@ import torch
 from . import _lib
 from ._lib import KdaError, KdaQkShape, check
 from ._views import (dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, no_tangents,
-                     used_on, view, viewable)
+                     not_recorded, used_on, view, viewable)
 from .api import LAYOUTS, _ptr
 
 
@@ -102,6 +102,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k
                                 interleaved, dq_out, dk_out)
         if res is not None:
             return res if res.__class__ is tuple else check(res, "kda_qk_norm_rope_backward")
+    not_recorded("qk_norm_rope_backward")
     no_tangents("qk_norm_rope_backward", dq_out, dk_out, q, k, inv_freq, q_weight, k_weight)
     shape = _check(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved)
     dev = q.device
@@ -177,6 +178,7 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps: float, layo
         res = calls.qk_forward(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved)
         if res is not None:
             return res if res.__class__ is tuple else check(res, "kda_qk_norm_rope")
+    not_recorded("qk_norm_rope")
     if inv_freq is not None and needs_grad(inv_freq):
         raise ValueError("inv_freq has no gradient here")
     if needs_grad(q, k, q_weight, k_weight):

@@ -28,7 +28,7 @@ import torch
 from . import _lib
 from ._lib import KdaError, KdaRecurrenceShape, check
 from ._views import (DTYPES, dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, no_tangents,
-                     used_on, view, viewable)
+                     not_recorded, used_on, view, viewable)
 from .api import LAYOUTS, _ptr
 
 _F32 = torch.float32
@@ -222,6 +222,7 @@ def gated_recurrence_backward(dout, dfinal_state, x, g, beta, initial_state, A_l
                                                dt_bias, lower_bound, states, dout, dfinal_state)
         if res is not None:
             return res if res.__class__ is tuple else check(res, "kda_recurrence_backward")
+    not_recorded("gated_recurrence_backward")
     no_tangents("gated_recurrence_backward", dout, dfinal_state, x, g, beta, initial_state, A_log,
                 dt_bias, states)
     dev = x.device
@@ -304,6 +305,7 @@ def gated_recurrence(x, g, beta, initial_state, A_log, dt_bias, lower_bound: flo
                                               dt_bias, lower_bound, return_states)
         if res is not None:
             return res if res.__class__ is tuple else check(res, "kda_recurrence_forward")
+    not_recorded("gated_recurrence")
     if needs_grad(x, g, beta, initial_state, A_log, dt_bias):
         if (out is not None or final_state is not None or return_states or workspace is not None
                 or stream is not None):
@@ -329,6 +331,7 @@ def gated_recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound: float,
         res = calls.recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound, out, state_out)
         if res is not None:
             return res if res.__class__ is tuple else check(res, "kda_recurrence_step")
+    not_recorded("gated_recurrence_step")
     dev = x.device
     if dev.type != "cuda":
         raise ValueError("gated_recurrence_step runs on a CUDA device only")

@@ -175,3 +175,37 @@ def test_forward_mode_derivatives_are_refused(way):
             assert kda.gated_recurrence(*plain)[0].isfinite().all()
             assert kda.qk_norm_rope(**qk)[0].isfinite().all() and single(d)[0].isfinite().all()
     assert calls == 12
+
+
+def test_recording_a_call_is_refused(way):
+    """torch.jit.trace and make_fx would keep the results of the traced call as constants."""
+    from torch.fx.experimental.proxy_tensor import make_fx
+    d = make("TND", [30, 9], 2, 64, FP, seed=6)
+    if way == "python":
+        d["plan"]._handle = None
+    a = args(d, -1.0, "TND")
+    states = kda.gated_recurrence(*a, return_states=True)[2]
+    qk = qk_inputs()
+    rest = {n: v for n, v in qk.items() if n != "q"}
+    runs = [lambda x: kda.gated_recurrence(x, *a[1:])[0],
+            lambda x: kda.gated_recurrence_backward(x, None, *a, states)[0],
+            lambda x: single(dict(d, x=x))[0]]
+    for f, t in [(f, d["x"]) for f in runs] + [
+            (lambda q: kda.qk_norm_rope(q=q, **rest)[0], qk["q"]),
+            (lambda q: kda.qk_norm_rope_backward(q, qk["k"], **qk)[0], qk["q"])]:
+        for want in (False, True):
+            t = t.clone().requires_grad_(want)
+            with pytest.raises(RuntimeError, match="recorded"):
+                torch.jit.trace(f, (t,), check_trace=False)
+            with pytest.raises(RuntimeError, match="recorded"):
+                make_fx(f)(t)
+        # modes that only watch are no recording
+        from torch.utils._python_dispatch import TorchDispatchMode
+
+        class Watch(TorchDispatchMode):
+            def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+                return func(*args, **(kwargs or {}))
+        with Watch(), torch.no_grad():
+            watched = f(t)
+        with torch.no_grad():
+            assert torch.equal(watched, f(t))
