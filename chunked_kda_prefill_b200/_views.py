@@ -96,6 +96,20 @@ def needs_grad(*tensors) -> bool:
                                      and any(t is not None and t.requires_grad for t in tensors))
 
 
+def results(*tensors) -> None:
+    """Checks the results that a caller supplies: a call writes to their memory, which autograd does not
+    follow."""
+    if needs_grad(*tensors):
+        raise ValueError("results that require a gradient cannot be written to; use torch.no_grad()")
+
+
+def written(*tensors) -> None:
+    """Tells autograd that supplied results have new values, for graphs that saved the old ones."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 def not_recorded(what: str) -> None:
     """Refuses a call while torch.jit.trace or make_fx records: they see no operation of torch here and
     would keep the results as constants."""

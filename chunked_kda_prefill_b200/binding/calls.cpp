@@ -352,13 +352,16 @@ PyObject* recurrence_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
       !dense(A, ScalarType::Float, s.slice(1, 1)) || !dense(bias, ScalarType::Float, s.slice(1, 2)) ||
       !maybe(a[3], dev, ScalarType::Float, s, &state) || !number(a[6], &lb) ||
       !maybe(a[7], dev, type, s, &out_arg) || !maybe(a[8], dev, ScalarType::Float, s, &state_arg) ||
-      wants_grad({x, g, beta, state, A, bias}))
+      wants_grad({x, g, beta, state, A, bias, out_arg, state_arg}))
     Py_RETURN_NONE;
   const Tensor out = out_arg ? *out_arg : like(*x);
   const Tensor next = state_arg ? *state_arg : at::empty(s, x->options().dtype(ScalarType::Float));
   CALL(lib.rec_step((int32_t)s[0], (int32_t)s[1], (int32_t)s[2], code, x->data_ptr(), g->data_ptr(),
                     beta->data_ptr(), data(state), data(A), data(bias), lb, out.data_ptr(),
                     data(&next), stream_of(dev)));
+  // graphs that saved a supplied result's old values are to notice
+  for (const Tensor* t : {out_arg, state_arg})
+    if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
   return tuple_of({&out, &next});
   END_HANDLE_TH_ERRORS
 }

@@ -19,7 +19,7 @@ import torch
 from . import _lib
 from ._lib import KdaError, KdaQkShape, check
 from ._views import (dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, no_tangents,
-                     not_recorded, used_on, view, viewable)
+                     not_recorded, results, used_on, view, viewable, written)
 from .api import LAYOUTS, _ptr
 
 
@@ -67,6 +67,8 @@ def _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interle
              stream):
     shape = _check(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleaved)
     dev = q.device
+    results(q_out, k_out)
+    given = q_out, k_out
     if q_out is not None:
         expect_dense(q_out, "q_out", q.dtype, dev, q.shape)
     if k_out is not None:
@@ -83,6 +85,7 @@ def _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interle
             ctypes.byref(shape), ctypes.byref(view(q, "q", layout)),
             ctypes.byref(view(k, "k", layout)), _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
             _ptr(k_weight), q_out.data_ptr(), k_out.data_ptr(), handle), "kda_qk_norm_rope")
+    written(*given)
     return q_out, k_out
 
 
@@ -108,6 +111,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k
     dev = q.device
     expect(dq_out, "dq_out", q.dtype, dev, q.shape)
     expect(dk_out, "dk_out", q.dtype, dev, k.shape)
+    results(dq, dk)
+    given = dq, dk
     for t, name, like in ((dq, "dq", q), (dk, "dk", k)):
         if t is not None:
             expect_dense(t, name, q.dtype, dev, like.shape)
@@ -135,6 +140,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k
             ctypes.byref(view(k, "k", layout)), _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
             _ptr(k_weight), ws.data_ptr(), ws_bytes, dq.data_ptr(), dk.data_ptr(),
             _ptr(dqw), _ptr(dkw), handle), "kda_qk_norm_rope_backward")
+    written(*given)
     return dq, dk, dqw, dkw
 
 

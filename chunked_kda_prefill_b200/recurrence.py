@@ -28,7 +28,7 @@ import torch
 from . import _lib
 from ._lib import KdaError, KdaRecurrenceShape, check
 from ._views import (DTYPES, dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, no_tangents,
-                     not_recorded, used_on, view, viewable)
+                     not_recorded, results, used_on, view, viewable, written)
 from .api import LAYOUTS, _ptr
 
 _F32 = torch.float32
@@ -178,6 +178,8 @@ def _forward(x, g, beta, initial_state, A_log, dt_bias, lower_bound, layout, pla
              final_state, want_states, workspace, stream):
     dev = x.device
     code = _check(plan, layout, dev, x, g, beta, initial_state, A_log, dt_bias)
+    results(out, final_state)
+    given = out, final_state
     if out is not None:
         expect_dense(out, "out", x.dtype, dev, plan._x)
     if final_state is not None:
@@ -204,6 +206,7 @@ def _forward(x, g, beta, initial_state, A_log, dt_bias, lower_bound, layout, pla
             ctypes.byref(view(beta, "beta", layout, channels=False)), _ptr(initial_state),
             A_log.data_ptr(), dt_bias.data_ptr(), float(lower_bound), _ptr(states), ws_ptr,
             ws_bytes, out.data_ptr(), final_state.data_ptr(), handle), "kda_recurrence_forward")
+    written(*given)
     return out, final_state, states
 
 
@@ -356,6 +359,8 @@ def gated_recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound: float,
         expect_dense(dt_bias, "dt_bias", _F32, dev, shape[1:])
     if state is not None:
         expect_dense(state, "state", _F32, dev, shape)
+    results(out, state_out)
+    given = out, state_out
     if out is not None:
         expect_dense(out, "out", x.dtype, dev, shape)
     if state_out is not None:
@@ -373,4 +378,5 @@ def gated_recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound: float,
             B, N, D, code, x.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state),
             A_log.data_ptr(), dt_bias.data_ptr(), float(lower_bound), out.data_ptr(),
             state_out.data_ptr(), handle), "kda_recurrence_step")
+    written(*given)
     return out, state_out

@@ -209,3 +209,73 @@ def test_recording_a_call_is_refused(way):
             watched = f(t)
         with torch.no_grad():
             assert torch.equal(watched, f(t))
+
+
+def test_results_in_place_are_seen_by_autograd(way):
+    """A tensor that a graph has saved and a call then writes to: the graph's backward pass says so."""
+    def saved(t):
+        leaf = torch.ones_like(t, requires_grad=True)
+        return (leaf * t).sum()
+
+    d = make("TND", [30, 9], 2, 64, FP, seed=7)
+    if way == "python":
+        d["plan"]._handle = None
+    a = args(d, -1.0, "TND")
+    qk = qk_inputs()
+    empty = {n: torch.empty_like(d[n]) for n in ("x", "h0")}
+    one = torch.empty_like(d["x"][:2])
+    dense = lambda n: qk[n].clone()  # noqa: E731
+    grads = {"dq": dense("q"), "dk": dense("k")}
+    turned = {"q_out": dense("q"), "k_out": dense("k")}
+    cases = [
+        (d["h0"], lambda: single(d, state_out=d["h0"])),
+        (empty["h0"], lambda: single(d, state_out=empty["h0"])),
+        (one, lambda: single(d, out=one)),
+        (d["h0"], lambda: kda.gated_recurrence(*a, final_state=d["h0"])),
+        (empty["x"], lambda: kda.gated_recurrence(*a, out=empty["x"])),
+        (qk["q"], lambda: kda.qk_norm_rope(**qk, q_out=qk["q"])),
+        (turned["k_out"], lambda: kda.qk_norm_rope(**qk, **turned)),
+        (grads["dq"], lambda: kda.qk_norm_rope_backward(grads["dq"], grads["dk"], **qk, **grads)),
+        (grads["dk"], lambda: kda.qk_norm_rope_backward(grads["dq"], grads["dk"], **qk, **grads))]
+    for i, (t, call) in enumerate(cases):
+        loss = saved(t)
+        with torch.no_grad():
+            call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+        # a call that is refused changes nothing, and a view tells its base
+        before = t._version
+        base = torch.zeros(2, *t.shape, device="cuda", dtype=t.dtype)
+        with pytest.raises((kda.KdaError, ValueError)):
+            single(d, lb=-7.0, state_out=d["h0"])
+        assert t._version == before, i
+        base[0].copy_(t)
+        loss = saved(base)
+        with torch.no_grad():
+            single(d, state_out=base.flatten()[:d["h0"].numel()].view_as(d["h0"]))
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    with torch.inference_mode():
+        state = d["h0"].clone()
+    single(d, state_out=state)  # no counter to move
+
+
+def test_results_that_want_a_gradient_are_refused(way):
+    d = make("TND", [30, 9], 2, 64, FP, seed=8)
+    if way == "python":
+        d["plan"]._handle = None
+    a = args(d, -1.0, "TND")
+    qk = qk_inputs()
+    leaf = lambda t: torch.empty_like(t).requires_grad_()  # noqa: E731
+    calls = [lambda: single(d, out=leaf(d["x"][:2])), lambda: single(d, state_out=leaf(d["h0"])),
+             lambda: kda.gated_recurrence(*a, out=leaf(d["x"])),
+             lambda: kda.gated_recurrence(*a, final_state=leaf(d["h0"])),
+             lambda: kda.qk_norm_rope(**qk, q_out=leaf(qk["q"])),
+             lambda: kda.qk_norm_rope(**qk, k_out=leaf(qk["k"])),
+             lambda: kda.qk_norm_rope_backward(qk["q"], qk["k"], **qk, dq=leaf(qk["q"])),
+             lambda: kda.qk_norm_rope_backward(qk["q"], qk["k"], **qk, dk=leaf(qk["k"]))]
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()
+        with torch.no_grad():
+            call()
