@@ -20,7 +20,7 @@ their gradients would be accumulated on that graph's stream (``torch.autograd.gr
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass
+from dataclasses import dataclass, fields
 
 import numpy as np
 import torch
@@ -63,6 +63,14 @@ class KdaRecurrencePlan:
             sh.layout, sh.B, sh.N, sh.S, sh.D, self.host.ctypes.data, self.host.size, self.host,
             self.dev, self.workspace_bytes, self.backward_workspace_bytes, self.states_shape[0])
         self._shapes = {}
+
+    # copies and pickles hold the fields; the addresses and the compiled calls' handle are made anew
+    def __getstate__(self):
+        return {f.name: getattr(self, f.name) for f in fields(self)}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        self.__post_init__()
 
     def _shape_for(self, dtype: int) -> KdaRecurrenceShape:
         """The shape with a call's element type (the schedule does not depend on it)."""

@@ -279,3 +279,18 @@ def test_results_that_want_a_gradient_are_refused(way):
             call()
         with torch.no_grad():
             call()
+
+
+def test_copies_of_a_plan(cuda_ok):
+    """A plan that went through copy and pickle, as a module that keeps one does."""
+    import copy
+    import pickle
+    d = make("TND", [700, 31], 2, 64, BF, seed=9)
+    want = both(d)
+    for again in (copy.copy, copy.deepcopy, lambda p: pickle.loads(pickle.dumps(p))):
+        plan = again(d["plan"])
+        assert plan._handle is not None
+        got = both(dict(d, plan=plan))
+        assert all(torch.equal(got[n], want[n]) for n in want)
+        del plan
+    assert all(torch.equal(p, want[n]) for n, p in both(d).items())

@@ -1,7 +1,14 @@
 """What the binding of the operators around the prefill sees of a call, without a GPU."""
+import copy
+import ctypes
+import pickle
+
+import numpy as np
+import pytest
 import torch
 from torch.autograd import forward_ad
 
+import chunked_kda_prefill_b200 as kda
 from chunked_kda_prefill_b200 import _views
 
 
@@ -16,3 +23,20 @@ def test_tangents_count_as_wanted_gradients():
                 assert not _views.has_tangent(t, leaf, None)
     with torch.no_grad():
         assert not _views.needs_grad(leaf, t)
+
+
+@pytest.mark.parametrize("again", [copy.copy, copy.deepcopy, lambda p: pickle.loads(pickle.dumps(p))])
+def test_plans_are_copied_and_pickled(again):
+    plan = kda.recurrence_plan(torch.zeros(9, 2, 64), "TND", cu_seqlens=[0, 4, 9])
+    twin = again(plan)
+    assert twin.layout == "TND" and twin.tiles == plan.tiles and twin._shape_for(1).dtype == 1
+    assert np.array_equal(twin.host, plan.host) and torch.equal(twin.dev, plan.dev)
+    assert (twin.workspace_bytes, twin.backward_workspace_bytes, twin.states_shape) == (
+        plan.workspace_bytes, plan.backward_workspace_bytes, plan.states_shape)
+    assert (twin._handle is None) == (plan._handle is None)
+    # its address is that of its own words
+    assert ctypes_address(twin._host_ptr) == twin.host.ctypes.data
+
+
+def ctypes_address(p):
+    return ctypes.cast(p, ctypes.c_void_p).value
