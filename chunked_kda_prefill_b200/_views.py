@@ -56,6 +56,12 @@ def viewable(t: torch.Tensor) -> bool:
             and all(n == 1 or s * size % 16 == 0 for n, s in zip(t.shape[:-1], t.stride()[:-1])))
 
 
+def readable(t: torch.Tensor) -> torch.Tensor:
+    """A gradient as view() and the alignment rule take it: itself, or a dense copy (contiguous() would
+    keep a dense slice that starts at an odd address)."""
+    return t if viewable(t) else t.clone(memory_format=torch.contiguous_format)
+
+
 @contextlib.contextmanager
 def _on(device, stream):
     with torch.cuda.device(device), torch.cuda.stream(stream):

@@ -19,7 +19,7 @@ import torch
 from . import _lib
 from ._lib import KdaError, KdaQkShape, check
 from ._views import (dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, no_tangents,
-                     not_recorded, results, used_on, view, viewable, written)
+                     not_recorded, readable, results, used_on, view, written)
 from .api import LAYOUTS, _ptr
 
 
@@ -155,7 +155,7 @@ class _QkNormRope(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dq_out, dk_out):
-        dq_out, dk_out = (t if viewable(t) else t.contiguous() for t in (dq_out, dk_out))
+        dq_out, dk_out = readable(dq_out), readable(dk_out)
         q, k, positions, inv_freq, q_weight, k_weight = ctx.saved_tensors
         dq, dk, dqw, dkw = qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq,
                                                  q_weight, k_weight, *ctx.call)

@@ -28,7 +28,7 @@ import torch
 from . import _lib
 from ._lib import KdaError, KdaRecurrenceShape, check
 from ._views import (DTYPES, dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, no_tangents,
-                     not_recorded, results, used_on, view, viewable, written)
+                     not_recorded, readable, results, used_on, view, written)
 from .api import LAYOUTS, _ptr
 
 _F32 = torch.float32
@@ -282,10 +282,10 @@ class _GatedRecurrence(torch.autograd.Function):
         if dout is None and dfinal_state is None:
             return (None,) * 9
         x, g, beta, initial_state, A_log, dt_bias, states = ctx.saved_tensors
-        if dout is not None and not viewable(dout):
-            dout = dout.contiguous()
+        if dout is not None:
+            dout = readable(dout)
         if dfinal_state is not None:
-            dfinal_state = dfinal_state.contiguous()
+            dfinal_state = readable(dfinal_state.contiguous())
         grads = gated_recurrence_backward(dout, dfinal_state, x, g, beta, initial_state, A_log,
                                           dt_bias, *ctx.call, states)
         return grads + (None,) * 3

@@ -294,3 +294,37 @@ def test_copies_of_a_plan(cuda_ok):
         assert all(torch.equal(got[n], want[n]) for n in want)
         del plan
     assert all(torch.equal(p, want[n]) for n, p in both(d).items())
+
+
+def after_an_odd_number(t):
+    """t behind three values of another tensor: its gradient is a dense slice that starts 12 (fp32) or
+    6 (bf16) bytes off any alignment."""
+    return torch.cat([torch.zeros(3, dtype=t.dtype, device=t.device), t.flatten()])
+
+
+@pytest.mark.parametrize("kind", [BF, FP])
+def test_gradients_at_odd_addresses(kind, cuda_ok):
+    d = make("TND", [70, 33], 2, 64, kind, seed=10)
+    gen = torch.Generator().manual_seed(3)
+    leaves = lambda: [d[n].clone().requires_grad_() for n in  # noqa: E731
+                      ("x", "g", "beta", "h0", "A_log", "dt_bias")]
+
+    def grads(ts, results, ups, spread):
+        pieces = [spread(t) for t in results]
+        ups = [spread(u) for u in ups]
+        return torch.autograd.grad(pieces, ts, ups)
+
+    ups = [torch.randn(d["x"].shape, generator=gen).cuda().to(kind), d["dfinal"]]
+    got = []
+    for spread in (after_an_odd_number, lambda t: t):
+        ts = leaves()
+        got.append(grads(ts, kda.gated_recurrence(*ts, -1.0, "TND", d["plan"]), ups, spread))
+    assert all(torch.equal(p, q) for p, q in zip(*got))
+    qk = qk_inputs(kind)
+    names = ("q", "k", "q_weight", "k_weight")
+    ups = [torch.randn(qk[n].shape, generator=gen).cuda().to(kind) for n in ("q", "k")]
+    got = []
+    for spread in (after_an_odd_number, lambda t: t):
+        ts = {n: qk[n].clone().requires_grad_() for n in names}
+        got.append(grads(list(ts.values()), kda.qk_norm_rope(**dict(qk, **ts)), ups, spread))
+    assert all(torch.equal(p, q) for p, q in zip(*got))

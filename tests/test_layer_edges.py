@@ -40,3 +40,15 @@ def test_plans_are_copied_and_pickled(again):
 
 def ctypes_address(p):
     return ctypes.cast(p, ctypes.c_void_p).value
+
+
+def test_gradients_are_taken_from_any_address():
+    whole = torch.arange(3 + 4 * 2 * 64.)
+    odd = whole[3:].view(4, 2, 64)
+    assert odd.is_contiguous() and odd.data_ptr() % 16 and not _views.viewable(odd)
+    even = _views.readable(odd)
+    assert _views.viewable(even) and even.is_contiguous() and torch.equal(even, odd)
+    for kept in (even, even[:, :1], even[::2]):
+        assert _views.readable(kept) is kept
+    for copied in (torch.ones(()).expand(4, 2, 64), odd.transpose(1, 2)):
+        assert _views.readable(copied).is_contiguous() and torch.equal(_views.readable(copied), copied)
