@@ -29,6 +29,8 @@ def expect(t, name: str, dtype, device, shape) -> None:
         raise ValueError(f"{name} must be on {device}")
     if t.shape != shape:
         raise KdaError(3, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.is_neg():
+        raise ValueError(f"{name} is marked as negated but not rewritten: pass {name}.resolve_neg()")
 
 
 def expect_dense(t, name: str, dtype, device, shape) -> None:
@@ -58,7 +60,8 @@ def viewable(t: torch.Tensor) -> bool:
 
 def readable(t: torch.Tensor) -> torch.Tensor:
     """A gradient as view() and the alignment rule take it: itself, or a dense copy (contiguous() would
-    keep a dense slice that starts at an odd address)."""
+    keep a dense slice that starts at an odd address).  A lazy negation is carried out."""
+    t = t.resolve_neg()
     return t if viewable(t) else t.clone(memory_format=torch.contiguous_format)
 
 

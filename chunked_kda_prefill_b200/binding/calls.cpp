@@ -58,12 +58,12 @@ void drop_plan(PyObject* capsule) {
 }
 
 // A plain CUDA tensor on device `dev`; null for anything else (a tensor that is another class's view
-// of its own kind included).
+// of its own kind, and one that is negated by a mark alone, included).
 const Tensor* plain(PyObject* o, int dev) {
   if (!THPVariable_Check(o)) return nullptr;
   const Tensor& t = THPVariable_Unpack(o);
   if (!t.defined() || !t.is_cuda() || t.get_device() != dev || t.layout() != at::kStrided ||
-      t.unsafeGetTensorImpl()->is_python_dispatch())
+      t.unsafeGetTensorImpl()->is_python_dispatch() || t.is_neg())
     return nullptr;
   return &t;
 }

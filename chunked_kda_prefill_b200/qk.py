@@ -47,6 +47,7 @@ def _check(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleav
         k_shape, tokens = (B, Nk, S, D), (B, S)
     if B >= _LIMIT or S >= _LIMIT or Nq >= _LIMIT or Nk >= _LIMIT or D >= _LIMIT:
         raise KdaError(3, "a size of q or k does not fit 32 bits")
+    expect(q, "q", q.dtype, dev, q.shape)
     expect(k, "k", q.dtype, dev, k_shape)
     if positions is not None:
         expect_dense(positions, "positions", torch.int32, dev, tokens)

@@ -151,9 +151,11 @@ def _check(plan, layout, dev, x, g, beta, initial_state, A_log, dt_bias):
             and x.shape == g.shape == shape and beta.shape == plan._rows
             and A_log.shape == plan._heads and dt_bias.shape == plan._params
             and A_log.is_contiguous() and dt_bias.is_contiguous()
+            and not (x.is_neg() or g.is_neg() or beta.is_neg() or A_log.is_neg() or dt_bias.is_neg())
             and (initial_state is None
                  or (initial_state.get_device() == index and initial_state.dtype is _F32
-                     and initial_state.shape == plan._state and initial_state.is_contiguous()))):
+                     and initial_state.shape == plan._state and initial_state.is_contiguous()
+                     and not initial_state.is_neg()))):
         return code
     if dev.type != "cuda":
         raise ValueError("the gated recurrence runs on a CUDA device only")
@@ -359,7 +361,8 @@ def gated_recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound: float,
             and g.dtype is kind and beta.dtype is kind and A_log.dtype is dt_bias.dtype is _F32
             and g.shape == shape and beta.shape == (B, N) and A_log.shape == (N,)
             and dt_bias.shape == (N, D) and x.is_contiguous() and g.is_contiguous()
-            and beta.is_contiguous() and A_log.is_contiguous() and dt_bias.is_contiguous()):
+            and beta.is_contiguous() and A_log.is_contiguous() and dt_bias.is_contiguous()
+            and not (x.is_neg() or g.is_neg() or beta.is_neg() or A_log.is_neg() or dt_bias.is_neg())):
         expect_dense(x, "x", kind, dev, shape)
         expect_dense(g, "g", kind, dev, shape)
         expect_dense(beta, "beta", kind, dev, shape[:2])

@@ -328,3 +328,52 @@ def test_gradients_at_odd_addresses(kind, cuda_ok):
         ts = {n: qk[n].clone().requires_grad_() for n in names}
         got.append(grads(list(ts.values()), kda.qk_norm_rope(**dict(qk, **ts)), ups, spread))
     assert all(torch.equal(p, q) for p, q in zip(*got))
+
+
+def test_lazily_negated_tensors(way):
+    """Values that torch has marked as negated but not rewritten are refused, and as gradients taken
+    for what they stand for."""
+    d = make("TND", [30, 9], 2, 64, FP, seed=11)
+    if way == "python":
+        d["plan"]._handle = None
+    a = args(d, -1.0, "TND")
+    names = ("x", "g", "beta", "h0", "A_log", "dt_bias")
+    for i, name in enumerate(names):
+        mine = list(a)
+        mine[i] = torch._neg_view(a[i])
+        assert mine[i].is_neg() and mine[i].is_contiguous()
+        with pytest.raises(ValueError, match="negat"):
+            kda.gated_recurrence(*mine)
+        with pytest.raises(ValueError, match="negat"):
+            kda.gated_recurrence(*mine[:6], *a[6:], final_state=torch.empty_like(d["h0"]))
+    one = [d[n][:2].contiguous() for n in names[:3]] + [d[n] for n in names[3:]]
+    for i in range(6):
+        mine = one[:i] + [torch._neg_view(one[i])] + one[i + 1:]
+        with pytest.raises(ValueError, match="negat"):
+            kda.gated_recurrence_step(*mine, -1.0)
+    for kw in ({"out": torch._neg_view(torch.empty_like(one[0]))},
+               {"state_out": torch._neg_view(torch.empty_like(one[3]))}):
+        with pytest.raises(ValueError, match="negat"):
+            kda.gated_recurrence_step(*one, -1.0, **kw)
+    states = kda.gated_recurrence(*a, return_states=True)[2]
+    for g in ((torch._neg_view(d["dout"]), None), (None, torch._neg_view(d["dfinal"]))):
+        with pytest.raises(ValueError, match="negat"):
+            kda.gated_recurrence_backward(*g, *a, states)
+    qk = qk_inputs()
+    for name in ("q", "k", "inv_freq", "q_weight", "k_weight"):
+        c = dict(qk, **{name: torch._neg_view(qk[name])})
+        with pytest.raises(ValueError, match="negat"):
+            kda.qk_norm_rope(**c)
+        with pytest.raises(ValueError, match="negat"):
+            kda.qk_norm_rope_backward(qk["q"], qk["k"], **c)
+    # a gradient that arrives like this
+    ts = [d[n].clone().requires_grad_() for n in ("x", "g", "beta", "h0", "A_log", "dt_bias")]
+    out, final = kda.gated_recurrence(*ts, -1.0, "TND", d["plan"])
+    got = torch.autograd.grad([out, final], ts, [torch._neg_view(d["dout"]), torch._neg_view(d["dfinal"])])
+    want = kda.gated_recurrence_backward(-d["dout"], -d["dfinal"], *a, states)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    q, k = (qk[n].clone().requires_grad_() for n in ("q", "k"))
+    both_out = kda.qk_norm_rope(**dict(qk, q=q, k=k))
+    got = torch.autograd.grad(both_out, [q, k], [torch._neg_view(qk["q"]), torch._neg_view(qk["k"])])
+    want = kda.qk_norm_rope_backward(-qk["q"], -qk["k"], **qk)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))

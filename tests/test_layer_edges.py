@@ -52,3 +52,15 @@ def test_gradients_are_taken_from_any_address():
         assert _views.readable(kept) is kept
     for copied in (torch.ones(()).expand(4, 2, 64), odd.transpose(1, 2)):
         assert _views.readable(copied).is_contiguous() and torch.equal(_views.readable(copied), copied)
+
+
+def test_marked_negations_are_not_read_as_they_lie():
+    t = torch.arange(1, 9 * 64 + 1.).view(9, 64)
+    minus = torch._neg_view(t)
+    assert minus.is_neg() and minus.data_ptr() == t.data_ptr() and minus.is_contiguous()
+    _views.expect(t, "t", t.dtype, t.device, t.shape)
+    for check in (_views.expect, _views.expect_dense):
+        with pytest.raises(ValueError, match="negat"):
+            check(minus, "t", t.dtype, t.device, t.shape)
+    got = _views.readable(minus)
+    assert not got.is_neg() and torch.equal(got, -t)
