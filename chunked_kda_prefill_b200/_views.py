@@ -31,6 +31,8 @@ def expect(t, name: str, dtype, device, shape) -> None:
         raise KdaError(3, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.is_neg():
         raise ValueError(f"{name} is marked as negated but not rewritten: pass {name}.resolve_neg()")
+    if not t.data_ptr() and t.numel():  # NULL would mean that it was left out
+        raise ValueError(f"{name} has no memory of its own")
 
 
 def expect_dense(t, name: str, dtype, device, shape) -> None:

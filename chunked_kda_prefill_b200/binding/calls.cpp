@@ -58,12 +58,13 @@ void drop_plan(PyObject* capsule) {
 }
 
 // A plain CUDA tensor on device `dev`; null for anything else (a tensor that is another class's view
-// of its own kind, and one that is negated by a mark alone, included).
+// of its own kind, has no memory, or is negated by a mark alone, included).
 const Tensor* plain(PyObject* o, int dev) {
   if (!THPVariable_Check(o)) return nullptr;
   const Tensor& t = THPVariable_Unpack(o);
   if (!t.defined() || !t.is_cuda() || t.get_device() != dev || t.layout() != at::kStrided ||
-      t.unsafeGetTensorImpl()->is_python_dispatch() || t.is_neg())
+      t.unsafeGetTensorImpl()->is_python_dispatch() || t.is_neg() || !t.has_storage() ||
+      !t.const_data_ptr())
     return nullptr;
   return &t;
 }
@@ -164,11 +165,17 @@ PyObject* tuple_of(std::initializer_list<const Tensor*> ts) {
   }
   return r;
 }
-#define CALL(expr)             \
-  kda_status_t status;         \
-  Py_BEGIN_ALLOW_THREADS       \
-  status = (expr);             \
-  Py_END_ALLOW_THREADS         \
+// Lets other threads of the interpreter run, until the end of its scope however that is left.
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+#define CALL(expr)        \
+  kda_status_t status;    \
+  {                       \
+    const Unlocked here;  \
+    status = (expr);      \
+  }                       \
   if (status != KDA_OK) return PyLong_FromLong(status)
 
 // bind(addresses of the entry points, in the order of `lib`)

@@ -155,7 +155,7 @@ def _check(plan, layout, dev, x, g, beta, initial_state, A_log, dt_bias):
             and (initial_state is None
                  or (initial_state.get_device() == index and initial_state.dtype is _F32
                      and initial_state.shape == plan._state and initial_state.is_contiguous()
-                     and not initial_state.is_neg()))):
+                     and initial_state.data_ptr() and not initial_state.is_neg()))):
         return code
     if dev.type != "cuda":
         raise ValueError("the gated recurrence runs on a CUDA device only")

@@ -377,3 +377,34 @@ def test_lazily_negated_tensors(way):
     got = torch.autograd.grad(both_out, [q, k], [torch._neg_view(qk["q"]), torch._neg_view(qk["k"])])
     want = kda.qk_norm_rope_backward(-qk["q"], -qk["k"], **qk)
     assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+def test_tensors_without_memory_of_their_own(way):
+    """Batched (vmap) and functional tensors have no address to pass on: every call says so, also where
+    the argument could be left out."""
+    d = make("TND", [30, 9], 2, 64, FP, seed=12)
+    if way == "python":
+        d["plan"]._handle = None
+    a = args(d, -1.0, "TND")
+    names = ("x", "g", "beta", "h0", "A_log", "dt_bias")
+    one = [d[n][:2].contiguous() for n in names[:3]] + [d[n] for n in names[3:]]
+    states = kda.gated_recurrence(*a, return_states=True)[2]
+    qk = qk_inputs()
+    qk["positions"] = torch.arange(40, dtype=torch.int32, device="cuda")
+    put = lambda ts, i, t: (*ts[:i], t, *ts[i + 1:])  # noqa: E731
+    cases = [(a[i], lambda t, i=i: kda.gated_recurrence(*put(a, i, t))[0]) for i in range(6)]
+    cases += [(a[i], lambda t, i=i: kda.gated_recurrence_backward(d["dout"], None, *put(a, i, t), states)[0])
+              for i in range(6)]
+    cases += [(one[i], lambda t, i=i: kda.gated_recurrence_step(*put(one, i, t), -1.0)[0]) for i in range(6)]
+    cases += [(t, lambda t, i=i: kda.gated_recurrence_backward(
+        *put((d["dout"], d["dfinal"]), i, t), *a, states)[0]) for i, t in ((0, d["dout"]), (1, d["dfinal"]))]
+    for name in ("q", "k", "positions", "inv_freq", "q_weight", "k_weight"):
+        cases += [(qk[name], lambda t, n=name: kda.qk_norm_rope(**dict(qk, **{n: t}))[0]),
+                  (qk[name], lambda t, n=name: kda.qk_norm_rope_backward(
+                      qk["q"], qk["k"], **dict(qk, **{n: t}))[0])]
+    for i, (t, call) in enumerate(cases):
+        with pytest.raises((RuntimeError, ValueError)):
+            torch.vmap(call)(torch.stack([t, t]))
+        with pytest.raises((RuntimeError, ValueError)):
+            torch.func.functionalize(call)(t)
+        assert call(t) is not None, i

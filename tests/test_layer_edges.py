@@ -64,3 +64,17 @@ def test_marked_negations_are_not_read_as_they_lie():
             check(minus, "t", t.dtype, t.device, t.shape)
     got = _views.readable(minus)
     assert not got.is_neg() and torch.equal(got, -t)
+
+
+def test_tensors_without_memory_have_no_address():
+    t = torch.zeros(3, 64)
+
+    def check(a):
+        with pytest.raises((RuntimeError, ValueError)):
+            _views.expect_dense(a, "a", t.dtype, a.device, a.shape)
+        return a * 1
+
+    torch.func.functionalize(check)(t)
+    torch.vmap(check)(t)
+    empty = torch.zeros(0, 64)
+    _views.expect_dense(empty, "empty", t.dtype, t.device, empty.shape)
