@@ -911,6 +911,8 @@ kda_status_t prepare(const kda_recurrence_shape_t* shape, const int32_t* plan_ho
   in[5] = dense_range(dt_bias, z.params);
   in[6] = dense_range(plan_dev, n_int32 * 4);
   in[7] = dense_range(workspace, workspace ? need : 0);
+  for (int i = 0; i < 7; ++i)  // it is written to
+    if (overlap(in[i], in[7])) return KDA_ERR_ALIAS;
   p->plan = plan_dev;
   p->checksum = plan_host[RH_CHECKSUM];
   p->N = shape->N;
@@ -1101,6 +1103,8 @@ extern "C" kda_status_t kda_recurrence_backward(
                             dense_range(ddt_bias, z.params)};
   const ByteRange grads[] = {r_dout, dense_range(dfinal_state, z.state)};
   if (any_overlap(in, outs) || any_overlap(grads, outs)) return KDA_ERR_ALIAS;
+  for (const ByteRange& r : {grads[0], grads[1], in[8]})
+    if (overlap(r, in[7])) return KDA_ERR_ALIAS;  // the workspace
   if ((st = check_device()) != KDA_OK) return st;
 
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

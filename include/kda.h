@@ -339,7 +339,7 @@ KDA_API kda_status_t kda_recurrence_states_size(const int32_t* plan_host, size_t
  *                    length are written as zeros, and the inputs' rows there are never read.
  *   final_state    : fp32 [B, N, D], the unrounded state after each sequence's last token; may be
  *                    initial_state itself, must not overlap it otherwise.
- * Outputs must not overlap one another or an input (KDA_ERR_ALIAS). */
+ * Outputs and the workspace must not overlap one another or an input (KDA_ERR_ALIAS). */
 KDA_API kda_status_t kda_recurrence_forward(
     const kda_recurrence_shape_t* shape, const int32_t* plan_host, const int32_t* plan_dev,
     size_t n_int32, const kda_view_t* x, const kda_view_t* g, const kda_view_t* beta,

@@ -10,6 +10,8 @@ from torch.autograd import forward_ad
 
 import chunked_kda_prefill_b200 as kda
 from chunked_kda_prefill_b200 import _views
+from test_abi import gpu_visible
+from test_layer_abi import rec_call, rec_plan, rec_shape
 
 
 def test_tangents_count_as_wanted_gradients():
@@ -78,3 +80,21 @@ def test_tensors_without_memory_have_no_address():
     torch.vmap(check)(t)
     empty = torch.zeros(0, 64)
     _views.expect_dense(empty, "empty", t.dtype, t.device, empty.shape)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_a_workspace_over_an_input_is_refused(backward):
+    L, shape = kda.load(), rec_shape(B=1, S=9000, N=1)
+    st, p = rec_plan(L, shape)
+    assert st == 0 and p[12] > 0  # cut: the workspace holds maps, and the gradients' parts
+    ok = (11, 13)  # no device
+    names = {"x": 0x10000000, "g": 0x20000000, "beta": 0x30000000, "A": 0x50000000, "bias": 0x51000000,
+             "plan_dev": 0x52000000}
+    names |= ({"dout": 0x38000000, "states": 0x60000000, "dfinal": 0x41000000} if backward
+              else {"h0": 0x40000000})
+    for name, address in names.items():
+        assert rec_call(L, p, shape, backward, ws=address) == 9, name
+    if not gpu_visible():
+        assert rec_call(L, p, shape, backward) in ok
+        # behind the last byte
+        assert rec_call(L, p, shape, backward, ws=0x50000100) in ok
