@@ -88,6 +88,11 @@ def build_calls(force: bool = False) -> str:
             f'-DKDA_TORCH_VERSION="{torch.__version__}"', "-I", sysconfig.get_paths()["include"]]
            + ["-I", include, "-I", os.path.join(include, "torch", "csrc", "api", "include"), "-I",
               cuda, src, "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-o", tmp])
+    # from here on an older file does not fit the header or the torch that are here: without it the
+    # calls go through ctypes
+    for f in (CALLS, stamp):
+        if os.path.exists(f):
+            os.remove(f)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")

@@ -9,7 +9,7 @@ import torch
 from torch.autograd import forward_ad
 
 import chunked_kda_prefill_b200 as kda
-from chunked_kda_prefill_b200 import _views
+from chunked_kda_prefill_b200 import _views, build
 from test_abi import gpu_visible
 from test_layer_abi import rec_call, rec_plan, rec_shape
 
@@ -98,3 +98,20 @@ def test_a_workspace_over_an_input_is_refused(backward):
         assert rec_call(L, p, shape, backward) in ok
         # behind the last byte
         assert rec_call(L, p, shape, backward, ws=0x50000100) in ok
+
+
+def test_compiled_calls_that_no_longer_fit_are_removed(tmp_path, monkeypatch):
+    """Without a compiler that works, the file of an earlier build does not stay beside a newer library."""
+    calls = tmp_path / "_calls.so"
+    calls.write_bytes(b"of an earlier header")
+    monkeypatch.setattr(build, "CALLS", str(calls))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setenv("CXX", "false")
+    with pytest.raises(RuntimeError):
+        build.build_calls()
+    assert not calls.exists()
+    monkeypatch.setenv("CXX", str(tmp_path / "no-such-compiler"))
+    calls.write_bytes(b"of an earlier header")
+    with pytest.raises(OSError):
+        build.build_calls()
+    assert not calls.exists()
