@@ -14,11 +14,29 @@ from ._lib import KdaError, KdaView
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
+_included = torch._C._dispatch_tls_is_dispatch_key_included
+_PRE_DISPATCH = torch._C.DispatchKey.PreDispatch
+
+
 def dtype_code(t: torch.Tensor, name: str) -> int:
     code = DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be bf16, fp16 or fp32, got {t.dtype}")
     return code
+
+
+def negated(name: str) -> None:
+    raise ValueError(f"{name} is marked as negated but not rewritten: pass {name}.resolve_neg()")
+
+
+def address(t: torch.Tensor | None) -> int | None:
+    """Of an argument that may be left out (None)."""
+    if t is None:
+        return None
+    p = t.data_ptr()
+    if not p and t.numel():  # a null address would mean that it was left out
+        raise ValueError("an argument has no memory of its own")
+    return p
 
 
 def expect(t, name: str, dtype, device, shape) -> None:
@@ -30,9 +48,7 @@ def expect(t, name: str, dtype, device, shape) -> None:
     if t.shape != shape:
         raise KdaError(3, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.is_neg():
-        raise ValueError(f"{name} is marked as negated but not rewritten: pass {name}.resolve_neg()")
-    if not t.data_ptr() and t.numel():  # NULL would mean that it was left out
-        raise ValueError(f"{name} has no memory of its own")
+        negated(name)
 
 
 def expect_dense(t, name: str, dtype, device, shape) -> None:
@@ -47,10 +63,10 @@ def view(t: torch.Tensor, name: str, layout: str, channels: bool = True) -> KdaV
     if channels and st[-1] != 1:
         raise ValueError(f"{name}'s channels must be contiguous")
     if layout == "BNSD":
-        return KdaView(t.data_ptr(), st[0], st[1], st[2])
+        return KdaView(address(t), st[0], st[1], st[2])
     if layout == "BSND":
-        return KdaView(t.data_ptr(), st[0], st[2], st[1])
-    return KdaView(t.data_ptr(), 0, st[1], st[0])
+        return KdaView(address(t), st[0], st[2], st[1])
+    return KdaView(address(t), 0, st[1], st[0])
 
 
 def viewable(t: torch.Tensor) -> bool:
@@ -99,19 +115,27 @@ def used_on(stream, *tensors) -> None:
 
 def has_tangent(*tensors) -> bool:
     """Whether one carries a forward-mode derivative (which requires_grad does not say)."""
+    if getattr(forward_ad, "_current_level", 0) < 0:  # none can: asking each costs half a microsecond
+        return False
     return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def needs_grad(*tensors) -> bool:
-    return has_tangent(*tensors) or (torch.is_grad_enabled()
-                                     and any(t is not None and t.requires_grad for t in tensors))
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            if torch.is_grad_enabled():
+                return True
+            break
+    return has_tangent(*tensors)
 
 
 def results(*tensors) -> None:
     """Checks the results that a caller supplies: a call writes to their memory, which autograd does not
     follow."""
-    if needs_grad(*tensors):
-        raise ValueError("results that require a gradient cannot be written to; use torch.no_grad()")
+    for t in tensors:
+        if t is not None and needs_grad(t):
+            raise ValueError("results that require a gradient cannot be written to; use "
+                             "torch.no_grad()")
 
 
 def written(*tensors) -> None:
@@ -124,8 +148,14 @@ def written(*tensors) -> None:
 def not_recorded(what: str) -> None:
     """Refuses a call while torch.jit.trace or make_fx records: they see no operation of torch here and
     would keep the results as constants."""
-    proxies = sys.modules.get("torch.fx.experimental.proxy_tensor")  # not loaded: nobody uses make_fx
-    if torch.jit.is_tracing() or (proxies is not None and proxies.get_proxy_mode() is not None):
+    if torch.compiler.is_compiling():  # it takes none of these calls into its graphs
+        return
+    recorded = torch._C._is_tracing()
+    if not recorded and (torch._C._len_torch_dispatch_stack() > 0 or _included(_PRE_DISPATCH)):
+        # a mode is on; without this module it is not make_fx's
+        proxies = sys.modules.get("torch.fx.experimental.proxy_tensor")
+        recorded = proxies is not None and proxies.get_proxy_mode() is not None
+    if recorded:
         raise RuntimeError(f"{what} cannot be recorded by torch.jit.trace or make_fx: its results "
                            "would be constants of the recording")
 

@@ -5,7 +5,9 @@
 Per token and head, r = 1 / sqrt(mean(x^2) + eps) and n = x r weight; the pair i of the first
 2 * len(inv_freq) channels then turns by position * inv_freq[i].  The outputs are dense in the
 layout, as flash_kda and decode take them.  ``qk_norm_rope`` is differentiable with respect to q, k
-and the weights (once, in reverse mode: inputs with a forward-mode tangent are refused); ``qk_norm_rope_backward`` is its backward pass as a call of its own.
+and the weights (once, in reverse mode: inputs with a forward-mode tangent are refused);
+``qk_norm_rope_backward`` is its backward pass as a call of its own.  Neither can be recorded by
+torch.jit.trace or make_fx, nor batched by vmap.
 
 Single tokens (a decode batch) are the TND layout with one token per sequence: q [B, Nq, D],
 positions [B].
@@ -18,9 +20,9 @@ import torch
 
 from . import _lib
 from ._lib import KdaError, KdaQkShape, check
-from ._views import (dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, no_tangents,
-                     not_recorded, readable, results, used_on, view, written)
-from .api import LAYOUTS, _ptr
+from ._views import (address, dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad,
+                     negated, no_tangents, not_recorded, readable, results, used_on, view, written)
+from .api import LAYOUTS
 
 
 _LIMIT = 1 << 31
@@ -47,7 +49,8 @@ def _check(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interleav
         k_shape, tokens = (B, Nk, S, D), (B, S)
     if B >= _LIMIT or S >= _LIMIT or Nq >= _LIMIT or Nk >= _LIMIT or D >= _LIMIT:
         raise KdaError(3, "a size of q or k does not fit 32 bits")
-    expect(q, "q", q.dtype, dev, q.shape)
+    if q.is_neg():
+        negated("q")
     expect(k, "k", q.dtype, dev, k_shape)
     if positions is not None:
         expect_dense(positions, "positions", torch.int32, dev, tokens)
@@ -84,8 +87,8 @@ def _forward(q, k, positions, inv_freq, q_weight, k_weight, eps, layout, interle
             k_out = dense_like(k)
         check(_lib.load().kda_qk_norm_rope(
             ctypes.byref(shape), ctypes.byref(view(q, "q", layout)),
-            ctypes.byref(view(k, "k", layout)), _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
-            _ptr(k_weight), q_out.data_ptr(), k_out.data_ptr(), handle), "kda_qk_norm_rope")
+            ctypes.byref(view(k, "k", layout)), address(positions), address(inv_freq), address(q_weight),
+            address(k_weight), q_out.data_ptr(), k_out.data_ptr(), handle), "kda_qk_norm_rope")
     written(*given)
     return q_out, k_out
 
@@ -138,9 +141,9 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k
         check(L.kda_qk_norm_rope_backward(
             ctypes.byref(shape), ctypes.byref(view(dq_out, "dq_out", layout)),
             ctypes.byref(view(dk_out, "dk_out", layout)), ctypes.byref(view(q, "q", layout)),
-            ctypes.byref(view(k, "k", layout)), _ptr(positions), _ptr(inv_freq), _ptr(q_weight),
-            _ptr(k_weight), ws.data_ptr(), ws_bytes, dq.data_ptr(), dk.data_ptr(),
-            _ptr(dqw), _ptr(dkw), handle), "kda_qk_norm_rope_backward")
+            ctypes.byref(view(k, "k", layout)), address(positions), address(inv_freq), address(q_weight),
+            address(k_weight), ws.data_ptr(), ws_bytes, dq.data_ptr(), dk.data_ptr(),
+            address(dqw), address(dkw), handle), "kda_qk_norm_rope_backward")
     written(*given)
     return dq, dk, dqw, dkw
 

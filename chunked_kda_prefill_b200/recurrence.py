@@ -10,8 +10,10 @@ Per sequence, head n and channel d, with flash_kda's activations of the gate and
     h_t = a_t h_{t-1} + sigmoid(beta_t[n]) x_t,        out_t = h_t
 
 ``gated_recurrence`` is differentiable with respect to x, g, beta, initial_state, A_log and
-dt_bias (once, in reverse mode: inputs with a forward-mode tangent are refused).  ``gated_recurrence_backward`` is its backward pass as a call of its own, and
+dt_bias (once, in reverse mode: inputs with a forward-mode tangent are refused).
+``gated_recurrence_backward`` is its backward pass as a call of its own, and
 ``gated_recurrence_step`` one token for each sequence, from the state that a prefill returned.
+None of them can be recorded by torch.jit.trace or make_fx, nor batched by vmap.
 
 Every call can be captured in a CUDA graph; the plan is made before.  When a training step is
 captured, torch's rule holds: no eager autograd graph of the same leaves may be alive then, since
@@ -27,9 +29,9 @@ import torch
 
 from . import _lib
 from ._lib import KdaError, KdaRecurrenceShape, check
-from ._views import (DTYPES, dense_like, dtype_code, expect, expect_dense, launch_on, needs_grad, no_tangents,
-                     not_recorded, readable, results, used_on, view, written)
-from .api import LAYOUTS, _ptr
+from ._views import (DTYPES, address, dense_like, dtype_code, expect, expect_dense, launch_on,
+                     needs_grad, no_tangents, not_recorded, readable, results, used_on, view, written)
+from .api import LAYOUTS
 
 _F32 = torch.float32
 _STATUS_BYTES = 256  # a workspace that holds the device status alone
@@ -155,7 +157,7 @@ def _check(plan, layout, dev, x, g, beta, initial_state, A_log, dt_bias):
             and (initial_state is None
                  or (initial_state.get_device() == index and initial_state.dtype is _F32
                      and initial_state.shape == plan._state and initial_state.is_contiguous()
-                     and initial_state.data_ptr() and not initial_state.is_neg()))):
+                     and not initial_state.is_neg()))):
         return code
     if dev.type != "cuda":
         raise ValueError("the gated recurrence runs on a CUDA device only")
@@ -213,8 +215,8 @@ def _forward(x, g, beta, initial_state, A_log, dt_bias, lower_bound, layout, pla
         check(_lib.load().kda_recurrence_forward(
             ctypes.byref(plan._shape_for(code)), plan._host_ptr, plan.dev.data_ptr(),
             plan.host.size, ctypes.byref(view(x, "x", layout)), ctypes.byref(view(g, "g", layout)),
-            ctypes.byref(view(beta, "beta", layout, channels=False)), _ptr(initial_state),
-            A_log.data_ptr(), dt_bias.data_ptr(), float(lower_bound), _ptr(states), ws_ptr,
+            ctypes.byref(view(beta, "beta", layout, channels=False)), address(initial_state),
+            A_log.data_ptr(), dt_bias.data_ptr(), float(lower_bound), address(states), ws_ptr,
             ws_bytes, out.data_ptr(), final_state.data_ptr(), handle), "kda_recurrence_forward")
     written(*given)
     return out, final_state, states
@@ -258,11 +260,11 @@ def gated_recurrence_backward(dout, dfinal_state, x, g, beta, initial_state, A_l
             ctypes.byref(plan._shape_for(code)), plan._host_ptr, plan.dev.data_ptr(),
             plan.host.size,
             ctypes.byref(view(dout, "dout", layout)) if dout is not None else None,
-            _ptr(dfinal_state), ctypes.byref(view(x, "x", layout)),
+            address(dfinal_state), ctypes.byref(view(x, "x", layout)),
             ctypes.byref(view(g, "g", layout)),
             ctypes.byref(view(beta, "beta", layout, channels=False)), A_log.data_ptr(),
             dt_bias.data_ptr(), float(lower_bound), states.data_ptr(),
-            ws.data_ptr(), ws_bytes, dx.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), _ptr(dh0),
+            ws.data_ptr(), ws_bytes, dx.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), address(dh0),
             dA_log.data_ptr(), ddt_bias.data_ptr(), handle), "kda_recurrence_backward")
     return dx, dg, dbeta, dh0, dA_log, ddt_bias
 
@@ -386,7 +388,7 @@ def gated_recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound: float,
             state_out = (torch.empty_like(state) if state is not None else
                          torch.empty(shape, dtype=torch.float32, device=dev))
         check(_lib.load().kda_recurrence_step(
-            B, N, D, code, x.data_ptr(), g.data_ptr(), beta.data_ptr(), _ptr(state),
+            B, N, D, code, x.data_ptr(), g.data_ptr(), beta.data_ptr(), address(state),
             A_log.data_ptr(), dt_bias.data_ptr(), float(lower_bound), out.data_ptr(),
             state_out.data_ptr(), handle), "kda_recurrence_step")
     written(*given)

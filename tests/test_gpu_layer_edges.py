@@ -408,3 +408,23 @@ def test_tensors_without_memory_of_their_own(way):
         with pytest.raises((RuntimeError, ValueError)):
             torch.func.functionalize(call)(t)
         assert call(t) is not None, i
+
+
+def test_calls_in_a_compiled_function(way):
+    """torch.compile takes no call into its graphs, and runs it between them as it stands."""
+    d = make("TND", [30, 9], 2, 64, FP, seed=13)
+    if way == "python":
+        d["plan"]._handle = None
+    a, qk, out = args(d, -1.0, "TND"), qk_inputs(), torch.empty_like(d["x"])
+    rest = {n: v for n, v in qk.items() if n != "q"}
+    for f, t in ((lambda x: kda.gated_recurrence(x * 2, *a[1:])[0] * 3, d["x"]),
+                 (lambda x: kda.gated_recurrence(x * 2, *a[1:], out=out)[0] * 3, d["x"]),
+                 (lambda q: kda.qk_norm_rope(q=q * 2, **rest)[0] * 3, qk["q"])):
+        torch._dynamo.reset()
+        assert torch.equal(torch.compile(f, backend="eager")(t), f(t))
+    torch._dynamo.reset()
+    t, u = (d["x"].clone().requires_grad_() for _ in range(2))
+    f = lambda x: kda.gated_recurrence(x * 2, *a[1:])[0].sum()  # noqa: E731
+    torch.compile(f, backend="eager")(t).backward()
+    f(u).backward()
+    assert torch.equal(t.grad, u.grad)

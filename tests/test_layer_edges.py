@@ -73,13 +73,13 @@ def test_tensors_without_memory_have_no_address():
 
     def check(a):
         with pytest.raises((RuntimeError, ValueError)):
-            _views.expect_dense(a, "a", t.dtype, a.device, a.shape)
+            _views.address(a)
         return a * 1
 
     torch.func.functionalize(check)(t)
     torch.vmap(check)(t)
-    empty = torch.zeros(0, 64)
-    _views.expect_dense(empty, "empty", t.dtype, t.device, empty.shape)
+    assert _views.address(None) is None and _views.address(t) == t.data_ptr()
+    assert _views.address(torch.zeros(0)) == 0
 
 
 @pytest.mark.parametrize("backward", [False, True])
@@ -115,3 +115,28 @@ def test_compiled_calls_that_no_longer_fit_are_removed(tmp_path, monkeypatch):
     with pytest.raises(OSError):
         build.build_calls()
     assert not calls.exists()
+
+
+def test_recordings_are_told_from_other_modes():
+    from torch.fx.experimental.proxy_tensor import make_fx
+    from torch.utils._python_dispatch import TorchDispatchMode
+    t = torch.ones(3)
+
+    def call(x):
+        _views.not_recorded("call")
+        return x * 2
+
+    for pre_dispatch in (False, True):
+        for mode in ("real", "fake", "symbolic"):
+            with pytest.raises(RuntimeError, match="recorded"):
+                make_fx(call, pre_dispatch=pre_dispatch, tracing_mode=mode)(t)
+    with pytest.raises(RuntimeError, match="recorded"):
+        torch.jit.trace(call, (t,))
+
+    class Watch(TorchDispatchMode):
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            return func(*args, **(kwargs or {}))
+
+    with Watch():
+        assert torch.equal(call(t), 2 * t)
+    assert torch.equal(torch.compile(call, backend="eager")(t), 2 * t)
