@@ -12,8 +12,9 @@
 // rows of the next steps are on their way to shared memory meanwhile (without them in registers more
 // blocks fit a multiprocessor), and only the sums over a row cross lanes.
 // Both passes are bound by HBM: 4 bytes a value forward (16-bit), 6 backward.  Forward 4x32x16384
-// bf16, 64 heads a token, 343 us: 6.26 TB/s of the 6.47 that a copy reaches; backward of 65536 tokens
-// with 40 heads 333 us, 6.05 TB/s.
+// bf16, 64 heads a token, 344 us: 6.24 TB/s of the 6.47 that a copy reaches; backward of 65536 tokens
+// with 40 heads 324 us, 6.2 TB/s.  The weights' gradients are fp32 sums over a block's rows, fp64 from
+// there on.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -396,10 +396,13 @@ __device__ __forceinline__ void store_rows(T* to, long long next, int valid, con
   }
 }
 
-// 4x32x16384 bf16: 292 us, 5.5 TB/s of the 6.47 that a copy reaches (6.05 TB/s where 148 units keep
+// 4x32x16384 bf16: 295 us, 5.5 TB/s of the 6.47 that a copy reaches (6.2 TB/s where 148 units keep
 // every multiprocessor busy).  What else is busy: 65 % of the special-function unit, three results a
-// value.  Sharing one reciprocal between two values (289 us) is not worth its second path for
-// products that overflow; 12 warps take 305 us, a stage fewer 325 us.
+// value.  Sharing one reciprocal between two values (289 us against 292) is not worth its second path
+// for products that overflow; 12 warps took 305 us, a stage fewer 325 us.
+// The gate's powers and its reciprocal are the approximate instructions (off by 2^-22 and by one unit in
+// the last place; values below the normal range become zero): 16-bit results do not hold the rest, fp32
+// ones come out with 0.4 to 2 times the error of separate fp32 operations.
 template <class T, int D, bool SOLO>
 __global__ void __launch_bounds__(32 * Block<T, false>::kWarps, 1)
     rec_forward_kernel(const __grid_constant__ RecParams p) {
@@ -528,9 +531,11 @@ __device__ __forceinline__ float warp_sums(float (&v)[K], int lane) {
   return v[0];
 }
 
-// 4x32x16384 bf16: 490 us, 5.75 TB/s (6.4 TB/s where 148 units keep every multiprocessor busy).  From
-// inputs in L2 it takes 466 us: 35 instructions a value, 57 % of the issue slots.  13 or 14 warps spill
-// registers (840-910 us); 11 warps with a stage more take 520 us.
+// 4x32x16384 bf16: 480 us, 5.9 TB/s (6.45 TB/s where 148 units keep every multiprocessor busy).  35
+// instructions a value take 58 % of the issue slots.  13 or 14 warps spill registers (840-910 us); 11
+// warps with a stage more took 520 us.
+// The parameters' gradients are fp32 sums over a warp's tiles of a segment, fp64 from there on: fp64
+// sums over the tiles would take 8 registers more of the 168, which are all in use.
 template <class T, int D, bool SOLO>
 __global__ void __launch_bounds__(32 * Block<T, true>::kWarps, 1)
     rec_backward_kernel(const __grid_constant__ RecParams p) {
@@ -716,7 +721,7 @@ constexpr int kMapWarps = 16;
 // The maps of the segments of cut sequences, one block each: row 0 of a sequence is its start, row
 // k + 1 the map of the walk's k-th segment (the last one's is not needed).  A warp takes a
 // sixteenth of the tokens, a batch at a time with the next one's loads under way.
-// Bound by the special-function unit as the walk is: 2x16x4000 in 9 segments 18 us, of which the
+// Bound by the special-function unit as the walk is: 2x16x4000 in 9 segments 20 us, of which the
 // unit needs 11.
 template <class T, int D, bool BACKWARD>
 __global__ void __launch_bounds__(32 * kMapWarps, 1) rec_maps_kernel(const __grid_constant__ RecParams p) {
@@ -838,8 +843,8 @@ __global__ void __launch_bounds__(1024) rec_params_kernel(const __grid_constant_
   else if (d0 == 0) dA_log[n] = (float)sum;
 }
 
-// One token of every sequence, 4 channels a thread.  Bound by HBM, 14 bytes a value (16-bit), and by
-// the launch: 256 x 32 x 128 3.3 us (4.5 TB/s), one sequence 2.0 us.
+// One token of every sequence, 4 channels a thread.  Bound by the launch and by HBM, 14 bytes a value
+// (16-bit): one sequence 1.7 us, 256 x 32 x 128 3.9 us (3.8 TB/s; 3.3 us from L2).
 template <class T, int D>
 __global__ void __launch_bounds__(256) rec_step_kernel(const T* x, const T* g, const T* beta,
                                                        const float* h0, const float* A_log,

@@ -62,8 +62,11 @@ long long segments_of(long long tiles, long long most) {
 // Counted in tiles of a multiprocessor (about 0.16 us each), a pass takes as long, uncut, as its
 // longest sequence, one tile after another, or as all tiles over the multiprocessors.  Cut, a segment
 // costs 8 more for filling its ring, the maps 0.6 of all tiles and 25 for their launch, and the joins
-// 0.3 for each segment before (all measured).  Of the cuts into segments for one to eight rounds over
-// the multiprocessors the cheapest is taken.
+// 0.3 for each segment before.  Of the cuts into segments for one to eight rounds over the
+// multiprocessors the cheapest is taken.  The costs are those of bf16 sequences of equal length and
+// stand for both passes and all types; the maps of sequences that stay whole are counted though none
+// are formed, and uncut lengths are taken to fill all multiprocessors alike (a document of 16384
+// tokens with fifty of 700 and 32 heads gives the fullest one 2928 tiles, with 1394 on average).
 kda_status_t check_lengths(const kda_recurrence_shape_t& s, const int32_t* cu, Cut* cut) {
   const int R = rec_tile_rows(s.D);
   long long tiles = 0, longest = 0;
@@ -127,8 +130,11 @@ kda_status_t build(const kda_recurrence_shape_t& s, const int32_t* cu, int32_t* 
   });
   std::stable_sort(segs.begin(), segs.end(),
                    [](const Segment& a, const Segment& d) { return a.len > d.len; });
-  // Many short segments: a warp each, if the longest one is no more than a warp's share of all tiles.
-  // Else a ring would pass by the units of kRecRing warps for each of its tiles.
+  // Many short segments: a warp each, if the longest one is no more than a warp's share of all tiles
+  // (else warps would stand idle behind it).  Against a ring for each, 16 heads, bf16, 65536 tokens
+  // forward, in documents of an eighth of that border 156 us against 190, a quarter 159 (175), half
+  // 144 (166), 0.9 of it 196 (158), 1.1 of it 148 (157), twice 197 (149), four times 324 (147):
+  // near the border it is the number of units over all warps that decides, which the rule leaves out.
   long long all = 0;
   for (const Segment& q : segs) all += tiles_of(q.len, R);
   const bool solo = tiles_of(segs[0].len, R) * kRecSpread * kRecRing <= all * s.N;

@@ -180,7 +180,8 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight, k_weight, eps: float, layo
     may be q and k themselves where those are dense.
 
     Differentiable when q, k or a weight requires a gradient; then q_out, k_out and stream cannot
-    be given (choose the stream with torch.cuda.stream).  A call on a given stream does not wait for
+    be given (choose the stream with torch.cuda.stream).  Supplied results may not require a
+    gradient, and autograd notices that they are written.  A call on a given stream does not wait for
     the streams that made its inputs.
     """
     calls = _lib.calls()

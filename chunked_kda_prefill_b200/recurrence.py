@@ -310,6 +310,7 @@ def gated_recurrence(x, g, beta, initial_state, A_log, dt_bias, lower_bound: flo
     Differentiable when an input requires a gradient; then out, final_state, return_states,
     workspace and stream cannot be given (choose the stream with torch.cuda.stream).  A call on a
     given stream does not wait for the streams that made its inputs.
+    Supplied results may not require a gradient, and autograd notices that they are written.
     ``return_states=True`` adds the states that gated_recurrence_backward needs.  ``workspace``
     (plan.workspace_bytes) keeps the call's device status for device_status; by default every call
     has a scratch of its own.
@@ -339,7 +340,8 @@ def gated_recurrence_step(x, g, beta, state, A_log, dt_bias, lower_bound: float,
     """One token of the recurrence for each sequence.  Returns (out, state_out).
 
     x, g: [B, N, D] in bf16, fp16 or fp32, beta: [B, N], all dense; state: fp32 [B, N, D] or None
-    (zeros); pass ``state_out=state`` to update it in place.  Not differentiable.
+    (zeros); pass ``state_out=state`` to update it in place.  Not differentiable.  Supplied results
+    may not require a gradient, and autograd notices that they are written.
     """
     calls = _lib.calls()
     if stream is None and calls is not None:
